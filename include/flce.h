@@ -333,6 +333,138 @@ typedef struct {
 int flce_weighted_mse_chunk(void* user, int64_t row0, int64_t rows, int64_t vocab, void* logits, int64_t ld,
                             int32_t dtype, float* loss, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Preference and policy losses over per-token log-probabilities (as
+ * flce_logprobs_forward gives them), forward and backward.
+ *
+ * Token tensors hold S sequences in one of two layouts:
+ *  - padded (offsets NULL): S rows of `length` tokens, each tensor with its own
+ *    row stride (flce_token_view.ld, in elements, >= length; 0 = length);
+ *  - packed (offsets not NULL): one row of `length` tokens in all; sequence s is
+ *    tokens offsets[s] .. offsets[s+1]-1 (device int64, or int32 with
+ *    FLCE_OFFSETS_INT32; S+1 entries, not decreasing, within [0, length]).
+ *    Tokens outside every sequence count as masked; ld is not read.
+ * mask: device bytes, non-zero = the token counts; NULL data = every token
+ * does.  What a masked token's other tensors hold is never used (it may be NaN
+ * or infinite), and its gradient is 0.  Data pointers need the alignment of
+ * their element only; 16-byte aligned rows run faster.  Sums are formed in
+ * fp64 in a fixed order: results are bitwise reproducible.
+ * The gradient buffers are contiguous: S x length (padded) or length (packed).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  const void* data;
+  int64_t ld;                 /* padded layout: elements between rows; 0 = length        */
+} flce_token_view;
+
+typedef enum {
+  FLCE_OFFSETS_INT32 = 1,             /* offsets are int32                               */
+  FLCE_ADVANTAGE_PER_SEQUENCE = 2     /* advantages hold one value per sequence          */
+} flce_sequence_flags;
+
+typedef enum {
+  FLCE_PREFERENCE_SIGMOID = 0,   /* -(1-eps) log sigmoid(h) - eps log sigmoid(-h)        */
+  FLCE_PREFERENCE_HINGE = 1,     /* max(0, 1 - h)                                        */
+  FLCE_PREFERENCE_SQUARED = 2    /* (h / beta - 1 / (2 beta))^2                          */
+} flce_preference_type;
+
+/*
+ * Preference loss over P = n_seqs / 2 pairs: sequences 0 .. P-1 are the chosen
+ * answers, P .. 2P-1 the rejected ones, pair p = (p, P + p).  With kept tokens
+ *   R_s = sum_t (logp_t - ref_t)           (ref absent: sum_t logp_t),
+ *         divided by the number of kept tokens with length_normalize
+ *         (a sequence without any has R_s = 0),
+ *   h_p = beta (R_p - R_{P+p}) - margin,   loss_p by `type`.
+ */
+typedef struct {
+  int64_t n_seqs;             /* S = 2P, even, >= 0                                      */
+  int64_t length;             /* padded: tokens per row; packed: tokens in all           */
+  int32_t dtype;              /* flce_dtype of logps, ref_logps and grad_logps           */
+  int32_t reduction;          /* over pairs; mean of no pair gives NaN                   */
+  int32_t type;               /* flce_preference_type                                    */
+  int32_t flags;              /* FLCE_OFFSETS_INT32 or 0                                 */
+  int32_t length_normalize;   /* 0 or 1                                                  */
+  int32_t reserved;           /* must be 0                                               */
+  double beta;                /* > 0                                                     */
+  double label_smoothing;     /* eps in [0, 1], sigmoid only (else 0)                    */
+  double margin;
+} flce_preference_params;
+
+/* Bytes of device workspace flce_preference_forward needs.  Host only. */
+int flce_preference_workspace_size(const flce_preference_params* p, size_t* bytes);
+
+/*
+ *  loss:     device fp32, 1 element (sum, mean) or P (none).
+ *  rewards:  device fp32 (S): beta R_s.
+ *  seq_grad: device fp32 (S): d loss_p / d logp_t of every kept token t of
+ *            sequence s, the factor 1/P of "mean" included; for the backward.
+ */
+int flce_preference_forward(const flce_preference_params* p, flce_token_view logps, flce_token_view ref_logps,
+                            flce_token_view mask, const void* offsets, float* loss, float* rewards, float* seq_grad,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_logps_t = g seq_grad_s on kept tokens, else 0; grad_loss (g): device fp32, 1 element or P (none). */
+int flce_preference_backward(const flce_preference_params* p, const float* grad_loss, const float* seq_grad,
+                             flce_token_view mask, const void* offsets, void* grad_logps, void* stream);
+
+/*
+ * Clipped policy loss with a KL term.  Per kept token, A its advantage,
+ *   r = exp(logp - old),  s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A),
+ *   with dual_clip c > 1 and A < 0: s = max(s, c A),
+ *   k = e^d - d - 1, d = ref - logp        (an unbiased estimate of KL(policy || reference)),
+ *   loss_t = -s + kl_coef k - entropy_coef entropy_t;
+ * sum over kept tokens, mean over them, the mean over sequences of each one's
+ * mean over its kept tokens (FLCE_REDUCTION_SEQUENCE_MEAN; sequences without
+ * any are left out), or none.  A mean of nothing is NaN, with zero gradients.
+ * On which side of a clipping border a ratio lies is decided in fp64 on
+ * logp - old; on the border itself the unclipped branch is taken.
+ */
+#define FLCE_REDUCTION_SEQUENCE_MEAN 3
+
+typedef struct {
+  int64_t n_seqs;             /* S >= 0                                                  */
+  int64_t length;             /* padded: tokens per row; packed: tokens in all           */
+  int32_t dtype;              /* flce_dtype of logps, old, ref, entropy, gradients       */
+  int32_t reduction;          /* flce_reduction or FLCE_REDUCTION_SEQUENCE_MEAN          */
+  int32_t flags;              /* flce_sequence_flags                                     */
+  int32_t reserved;           /* must be 0                                               */
+  double clip_low;            /* >= 0                                                    */
+  double clip_high;           /* >= 0                                                    */
+  double dual_clip;           /* > 1, or 0 = off                                         */
+  double kl_coef;             /* finite; 0 without a reference                           */
+  double entropy_coef;        /* finite; 0 without entropies                             */
+} flce_policy_params;
+
+typedef struct {
+  int64_t num_tokens;         /* kept tokens                                             */
+  float clip_fraction;        /* share of them whose gradient a clip cuts off            */
+  float kl;                   /* mean of k over them; 0 without a reference              */
+} flce_policy_metrics;
+
+/* Bytes of device workspace flce_policy_forward needs.  Host only. */
+int flce_policy_workspace_size(const flce_policy_params* p, size_t* bytes);
+
+/*
+ *  ref_logps, entropy: NULL data = absent.
+ *  advantages: fp32, per token (in the tokens' layout) or per sequence (S values).
+ *  loss:       device fp32, 1 element, or one per token (none; 0 where masked).
+ *  unit_grad:  device fp32, one per token, 16-byte aligned, or NULL when no
+ *              backward follows: d loss_t / d logp_t, 0 where masked.
+ *  weights:    device fp32 (1 + S), for the backward: [0] the weight of a
+ *              token's loss in the result, [1 + s] that of sequence s's tokens
+ *              (FLCE_REDUCTION_SEQUENCE_MEAN).
+ *  metrics:    device flce_policy_metrics, or NULL.
+ */
+int flce_policy_forward(const flce_policy_params* p, flce_token_view logps, flce_token_view old_logps,
+                        flce_token_view ref_logps, flce_token_view entropy, flce_token_view advantages,
+                        flce_token_view mask, const void* offsets, float* loss, float* unit_grad, float* weights,
+                        flce_policy_metrics* metrics, void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_logps (or NULL) = g w unit_grad, grad_entropy (or NULL) = -g w entropy_coef on kept tokens, both 0
+ * elsewhere; grad_loss (g): device fp32, 1 element or one per token (none). */
+int flce_policy_backward(const flce_policy_params* p, const float* grad_loss, const float* unit_grad,
+                         const float* weights, flce_token_view mask, const void* offsets, void* grad_logps,
+                         void* grad_entropy, void* stream);
+
 /* Library version, major*10000 + minor*100 + patch. */
 int flce_version(void);
 

@@ -10,7 +10,9 @@ declared in ``include/flce.h``).  This module only marshals arguments:
   the workspace with torch and pass the current HIP stream;
 * ``chunked_linear_loss`` / ``weighted_mse`` drive the generic chunked loss
   (``flce_chunked_linear_loss``) with a Python loss function or the built-in
-  weighted squared error (``flce_weighted_mse_chunk``).
+  weighted squared error (``flce_weighted_mse_chunk``);
+* ``preference_loss`` / ``policy_loss`` (``alignment.py``) are torch ops over
+  per-token log-probabilities (``flce_preference_*``, ``flce_policy_*``).
 
 There is no fallback: if the library is missing, ``load()`` raises.
 """
@@ -48,7 +50,9 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_get_st
             "flce_status_string", "flce_version", "flce_chunked_workspace_size",
             "flce_chunked_linear_loss", "flce_weighted_mse_chunk", "flce_forward_backward_workspace_size",
             "flce_forward_backward", "flce_scale_gradients", "flce_forward_timed", "flce_backward_timed",
-            "flce_forward_no_alloc")
+            "flce_forward_no_alloc", "flce_preference_workspace_size", "flce_preference_forward",
+            "flce_preference_backward", "flce_policy_workspace_size", "flce_policy_forward",
+            "flce_policy_backward")
 
 FLCE_KERNEL_FORWARD_TILES = 1
 FLCE_KERNEL_DLOGITS = 2
@@ -105,6 +109,42 @@ class flce_wmse_args(ctypes.Structure):
         ("row_weight", ctypes.c_void_p),
         ("feature_weight", ctypes.c_void_p),
         ("row_loss", ctypes.c_void_p),
+    ]
+
+
+class flce_token_view(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class flce_preference_params(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int64),
+        ("length", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reduction", ctypes.c_int32),
+        ("type", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("length_normalize", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("beta", ctypes.c_double),
+        ("label_smoothing", ctypes.c_double),
+        ("margin", ctypes.c_double),
+    ]
+
+
+class flce_policy_params(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int64),
+        ("length", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reduction", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("clip_low", ctypes.c_double),
+        ("clip_high", ctypes.c_double),
+        ("dual_clip", ctypes.c_double),
+        ("kl_coef", ctypes.c_double),
+        ("entropy_coef", ctypes.c_double),
     ]
 
 
@@ -175,6 +215,19 @@ def load(path: Optional[str] = None):
     i64 = ctypes.c_int64
     lib.flce_weighted_mse_chunk.argtypes = [vp, i64, i64, i64, vp, i64, ctypes.c_int32, vp, vp]
     lib.flce_weighted_mse_chunk.restype = ctypes.c_int
+    view, RP, LP = flce_token_view, ctypes.POINTER(flce_preference_params), ctypes.POINTER(flce_policy_params)
+    lib.flce_preference_workspace_size.argtypes = [RP, ctypes.POINTER(sz)]
+    lib.flce_preference_workspace_size.restype = ctypes.c_int
+    lib.flce_preference_forward.argtypes = [RP, view, view, view, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_preference_forward.restype = ctypes.c_int
+    lib.flce_preference_backward.argtypes = [RP, vp, vp, view, vp, vp, vp]
+    lib.flce_preference_backward.restype = ctypes.c_int
+    lib.flce_policy_workspace_size.argtypes = [LP, ctypes.POINTER(sz)]
+    lib.flce_policy_workspace_size.restype = ctypes.c_int
+    lib.flce_policy_forward.argtypes = [LP, view, view, view, view, view, view, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_policy_forward.restype = ctypes.c_int
+    lib.flce_policy_backward.argtypes = [LP, vp, vp, vp, view, vp, vp, vp, vp]
+    lib.flce_policy_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -289,6 +342,45 @@ def flce_chunked_linear_loss(params, inputs, weight, fn, user, loss, grad_inputs
 def weighted_mse_chunk_fn():
     """The library's built-in loss function (flce_weighted_mse_chunk) as a CHUNK_LOSS_FN."""
     return ctypes.cast(load().flce_weighted_mse_chunk, CHUNK_LOSS_FN)
+
+
+def flce_preference_workspace_size(params: flce_preference_params) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_preference_workspace_size(ctypes.byref(params), ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_preference_workspace_size")
+    return out.value
+
+
+def flce_preference_forward(params, logps, ref_logps, mask, offsets, loss, rewards, seq_grad, workspace,
+                            workspace_bytes, stream) -> int:
+    return load().flce_preference_forward(ctypes.byref(params), logps, ref_logps, mask, offsets, loss, rewards,
+                                          seq_grad, workspace, workspace_bytes, stream)
+
+
+def flce_preference_backward(params, grad_loss, seq_grad, mask, offsets, grad_logps, stream) -> int:
+    return load().flce_preference_backward(ctypes.byref(params), grad_loss, seq_grad, mask, offsets, grad_logps,
+                                           stream)
+
+
+def flce_policy_workspace_size(params: flce_policy_params) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_policy_workspace_size(ctypes.byref(params), ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_policy_workspace_size")
+    return out.value
+
+
+def flce_policy_forward(params, logps, old_logps, ref_logps, entropy, advantages, mask, offsets, loss, unit_grad,
+                        weights, metrics, workspace, workspace_bytes, stream) -> int:
+    return load().flce_policy_forward(ctypes.byref(params), logps, old_logps, ref_logps, entropy, advantages, mask,
+                                      offsets, loss, unit_grad, weights, metrics, workspace, workspace_bytes, stream)
+
+
+def flce_policy_backward(params, grad_loss, unit_grad, weights, mask, offsets, grad_logps, grad_entropy,
+                         stream) -> int:
+    return load().flce_policy_backward(ctypes.byref(params), grad_loss, unit_grad, weights, mask, offsets, grad_logps,
+                                       grad_entropy, stream)
 
 
 def flce_get_status(workspace, stream) -> int:
@@ -746,3 +838,8 @@ def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_ro
                         chunk_rows=chunk_rows, grad_weight_dtype=grad_weight_dtype,
                         grad_weight_accum_dtype=grad_weight_accum_dtype, grad_weight=grad_weight,
                         workspace=workspace)
+
+
+# ----------------------------------------------------------------------------- alignment losses
+
+from .alignment import policy_loss, preference_loss  # noqa: E402,F401

@@ -1,0 +1,295 @@
+"""Preference and policy losses over per-token log-probabilities: the torch side
+of flce_preference_* and flce_policy_* (include/flce.h has the formulas).
+
+Token tensors are (S, L), with any row stride and contiguous rows, or, with
+``offsets`` (S + 1 int64 or int32 values on the GPU), one packed (T,) tensor in
+which sequence s is ``[offsets[s], offsets[s + 1])``.  ``mask`` (bool or uint8,
+the tokens' shape) says which tokens count; nothing that a masked token holds is
+used, NaN and infinities included, and its gradient is 0.
+
+Everything runs on the current stream; nothing synchronises.
+"""
+from __future__ import annotations
+
+import contextlib
+import functools
+import math
+from typing import Optional
+
+from . import (FLCE_OK, DTYPES, REDUCTIONS, FlceError, _dtype_name, _ptr, _stream_handle, flce_policy_backward,
+               flce_policy_forward, flce_policy_params, flce_policy_workspace_size, flce_preference_backward,
+               flce_preference_forward, flce_preference_params, flce_preference_workspace_size, flce_token_view)
+
+PREFERENCE_TYPES = {"sigmoid": 0, "hinge": 1, "squared": 2}
+POLICY_REDUCTIONS = {**REDUCTIONS, "sequence_mean": 3}
+FLCE_OFFSETS_INT32 = 1
+FLCE_ADVANTAGE_PER_SEQUENCE = 2
+
+
+def _on_device(device):
+    """The library launches on the current device: makes it the tensors'."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _check_rows(t, name):
+    """Rows are read as contiguous; only the distance between them is free."""
+    if t.dim() == 1:
+        ok = t.stride(0) == 1 or t.shape[0] <= 1
+    else:
+        ok = (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
+    if not ok and t.numel() > 0:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {t.stride()}")
+
+
+def _view(t):
+    if t is None:
+        return flce_token_view(None, 0)
+    return flce_token_view(t.data_ptr(), t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0)
+
+
+def _check_tokens(logps, others, offsets, mask, constants, per_sequence=()):
+    """Types, shapes, layout and device of the token tensors.  The kernels trust all of them.
+    Returns (n_seqs, length, flags)."""
+    import torch
+    _dtype_name(logps)
+    for name, t in others:
+        if t is not None and t.dtype != logps.dtype:
+            raise TypeError(f"{name} dtype {t.dtype} differs from logps' {logps.dtype}")
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"mask must be bool or uint8, not {mask.dtype}")
+    flags = 0
+    if offsets is None:
+        if logps.dim() != 2:
+            raise ValueError(f"logps must be (S, L), or (T,) with offsets, got {tuple(logps.shape)}")
+        n_seqs, length = logps.shape
+    else:
+        if offsets.dtype not in (torch.int64, torch.int32):
+            raise TypeError(f"offsets must be int64 or int32, not {offsets.dtype}")
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError(f"offsets must hold S + 1 values, got shape {tuple(offsets.shape)}")
+        if logps.dim() != 1:
+            raise ValueError(f"packed logps must be (T,), got {tuple(logps.shape)}")
+        n_seqs, length = offsets.shape[0] - 1, logps.shape[0]
+        flags |= FLCE_OFFSETS_INT32 if offsets.dtype == torch.int32 else 0
+    named = [("logps", logps), *others, ("mask", mask)]
+    for name, t in named:
+        if t is not None and t.shape != logps.shape:
+            raise ValueError(f"{name} must have logps' shape {tuple(logps.shape)}, got {tuple(t.shape)}")
+    for name, t in named:
+        if t is not None:
+            _check_rows(t, name)
+    if offsets is not None and not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous")
+    for name, t in [*named, ("offsets", offsets), *per_sequence]:
+        if t is not None and (t.device.type != "cuda" or t.device != logps.device):
+            raise ValueError(f"{name} must be on logps' GPU ({logps.device}), not {t.device}")
+    if torch.is_grad_enabled():
+        for name, t in constants:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} is a constant of the loss and gets no gradient: detach it")
+    return n_seqs, length, flags
+
+
+def _raise_for(rc, where):
+    if rc != FLCE_OK:
+        raise FlceError(rc, where)
+
+
+# ----------------------------------------------------------------------------- preference loss
+
+def _preference_forward(p, logps, ref, mask, offsets):
+    import torch
+    dev = logps.device
+    pairs = p.n_seqs // 2
+    with _on_device(dev):
+        ws_bytes = flce_preference_workspace_size(p)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        loss = torch.empty((pairs,) if p.reduction == 0 else (), dtype=torch.float32, device=dev)
+        rewards = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
+        seq_grad = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
+        _raise_for(flce_preference_forward(p, _view(logps), _view(ref), _view(mask), _ptr(offsets), _ptr(loss),
+                                           _ptr(rewards), _ptr(seq_grad), _ptr(workspace), ws_bytes,
+                                           _stream_handle(dev)), "flce_preference_forward")
+    return loss, rewards, seq_grad
+
+
+@functools.lru_cache(maxsize=None)
+def _preference_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class PreferenceLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logps, ref, mask, offsets, p):
+            loss, rewards, seq_grad = _preference_forward(p, logps, ref, mask, offsets)
+            ctx.mark_non_differentiable(rewards)
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(seq_grad, mask, offsets)
+            ctx.p, ctx.like = p, (logps.shape, logps.dtype, logps.device)
+            return loss, rewards
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, g, _):
+            if g is None:
+                return (None,) * 5
+            seq_grad, mask, offsets = ctx.saved_tensors
+            shape, dtype, dev = ctx.like
+            g = g.to(torch.float32).contiguous()
+            grad = torch.empty(shape, dtype=dtype, device=dev)
+            with _on_device(dev):
+                _raise_for(flce_preference_backward(ctx.p, _ptr(g), _ptr(seq_grad), _view(mask), _ptr(offsets),
+                                                    _ptr(grad), _stream_handle(dev)), "flce_preference_backward")
+            return grad, None, None, None, None
+
+    return PreferenceLoss
+
+
+def preference_loss(logps, ref_logps=None, *, offsets=None, mask=None, beta: float = 0.1, loss_type: str = "sigmoid",
+                    label_smoothing: float = 0.0, margin: float = 0.0, length_normalize: bool = False,
+                    reduction: str = "mean", return_metrics: bool = False):
+    """Paired preference loss from per-token log-probabilities, differentiable in ``logps``.
+
+    The first half of the sequences are the chosen answers, the second half the rejected ones of
+    the same pairs.  R_s sums logps - ref_logps (or logps, without a reference) over a sequence's
+    kept tokens, divided by their number with ``length_normalize``; h = beta (R_chosen -
+    R_rejected) - margin; the loss of a pair is
+      "sigmoid"  -(1 - label_smoothing) log sigmoid(h) - label_smoothing log sigmoid(-h)
+      "hinge"    max(0, 1 - h)
+      "squared"  (h / beta - 1 / (2 beta))^2.
+    Returns the fp32 loss (one value, or one per pair for "none"); with ``return_metrics`` also
+    {"chosen_rewards", "rejected_rewards"}: beta R of each pair's answers."""
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"invalid reduction {reduction!r}")
+    if loss_type not in PREFERENCE_TYPES:
+        raise ValueError(f"invalid loss_type {loss_type!r}")
+    if not (math.isfinite(beta) and beta > 0):
+        raise ValueError(f"beta must be positive, got {beta}")
+    if not 0 <= label_smoothing <= 1 or (label_smoothing and loss_type != "sigmoid"):
+        raise ValueError(f"label_smoothing must be within [0, 1], and 0 unless loss_type is 'sigmoid', "
+                         f"got {label_smoothing}")
+    if not math.isfinite(margin):
+        raise ValueError(f"margin must be finite, got {margin}")
+    n_seqs, length, flags = _check_tokens(logps, [("ref_logps", ref_logps)], offsets, mask,
+                                          [("ref_logps", ref_logps)])
+    if n_seqs % 2:
+        raise ValueError(f"an even number of sequences is needed (chosen, then rejected), got {n_seqs}")
+    p = flce_preference_params(n_seqs, length, DTYPES[_dtype_name(logps)], REDUCTIONS[reduction],
+                               PREFERENCE_TYPES[loss_type], flags, 1 if length_normalize else 0, 0, beta,
+                               label_smoothing, margin)
+    loss, rewards = _preference_function().apply(logps, ref_logps, mask, offsets, p)
+    if not return_metrics:
+        return loss
+    return loss, {"chosen_rewards": rewards[:n_seqs // 2], "rejected_rewards": rewards[n_seqs // 2:]}
+
+
+# ----------------------------------------------------------------------------- policy loss
+
+def _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets, needs_grad, metrics):
+    import torch
+    dev = logps.device
+    with _on_device(dev):
+        ws_bytes = flce_policy_workspace_size(p)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        loss = torch.empty(logps.shape if p.reduction == 0 else (), dtype=torch.float32, device=dev)
+        unit = torch.empty(logps.shape, dtype=torch.float32, device=dev) if needs_grad else None
+        weights = torch.empty(1 + p.n_seqs, dtype=torch.float32, device=dev)
+        per_seq = p.flags & FLCE_ADVANTAGE_PER_SEQUENCE
+        adv = flce_token_view(advantages.data_ptr(), 0) if per_seq else _view(advantages)
+        _raise_for(flce_policy_forward(p, _view(logps), _view(old), _view(ref), _view(entropy), adv, _view(mask),
+                                       _ptr(offsets), _ptr(loss), _ptr(unit), _ptr(weights), _ptr(metrics),
+                                       _ptr(workspace), ws_bytes, _stream_handle(dev)), "flce_policy_forward")
+    return loss, unit, weights
+
+
+@functools.lru_cache(maxsize=None)
+def _policy_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class PolicyLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logps, entropy, old, ref, advantages, mask, offsets, p, metrics):
+            loss, unit, weights = _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets,
+                                                  ctx.needs_input_grad[0], metrics)
+            ctx.save_for_backward(unit, weights, mask, offsets)
+            ctx.p, ctx.like = p, (logps.shape, logps.dtype, logps.device)
+            return loss
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, g):
+            unit, weights, mask, offsets = ctx.saved_tensors
+            shape, dtype, dev = ctx.like
+            g = g.to(torch.float32).contiguous()
+            grads = [torch.empty(shape, dtype=dtype, device=dev) if need else None
+                     for need in ctx.needs_input_grad[:2]]
+            with _on_device(dev):
+                _raise_for(flce_policy_backward(ctx.p, _ptr(g), _ptr(unit), _ptr(weights), _view(mask),
+                                                _ptr(offsets), _ptr(grads[0]), _ptr(grads[1]), _stream_handle(dev)),
+                           "flce_policy_backward")
+            return (*grads, None, None, None, None, None, None, None)
+
+    return PolicyLoss
+
+
+def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, offsets=None, mask=None,
+                clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: Optional[float] = None,
+                kl_coef: float = 0.0, entropy_coef: float = 0.0, reduction: str = "mean",
+                return_metrics: bool = False):
+    """Clipped policy loss with a KL term, differentiable in ``logps`` and ``entropy``.
+
+    Per kept token, with r = exp(logps - old_logps) and A its advantage:
+      s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A); for A < 0 and ``dual_clip`` c: max(s, c A)
+      k = e^d - d - 1 with d = ref_logps - logps
+      loss = -s + kl_coef k - entropy_coef entropy
+    ``advantages`` (fp32): the tokens' shape, or one value per sequence, (S,) or (S, 1).
+    ``reduction``: "mean" over the kept tokens, "sequence_mean" (mean over sequences of each one's
+    mean, sequences without a kept token left out), "sum", or "none" (the tokens' shape).  A mean of
+    nothing is NaN, with zero gradients.
+    Returns the fp32 loss; with ``return_metrics`` also {"num_tokens" (int64), "clip_fraction",
+    "kl"}: tokens kept, the share whose gradient a clip cuts off, and the mean of k."""
+    import torch
+    if reduction not in POLICY_REDUCTIONS:
+        raise ValueError(f"invalid reduction {reduction!r}")
+    if not (clip_low >= 0 and clip_high >= 0):
+        raise ValueError(f"clip_low and clip_high must be at least 0, got {clip_low} and {clip_high}")
+    if dual_clip is not None and not (math.isfinite(dual_clip) and dual_clip > 1):
+        raise ValueError(f"dual_clip must be above 1, got {dual_clip}")
+    if not (math.isfinite(kl_coef) and math.isfinite(entropy_coef)):
+        raise ValueError(f"kl_coef and entropy_coef must be finite, got {kl_coef} and {entropy_coef}")
+    if kl_coef and ref_logps is None:
+        raise ValueError("kl_coef needs ref_logps")
+    if entropy_coef and entropy is None:
+        raise ValueError("entropy_coef needs entropy")
+    if advantages.dtype != torch.float32:
+        raise TypeError(f"advantages must be float32, not {advantages.dtype}")
+    others = [("old_logps", old_logps), ("ref_logps", ref_logps), ("entropy", entropy)]
+    constants = [("old_logps", old_logps), ("ref_logps", ref_logps), ("advantages", advantages)]
+    n_seqs, length, flags = _check_tokens(logps, others, offsets, mask, constants, [("advantages", advantages)])
+    per_seq = tuple(advantages.shape) in ((n_seqs,), (n_seqs, 1))
+    if advantages.shape == logps.shape:
+        if per_seq and advantages.dim() == 1:
+            raise ValueError(f"advantages of shape {tuple(advantages.shape)} could be per token or per sequence: "
+                             f"pass ({n_seqs}, 1) for one per sequence, or pad the packed tokens")
+        per_seq = False
+    elif not per_seq:
+        raise ValueError(f"advantages must have logps' shape {tuple(logps.shape)} or ({n_seqs},), "
+                         f"got {tuple(advantages.shape)}")
+    if per_seq:
+        if n_seqs > 1 and advantages.stride(0) != 1:
+            raise ValueError("advantages must be contiguous")
+        flags |= FLCE_ADVANTAGE_PER_SEQUENCE
+    else:
+        _check_rows(advantages, "advantages")
+    p = flce_policy_params(n_seqs, length, DTYPES[_dtype_name(logps)], POLICY_REDUCTIONS[reduction], flags, 0,
+                           clip_low, clip_high, dual_clip or 0.0, kl_coef, entropy_coef)
+    metrics = torch.empty(2, dtype=torch.int64, device=logps.device) if return_metrics else None
+    loss = _policy_function().apply(logps, entropy, old_logps, ref_logps, advantages, mask, offsets, p, metrics)
+    if not return_metrics:
+        return loss
+    both = metrics.view(torch.float32)
+    return loss, {"num_tokens": metrics[0], "clip_fraction": both[2], "kl": both[3]}
