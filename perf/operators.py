@@ -340,14 +340,15 @@ def _run_own(s):
             grads = torch.autograd.grad((lp, ent), leaves, (s["grad_logps"], s["grad_entropy"]))
             out.update(zip(("grad_hidden", "grad_weight", "grad_bias"), grads))
         return out
+    ref = s["ref_logps"].detach() if s["reference"] else None         # constants of both losses
     if s["op"] == "preference":
-        loss, metrics = flce.preference_loss(s["logps"], s["ref_logps"], offsets=s["offsets"], mask=s["mask"],
+        loss, metrics = flce.preference_loss(s["logps"], ref, offsets=s["offsets"], mask=s["mask"],
                                              beta=BETA, loss_type=s["loss"], label_smoothing=s["smoothing"],
                                              length_normalize=s["normalize"], return_metrics=True)
         grad, = torch.autograd.grad(loss, (s["logps"],))
         return dict(loss=loss.detach(), chosen=metrics["chosen_rewards"], rejected=metrics["rejected_rewards"],
                     grad=grad)
-    loss = flce.policy_loss(s["logps"], s["old_logps"], s["advantages"], ref_logps=s["ref_logps"],
+    loss = flce.policy_loss(s["logps"], s["old_logps"].detach(), s["advantages"], ref_logps=ref,
                             entropy=s["entropies"], offsets=s["offsets"], mask=s["mask"], clip_low=CLIP_LOW,
                             clip_high=CLIP_HIGH, dual_clip=DUAL if s["dual"] else None,
                             kl_coef=KL if s["reference"] else 0.0, entropy_coef=ENTROPY if s["entropy"] else 0.0,
