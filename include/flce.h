@@ -334,6 +334,39 @@ int flce_weighted_mse_chunk(void* user, int64_t row0, int64_t rows, int64_t voca
                             int32_t dtype, float* loss, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Log-probabilities of the targets and entropies, per token, with gradients:
+ *   logp_i = z_{i,t_i} - LSE_i,   H_i = -sum_j p_ij log p_ij,   p_ij = exp(z_ij - LSE_i),
+ * z as in flce_forward.  params->reduction must be FLCE_REDUCTION_NONE and z_loss
+ * 0.  Rows whose target is ignored (or out of range, see flce_get_status) give 0
+ * and take no gradient, whatever their hidden state holds.  A logit of -inf (a bias that masks vocabulary entries)
+ * has probability 0, and one below -2^99 counts as -inf; a row whose every logit
+ * does gives NaN.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of device workspace one call of `pass` needs (flce_pass).  Host only. */
+int flce_logprobs_workspace_size(const flce_params* p, int pass, size_t* bytes);
+
+/*
+ *  logps:   device fp32 (N).
+ *  entropy: device fp32 (N), in nats, or NULL.
+ *  lse:     device fp32 (N), every row: for the backward.
+ */
+int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* weight, const void* bias,
+                          const void* targets, float* logps, float* entropy, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of  sum_i grad_logps_i logp_i + grad_entropy_i H_i.
+ *  lse, entropy: from the forward (entropy may be NULL without grad_entropy).
+ *  grad_logps, grad_entropy: device fp32 (N); NULL = zeros.
+ *  grad_hidden, grad_weight, grad_bias, flags: as flce_backward.
+ */
+int flce_logprobs_backward(const flce_params* p, const void* hidden, const void* weight, const void* bias,
+                           const void* targets, const float* lse, const float* entropy, const float* grad_logps,
+                           const float* grad_entropy, void* grad_hidden, void* grad_weight, void* grad_bias,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Preference and policy losses over per-token log-probabilities (as
  * flce_logprobs_forward gives them), forward and backward.
  *

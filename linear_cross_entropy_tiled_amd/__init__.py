@@ -11,6 +11,8 @@ declared in ``include/flce.h``).  This module only marshals arguments:
 * ``chunked_linear_loss`` / ``weighted_mse`` drive the generic chunked loss
   (``flce_chunked_linear_loss``) with a Python loss function or the built-in
   weighted squared error (``flce_weighted_mse_chunk``);
+* ``token_logprobs`` (``logprobs.py``) is a torch op for per-token log-probabilities
+  and entropies of the head (``flce_logprobs_*``);
 * ``preference_loss`` / ``policy_loss`` (``alignment.py``) are torch ops over
   per-token log-probabilities (``flce_preference_*``, ``flce_policy_*``).
 
@@ -52,7 +54,8 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_get_st
             "flce_forward_backward", "flce_scale_gradients", "flce_forward_timed", "flce_backward_timed",
             "flce_forward_no_alloc", "flce_preference_workspace_size", "flce_preference_forward",
             "flce_preference_backward", "flce_policy_workspace_size", "flce_policy_forward",
-            "flce_policy_backward")
+            "flce_policy_backward", "flce_logprobs_workspace_size", "flce_logprobs_forward",
+            "flce_logprobs_backward")
 
 FLCE_KERNEL_FORWARD_TILES = 1
 FLCE_KERNEL_DLOGITS = 2
@@ -215,6 +218,12 @@ def load(path: Optional[str] = None):
     i64 = ctypes.c_int64
     lib.flce_weighted_mse_chunk.argtypes = [vp, i64, i64, i64, vp, i64, ctypes.c_int32, vp, vp]
     lib.flce_weighted_mse_chunk.restype = ctypes.c_int
+    lib.flce_logprobs_workspace_size.argtypes = [P, ctypes.c_int, ctypes.POINTER(sz)]
+    lib.flce_logprobs_workspace_size.restype = ctypes.c_int
+    lib.flce_logprobs_forward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_logprobs_forward.restype = ctypes.c_int
+    lib.flce_logprobs_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_logprobs_backward.restype = ctypes.c_int
     view, RP, LP = flce_token_view, ctypes.POINTER(flce_preference_params), ctypes.POINTER(flce_policy_params)
     lib.flce_preference_workspace_size.argtypes = [RP, ctypes.POINTER(sz)]
     lib.flce_preference_workspace_size.restype = ctypes.c_int
@@ -342,6 +351,27 @@ def flce_chunked_linear_loss(params, inputs, weight, fn, user, loss, grad_inputs
 def weighted_mse_chunk_fn():
     """The library's built-in loss function (flce_weighted_mse_chunk) as a CHUNK_LOSS_FN."""
     return ctypes.cast(load().flce_weighted_mse_chunk, CHUNK_LOSS_FN)
+
+
+def flce_logprobs_workspace_size(params: flce_params, pass_: int) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_logprobs_workspace_size(ctypes.byref(params), pass_, ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_logprobs_workspace_size")
+    return out.value
+
+
+def flce_logprobs_forward(params, hidden, weight, bias, targets, logps, entropy, lse, workspace, workspace_bytes,
+                          stream) -> int:
+    return load().flce_logprobs_forward(ctypes.byref(params), hidden, weight, bias, targets, logps, entropy, lse,
+                                        workspace, workspace_bytes, stream)
+
+
+def flce_logprobs_backward(params, hidden, weight, bias, targets, lse, entropy, grad_logps, grad_entropy, grad_hidden,
+                           grad_weight, grad_bias, workspace, workspace_bytes, stream) -> int:
+    return load().flce_logprobs_backward(ctypes.byref(params), hidden, weight, bias, targets, lse, entropy, grad_logps,
+                                         grad_entropy, grad_hidden, grad_weight, grad_bias, workspace, workspace_bytes,
+                                         stream)
 
 
 def flce_preference_workspace_size(params: flce_preference_params) -> int:
@@ -840,6 +870,7 @@ def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_ro
                         workspace=workspace)
 
 
-# ----------------------------------------------------------------------------- alignment losses
+# ----------------------------------------------------------------------------- alignment training
 
+from .logprobs import token_logprobs  # noqa: E402,F401
 from .alignment import policy_loss, preference_loss  # noqa: E402,F401

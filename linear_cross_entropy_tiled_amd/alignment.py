@@ -11,27 +11,19 @@ Everything runs on the current stream; nothing synchronises.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 import math
 from typing import Optional
 
-from . import (FLCE_OK, DTYPES, REDUCTIONS, FlceError, _dtype_name, _ptr, _stream_handle, flce_policy_backward,
+from . import (DTYPES, REDUCTIONS, _dtype_name, _ptr, _stream_handle, flce_policy_backward,
                flce_policy_forward, flce_policy_params, flce_policy_workspace_size, flce_preference_backward,
                flce_preference_forward, flce_preference_params, flce_preference_workspace_size, flce_token_view)
+from .logprobs import on_device, raise_for
 
 PREFERENCE_TYPES = {"sigmoid": 0, "hinge": 1, "squared": 2}
 POLICY_REDUCTIONS = {**REDUCTIONS, "sequence_mean": 3}
 FLCE_OFFSETS_INT32 = 1
 FLCE_ADVANTAGE_PER_SEQUENCE = 2
-
-
-def _on_device(device):
-    """The library launches on the current device: makes it the tensors'."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
 
 
 def _check_rows(t, name):
@@ -93,24 +85,19 @@ def _check_tokens(logps, others, offsets, mask, constants, per_sequence=()):
     return n_seqs, length, flags
 
 
-def _raise_for(rc, where):
-    if rc != FLCE_OK:
-        raise FlceError(rc, where)
-
-
 # ----------------------------------------------------------------------------- preference loss
 
 def _preference_forward(p, logps, ref, mask, offsets):
     import torch
     dev = logps.device
     pairs = p.n_seqs // 2
-    with _on_device(dev):
+    with on_device(dev):
         ws_bytes = flce_preference_workspace_size(p)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         loss = torch.empty((pairs,) if p.reduction == 0 else (), dtype=torch.float32, device=dev)
         rewards = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
         seq_grad = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
-        _raise_for(flce_preference_forward(p, _view(logps), _view(ref), _view(mask), _ptr(offsets), _ptr(loss),
+        raise_for(flce_preference_forward(p, _view(logps), _view(ref), _view(mask), _ptr(offsets), _ptr(loss),
                                            _ptr(rewards), _ptr(seq_grad), _ptr(workspace), ws_bytes,
                                            _stream_handle(dev)), "flce_preference_forward")
     return loss, rewards, seq_grad
@@ -140,8 +127,8 @@ def _preference_function():
             shape, dtype, dev = ctx.like
             g = g.to(torch.float32).contiguous()
             grad = torch.empty(shape, dtype=dtype, device=dev)
-            with _on_device(dev):
-                _raise_for(flce_preference_backward(ctx.p, _ptr(g), _ptr(seq_grad), _view(mask), _ptr(offsets),
+            with on_device(dev):
+                raise_for(flce_preference_backward(ctx.p, _ptr(g), _ptr(seq_grad), _view(mask), _ptr(offsets),
                                                     _ptr(grad), _stream_handle(dev)), "flce_preference_backward")
             return grad, None, None, None, None
 
@@ -191,7 +178,7 @@ def preference_loss(logps, ref_logps=None, *, offsets=None, mask=None, beta: flo
 def _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets, needs_grad, metrics):
     import torch
     dev = logps.device
-    with _on_device(dev):
+    with on_device(dev):
         ws_bytes = flce_policy_workspace_size(p)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         loss = torch.empty(logps.shape if p.reduction == 0 else (), dtype=torch.float32, device=dev)
@@ -199,7 +186,7 @@ def _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets, need
         weights = torch.empty(1 + p.n_seqs, dtype=torch.float32, device=dev)
         per_seq = p.flags & FLCE_ADVANTAGE_PER_SEQUENCE
         adv = flce_token_view(advantages.data_ptr(), 0) if per_seq else _view(advantages)
-        _raise_for(flce_policy_forward(p, _view(logps), _view(old), _view(ref), _view(entropy), adv, _view(mask),
+        raise_for(flce_policy_forward(p, _view(logps), _view(old), _view(ref), _view(entropy), adv, _view(mask),
                                        _ptr(offsets), _ptr(loss), _ptr(unit), _ptr(weights), _ptr(metrics),
                                        _ptr(workspace), ws_bytes, _stream_handle(dev)), "flce_policy_forward")
     return loss, unit, weights
@@ -227,8 +214,8 @@ def _policy_function():
             g = g.to(torch.float32).contiguous()
             grads = [torch.empty(shape, dtype=dtype, device=dev) if need else None
                      for need in ctx.needs_input_grad[:2]]
-            with _on_device(dev):
-                _raise_for(flce_policy_backward(ctx.p, _ptr(g), _ptr(unit), _ptr(weights), _view(mask),
+            with on_device(dev):
+                raise_for(flce_policy_backward(ctx.p, _ptr(g), _ptr(unit), _ptr(weights), _view(mask),
                                                 _ptr(offsets), _ptr(grads[0]), _ptr(grads[1]), _stream_handle(dev)),
                            "flce_policy_backward")
             return (*grads, None, None, None, None, None, None, None)

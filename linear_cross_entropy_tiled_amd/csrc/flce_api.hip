@@ -424,6 +424,71 @@ int flce_scale_gradients(const flce_params* p, const float* g, void* grad_hidden
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 
+// The log-probability entry points take the loss's parameters, of which the
+// reduction and the z-loss have no meaning there.
+static int logprobs_plan(const flce_params* p, Plan* pl) {
+  const int rc = make_plan(p, pl);
+  if (rc != FLCE_OK) return rc;
+  return pl->reduction == FLCE_REDUCTION_NONE && pl->z_loss == 0.0f ? FLCE_OK : FLCE_ERR_INVALID_ARG;
+}
+
+static size_t logprobs_backward_bytes(const Plan& pl) { return align_up(pl.b_bytes + size_t(pl.N_pad) * 4, 256); }
+
+int flce_logprobs_workspace_size(const flce_params* p, int pass, size_t* bytes) {
+  if (!bytes) return FLCE_ERR_INVALID_ARG;
+  Plan pl;
+  const int rc = logprobs_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  if (pass == FLCE_PASS_FORWARD) *bytes = logprobs_forward_bytes(pl);
+  else if (pass == FLCE_PASS_BACKWARD) *bytes = logprobs_backward_bytes(pl);
+  else return FLCE_ERR_INVALID_ARG;
+  return FLCE_OK;
+}
+
+int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* weight, const void* bias,
+                          const void* targets, float* logps, float* entropy, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  Plan pl;
+  const int rc = logprobs_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  pl.has_bias = bias != nullptr;
+  if (!workspace || !weight) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && (!hidden || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) || !aligned16(targets))
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < logprobs_forward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = launch_logprobs(pl, hidden, weight, bias, targets, logps, entropy, lse,
+                                       static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+int flce_logprobs_backward(const flce_params* p, const void* hidden, const void* weight, const void* bias,
+                           const void* targets, const float* lse, const float* entropy, const float* grad_logps,
+                           const float* grad_entropy, void* grad_hidden, void* grad_weight, void* grad_bias,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  Plan pl;
+  const int rc = logprobs_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  pl.has_bias = bias != nullptr;
+  if (!weight || !grad_weight || !workspace) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && (!hidden || !targets || !lse || !grad_hidden)) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && grad_entropy && !entropy) return FLCE_ERR_INVALID_ARG;
+  if (grad_bias && !bias) return FLCE_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) ||
+      !aligned16(targets) || !aligned16(grad_hidden) || !aligned16(grad_weight) || !aligned16(grad_bias))
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < logprobs_backward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  LogprobGrad lg;
+  lg.grad_logps = grad_logps;
+  lg.grad_entropy = grad_entropy;
+  lg.entropy = entropy;
+  lg.coefE = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.b_bytes);
+  pl.lg = &lg;
+  const hipError_t e = launch_backward(pl, hidden, weight, bias, targets, lse, nullptr, grad_hidden, grad_weight,
+                                       grad_bias, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
 int flce_chunked_workspace_size(const flce_chunked_params* p, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   ChunkPlan pl;

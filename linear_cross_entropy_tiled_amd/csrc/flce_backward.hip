@@ -122,6 +122,91 @@ __global__ __launch_bounds__(1024) void bwd_prep_kernel(PrepArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// The same constants for log-probabilities and entropies: with upstream gradients
+// g of log p_t and h of H,
+//   d / d z_j = g [j = t] - p_j (g + h (H + log p_j))
+//             = coefA p_j + coefE p_j log2 p_j - coefB [j = t],
+// coefA = -(g + h H), coefE = -h ln 2, coefB = -g.
+// ---------------------------------------------------------------------------
+struct LpPrepArgs {
+  const void* targets;
+  int tgt_i32;
+  const float* lse;
+  const float* entropy;
+  const float* grad_logps;
+  const float* grad_entropy;
+  int N, V, N_pad;
+  int64_t ignore_index;
+  float* coefA;
+  float* coefB;
+  float* coefE;
+  float* lseL;
+  int* tgt;
+  int* status;
+  float* dscale;
+  int f16_d;
+  float abs_scale;
+};
+
+__global__ __launch_bounds__(1024) void lp_prep_kernel(LpPrepArgs a) {
+  __shared__ float sm[1024];
+  __shared__ int sb[1024];
+  const int tid = threadIdx.x;
+  float dmax = 0.0f;
+  int bad = 0;
+  for (int i = tid; i < a.N_pad; i += 1024) {
+    // padding and ignored rows: coefficients 0 and an LSE beyond any logit, so that p = 0,
+    // but finite, so that coefE log2 p is 0 too
+    float ca = 0.0f, cb = 0.0f, ce = 0.0f, ll = -kMasked;
+    int tg = -1;
+    if (i < a.N) {
+      const int64_t t = load_target(a.targets, i, a.tgt_i32);
+      const bool in_range = t >= 0 && t < a.V;
+      bad |= (t != a.ignore_index && !in_range) ? 1 : 0;
+      if (t != a.ignore_index && in_range) {
+        ll = a.lse[i] * kLog2e;
+        const float g = a.grad_logps ? a.grad_logps[i] : 0.0f;
+        const float h = a.grad_entropy ? a.grad_entropy[i] : 0.0f;
+        cb = -g;
+        ca = a.grad_entropy ? -fmaf(h, a.entropy[i], g) : -g;
+        if (isnan(ll)) ca = ll;
+        ce = -h * kLn2;
+        tg = (int)t;
+      }
+    }
+    a.coefA[i] = ca;
+    a.coefB[i] = cb;
+    a.coefE[i] = ce;
+    a.lseL[i] = ll;
+    a.tgt[i] = tg;
+    // |p log2 p| < 0.54
+    dmax = fmaxf(dmax, fabsf(ca) + fabsf(cb) + 0.54f * fabsf(ce));
+  }
+  sm[tid] = dmax;
+  sb[tid] = bad;
+  __syncthreads();
+  for (int w = 512; w > 0; w >>= 1) {
+    if (tid < w) {
+      sm[tid] = fmaxf(sm[tid], sm[tid + w]);
+      sb[tid] |= sb[tid + w];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.status[0] = sb[0] ? FLCE_ERR_TARGET_OUT_OF_RANGE : FLCE_OK;
+    int s = 0;
+    const float bound = a.f16_d ? sm[0] * a.abs_scale : 0.0f;   // >= every |D|
+    if (bound > 0.0f && isfinite(bound)) {
+      int e;
+      frexpf(bound, &e);
+      s = min(max(14 - e, -120), 120);
+    }
+    a.dscale[0] = ldexpf(1.0f, s);
+    a.dscale[1] = ldexpf(1.0f, -s);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Stores of 4 consecutive values (one lane, 4 consecutive rows of a tile),
 // rounded to nearest even.
 // ---------------------------------------------------------------------------
@@ -205,6 +290,7 @@ struct DlogitsArgs {
   float* gb_part;   // [n_tt][ld_gb]
   int ld_gb;
   const float* dscale;   // [0]: factor D is stored with
+  const float* coefE;    // ENTROPY only
 };
 
 // DPP lane permutations within each 16-lane row, each an involution that
@@ -230,7 +316,11 @@ __device__ __forceinline__ void halve_exchange(float (&h)[32], int lane) {
   }
 }
 
-template <typename T, bool HAS_BIAS, bool SOFTCAP>
+// ENTROPY: D has the term coefE p log2 p besides (log-probabilities and entropies).
+// The exponent is kept finite there: a logit of -inf then has p = 0 and p log2 p = 0,
+// and so has every logit of an ignored row whose hidden state holds NaN, whose
+// coefficients are 0 (those of a row that counts are NaN then).
+template <typename T, bool HAS_BIAS, bool SOFTCAP, bool ENTROPY = false>
 __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a) {
   constexpr int E = sizeof(T);
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
@@ -258,7 +348,8 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
   // per-token coefficients (coefA, coefB, lseL, target) of the 256 tokens
   // and the bias of the 256 vocabulary rows, staged in LDS by DMA; the main
   // loop's first stage wait covers them
-  static __shared__ __attribute__((aligned(16))) char vec_lds[4 * 1024 + 256 * sizeof(T)];
+  static __shared__ __attribute__((aligned(16))) char vec_lds[(ENTROPY ? 5 : 4) * 1024 + 256 * sizeof(T)];
+  constexpr int kBiasAt = ENTROPY ? 5120 : 4096;
   {
     const uint32_t tok_bytes = 1024;   // the per-token arrays hold N_pad (a multiple of 256) entries
     if (wave == 0) dma_vector(a.coefA + t0, tok_bytes, vec_lds, 1024, lane);
@@ -269,7 +360,8 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
     // (same page) with a masked row
     if (HAS_BIAS && wave == 4)
       dma_vector(reinterpret_cast<const T*>(a.bias) + v0, ((uint32_t)max(min(a.V - v0, 256), 0) * E + 3u) & ~3u,
-                 vec_lds + 4096, 256 * E, lane);
+                 vec_lds + kBiasAt, 256 * E, lane);
+    if (ENTROPY && wave == 5) dma_vector(a.coefE + t0, tok_bytes, vec_lds + 4096, 1024, lane);
   }
 
   Acc acc[kMI][kNI];
@@ -290,13 +382,14 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
   const float s2 = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale;   // scale folded into the exp argument
   const float k1 = -a.two_cap * kLog2e;
   const float cmul = (SOFTCAP ? 4.0f * a.scale : a.scale) * a.dscale[0];
-  float cAs[kNI], cBs[kNI], k0[kNI];
+  float cAs[kNI], cBs[kNI], cEs[kNI], k0[kNI];
   int rel[kNI];
 #pragma unroll
   for (int ni = 0; ni < kNI; ni++) {
     const int tl = wn * kWaveN + acc_col(ni, lane);
     cAs[ni] = reinterpret_cast<const float*>(vec_lds)[tl] * cmul;
     cBs[ni] = reinterpret_cast<const float*>(vec_lds + 1024)[tl] * cmul;
+    if constexpr (ENTROPY) cEs[ni] = reinterpret_cast<const float*>(vec_lds + 4096)[tl] * cmul;
     const float lL = reinterpret_cast<const float*>(vec_lds + 2048)[tl];
     k0[ni] = SOFTCAP ? fmaf(a.cap, kLog2e, -lL) : -lL;
     rel[ni] = reinterpret_cast<const int*>(vec_lds + 3072)[tl] - vw;
@@ -312,7 +405,7 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
   for (int mi = 0; mi < kMI; mi++) {
     float sb[4];
     if constexpr (HAS_BIAS) {
-      lds_vec4<T>(vec_lds + 4096, wm * kWaveM + acc_row(mi, 0, lane), sb);
+      lds_vec4<T>(vec_lds + kBiasAt, wm * kWaveM + acc_row(mi, 0, lane), sb);
 #pragma unroll
       for (int j = 0; j < 4; j++) sb[j] *= s2;
     }
@@ -323,14 +416,23 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
       float f[4], d[4];   // f: softcap' / 4 with the cap, else unused
 #pragma unroll
       for (int r = 0; r < 4; r++) {
-        const float v = HAS_BIAS ? fmaf(acc[mi][ni][r], s2, sb[r]) : acc[mi][ni][r] * s2;
+        float v = HAS_BIAS ? fmaf(acc[mi][ni][r], s2, sb[r]) : acc[mi][ni][r] * s2;
+        if constexpr (ENTROPY && SOFTCAP) v = fmaxf(v, kMasked);
         if constexpr (SOFTCAP) {
           const float rr = fast_rcp(fast_exp2(v) + 1.0f);
-          const float p = fast_exp2(fmaf(rr, k1, k0[ni]));
+          const float x = fmaf(rr, k1, k0[ni]);   // log2 p
+          const float p = fast_exp2(x);
           f[r] = fmaf(-rr, rr, rr);
-          d[r] = (p * cAs[ni]) * f[r];
+          if constexpr (ENTROPY) d[r] = (p * fmaf(x, cEs[ni], cAs[ni])) * f[r];
+          else d[r] = (p * cAs[ni]) * f[r];
         } else {
-          d[r] = fast_exp2(fmaf(v, kLog2e, k0[ni])) * cAs[ni];
+          const float x = fmaf(v, kLog2e, k0[ni]);
+          if constexpr (ENTROPY) {
+            const float xf = fmaxf(x, kMasked);
+            d[r] = fast_exp2(xf) * fmaf(xf, cEs[ni], cAs[ni]);
+          } else {
+            d[r] = fast_exp2(x) * cAs[ni];
+          }
         }
       }
       // the target row, where some lane of the wave holds it here
@@ -695,15 +797,17 @@ __global__ __launch_bounds__(256) void bwd_gh_reduce(const float* part, int part
 }
 
 // hidden^T [H][N_pad] (zero for t >= N): the token-contiguous copy of hidden
-// that the grad_weight contraction reads as its register operand.
+// that the grad_weight contraction reads as its register operand.  With tgt, rows
+// without a target are zero too: their D is 0, and 0 times what they hold is to be 0.
 template <typename T>
-__global__ __launch_bounds__(256) void transpose_hidden_kernel(const T* x, int N, int H, int N_pad, T* xt) {
+__global__ __launch_bounds__(256) void transpose_hidden_kernel(const T* x, int N, int H, int N_pad, T* xt,
+                                                               const int* tgt) {
   __shared__ float tile[64][65];
   const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int r = ty; r < 64; r += 4) {
     const int t = t0 + r, h = h0 + tx;
-    tile[r][tx] = (t < N && h < H) ? load_elem<T>(x, (int64_t)t * H + h) : 0.0f;
+    tile[r][tx] = (t < N && h < H && (!tgt || tgt[t] >= 0)) ? load_elem<T>(x, (int64_t)t * H + h) : 0.0f;
   }
   __syncthreads();
   for (int r = ty; r < 64; r += 4) {
@@ -755,6 +859,42 @@ void launch_prep_rows(const Plan& pl, const void* targets, const float* lse, con
   bwd_prep_kernel<<<1, 1024, 0, st>>>(pa);
 }
 
+static void launch_lp_prep(const Plan& pl, const void* targets, const float* lse, float* coefA, float* coefB,
+                           float* lseL, int* tgt, int* status, float* dscale, hipStream_t st) {
+  LpPrepArgs a;
+  a.targets = targets;
+  a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
+  a.lse = lse;
+  a.entropy = pl.lg->entropy;
+  a.grad_logps = pl.lg->grad_logps;
+  a.grad_entropy = pl.lg->grad_entropy;
+  a.N = (int)pl.N;
+  a.V = (int)pl.V;
+  a.N_pad = (int)pl.N_pad;
+  a.ignore_index = pl.ignore_index;
+  a.coefA = coefA;
+  a.coefB = coefB;
+  a.coefE = pl.lg->coefE;
+  a.lseL = lseL;
+  a.tgt = tgt;
+  a.status = status;
+  a.dscale = dscale;
+  a.f16_d = pl.dtype == FLCE_F16;
+  a.abs_scale = fabsf(pl.scale);
+  lp_prep_kernel<<<1, 1024, 0, st>>>(a);
+}
+
+template <typename T, bool ENTROPY>
+static void launch_dlogits(const Plan& pl, const DlogitsArgs& d, int nwg, hipStream_t st) {
+  if (pl.has_bias) {
+    if (pl.cap > 0) bwd_dlogits_kernel<T, true, true, ENTROPY><<<nwg, kThreads, 0, st>>>(d);
+    else bwd_dlogits_kernel<T, true, false, ENTROPY><<<nwg, kThreads, 0, st>>>(d);
+  } else {
+    if (pl.cap > 0) bwd_dlogits_kernel<T, false, true, ENTROPY><<<nwg, kThreads, 0, st>>>(d);
+    else bwd_dlogits_kernel<T, false, false, ENTROPY><<<nwg, kThreads, 0, st>>>(d);
+  }
+}
+
 template <typename T>
 static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const void* weight,
                                     const void* bias, const void* targets, const float* lse,
@@ -768,11 +908,15 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
   float* gb_part = reinterpret_cast<float*>(ws + pl.b_gbpart);
 
   float* dscale = reinterpret_cast<float*>(ws + kDscaleOffset);
-  launch_prep_rows(pl, targets, lse, grad_loss, coefA, coefB, lseL, tgt, reinterpret_cast<int*>(ws), dscale, 0,
-                   pl.N_pad, st);
+  if (pl.lg)
+    launch_lp_prep(pl, targets, lse, coefA, coefB, lseL, tgt, reinterpret_cast<int*>(ws), dscale, st);
+  else
+    launch_prep_rows(pl, targets, lse, grad_loss, coefA, coefB, lseL, tgt, reinterpret_cast<int*>(ws), dscale, 0,
+                     pl.N_pad, st);
 
   T* hiddenT = reinterpret_cast<T*>(ws + pl.b_xt);
-  if (pl.N > 0) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, (int)pl.N_pad, hiddenT, st);
+  if (pl.N > 0) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, (int)pl.N_pad, hiddenT, st,
+                                         pl.lg ? tgt : nullptr);
   const bool gh_f32 = pl.dtype == FLCE_F32;
   float* accb = gh_f32 ? reinterpret_cast<float*>(grad_hidden) : reinterpret_cast<float*>(ws + pl.b_ghacc);
   const int ldD = (int)pl.Vc;
@@ -798,6 +942,7 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
       d.n_tt = (int)pl.n_tt;
       d.coefA = coefA;
       d.coefB = coefB;
+      d.coefE = pl.lg ? pl.lg->coefE : nullptr;
       d.lseL = lseL;
       d.tgt = tgt;
       d.D = D;
@@ -807,13 +952,8 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
       d.dscale = dscale;
       const int nwg = n_vt_c * (int)pl.n_tt;
       time_begin(pl, st);
-      if (pl.has_bias) {
-        if (pl.cap > 0) bwd_dlogits_kernel<T, true, true><<<nwg, kThreads, 0, st>>>(d);
-        else bwd_dlogits_kernel<T, true, false><<<nwg, kThreads, 0, st>>>(d);
-      } else {
-        if (pl.cap > 0) bwd_dlogits_kernel<T, false, true><<<nwg, kThreads, 0, st>>>(d);
-        else bwd_dlogits_kernel<T, false, false><<<nwg, kThreads, 0, st>>>(d);
-      }
+      if (pl.lg) launch_dlogits<T, true>(pl, d, nwg, st);
+      else launch_dlogits<T, false>(pl, d, nwg, st);
       time_end(pl, FLCE_KERNEL_DLOGITS, st);
     }
     {
@@ -883,17 +1023,18 @@ void launch_gb_reduce(int dtype, const float* part, int n_tt, int ld, int V, voi
 }
 
 template <typename T>
-static void launch_transpose_t(const void* hidden, int N, int H, int N_pad, void* hiddenT, hipStream_t st) {
+static void launch_transpose_t(const void* hidden, int N, int H, int N_pad, void* hiddenT, const int* tgt,
+                               hipStream_t st) {
   dim3 grid((unsigned)(N_pad / 64), (unsigned)((H + 63) / 64));
   transpose_hidden_kernel<T><<<grid, 256, 0, st>>>(reinterpret_cast<const T*>(hidden), N, H, N_pad,
-                                                   reinterpret_cast<T*>(hiddenT));
+                                                   reinterpret_cast<T*>(hiddenT), tgt);
 }
 
 void launch_transpose_hidden(int dtype, const void* hidden, int N, int H, int N_pad, void* hiddenT,
-                             hipStream_t st) {
-  if (dtype == FLCE_BF16) launch_transpose_t<bf16>(hidden, N, H, N_pad, hiddenT, st);
-  else if (dtype == FLCE_F16) launch_transpose_t<f16>(hidden, N, H, N_pad, hiddenT, st);
-  else launch_transpose_t<float>(hidden, N, H, N_pad, hiddenT, st);
+                             hipStream_t st, const int* tgt) {
+  if (dtype == FLCE_BF16) launch_transpose_t<bf16>(hidden, N, H, N_pad, hiddenT, tgt, st);
+  else if (dtype == FLCE_F16) launch_transpose_t<f16>(hidden, N, H, N_pad, hiddenT, tgt, st);
+  else launch_transpose_t<float>(hidden, N, H, N_pad, hiddenT, tgt, st);
 }
 
 void launch_gw(int dtype, const GwArgs& g, hipStream_t st) {

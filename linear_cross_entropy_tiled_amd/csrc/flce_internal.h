@@ -18,6 +18,7 @@ struct Plan {
   bool tgt_i32;                  // targets are int32 (else int64)
   bool gw_accum_out;             // one-pass path: sum grad_weight over the blocks in its own dtype
   float scale, cap, z_loss;
+  const struct LogprobGrad* lg;  // backward of the log-probabilities and entropies (else of the loss)
   flce_launch_timer* timer;      // optional event pairs around the matrix-core launches (caller-owned)
 
   int64_t n_tt, n_vt, n_ht;      // 256-wide tiles over tokens, vocabulary, hidden
@@ -43,6 +44,14 @@ struct Plan {
   bool fb_gw_acc32;              // grad_weight summed over the blocks in an fp32 workspace accumulator
   size_t fb_part, fb_blk, fb_coefA, fb_coefB, fb_lseL, fb_tgt, fb_Z, fb_xt, fb_ghacc, fb_gwacc, fb_ghpart,
       fb_gbpart, fb_bytes;
+};
+
+// Upstream gradients of flce_logprobs_backward.  coefE: N_pad fp32 of workspace.
+struct LogprobGrad {
+  const float* grad_logps;       // NULL: zero
+  const float* grad_entropy;     // NULL: zero
+  const float* entropy;          // the forward's entropies (with grad_entropy)
+  float* coefE;
 };
 
 // Vocabulary splits of the forward tile kernel for n_tt token tiles: about
@@ -131,9 +140,9 @@ struct GhArgs {
   const float* dscale;   // [1]: 2^-s, undoes the factor D is stored with
 };
 
-// hiddenT[h][t] = hidden[t][h] for t < N, 0 for N <= t < N_pad.
+// hiddenT[h][t] = hidden[t][h] for t < N, 0 for N <= t < N_pad and, with tgt, where tgt[t] < 0.
 void launch_transpose_hidden(int dtype, const void* hidden, int N, int H, int N_pad, void* hiddenT,
-                             hipStream_t st);
+                             hipStream_t st, const int* tgt = nullptr);
 void launch_gw(int dtype, const GwArgs& g, hipStream_t st);
 void launch_gh(int dtype, const GhArgs& h, hipStream_t st);
 // grad_hidden K-split planning (parts, 64-row stages per part) for a chunk of
@@ -176,6 +185,11 @@ hipError_t launch_forward_backward(const Plan& pl, const void* hidden, const voi
                                    const void* targets, const float* grad_loss, float* loss, float* lse,
                                    int64_t* num_correct, float* entropy_sum, void* grad_hidden, void* grad_weight,
                                    void* grad_bias, char* ws, hipStream_t st);
+
+// Log-probabilities and entropies of the targets (flce_logprobs_forward).
+size_t logprobs_forward_bytes(const Plan& pl);
+hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weight, const void* bias,
+                           const void* targets, float* logps, float* entropy, float* lse, char* ws, hipStream_t st);
 
 hipError_t launch_scale_gradients(const Plan& pl, const float* g, void* grad_hidden, void* grad_weight,
                                   void* grad_bias, hipStream_t st);

@@ -1,0 +1,380 @@
+// Per-token log-probabilities and entropies of a linear head, without its logits:
+// the tile loop of the forward pass with an epilogue of its own, then a merge of
+// the vocabulary splits.
+//
+// Everything is kept in base 2: y = z log2(e), so that an exponential is one
+// v_exp and the running maximum, sums and target need no conversions.  Per row,
+// over the logits seen so far,
+//   m = max y,   l = sum 2^(y - m),   T = sum 2^(y - m) (y - m),
+// and at the end  log2 p_t = y_t - m - log2 l,  H = ln 2 (log2 l - T / l).
+// T is taken relative to the maximum: H = lse - sum p z would subtract two numbers
+// of the size of the logits, and a near-certain row's small entropy would be lost
+// in their rounding; log2 l and T / l both go to 0 there.  On a new maximum m' =
+// m + d, l' = l 2^-d and T' = (T - d l) 2^-d.
+#include "flce_device.h"
+#include "flce_internal.h"
+
+namespace flce {
+
+struct LpTileArgs {
+  const char* hidden;
+  const char* weight;
+  const void* bias;
+  const void* targets;
+  int tgt_i32;
+  int N, H, V;
+  int64_t ignore_index;
+  float scale, cap, two_log2e_over_cap;
+  int n_vt, S, N_pad;
+  float* part;      // [4][S][N_pad]: m, l, T, y_t
+  int* status;      // set to FLCE_OK here; lp_rows_kernel reports bad targets
+};
+
+// A row's state over some of its logits.  With nothing seen: m = kMasked, l = T = 0.
+struct LpState {
+  float m, l, T, yt;
+};
+
+__device__ __forceinline__ void lp_merge(LpState& a, const LpState& b) {
+  const float mn = fmaxf(a.m, b.m);
+  // a state without any finite logit (l = 0) may have m = -inf or kMasked: its shift
+  // is not used, so that 0 times it is no NaN
+  const float da = a.l == 0.0f ? 0.0f : a.m - mn, db = b.l == 0.0f ? 0.0f : b.m - mn;
+  const float fa = fast_exp2(da), fb = fast_exp2(db);
+  a.T = fmaf(da, a.l, a.T) * fa + fmaf(db, b.l, b.T) * fb;
+  a.l = a.l * fa + b.l * fb;
+  a.m = mn;
+  a.yt = fmaxf(a.yt, b.yt);
+}
+
+template <typename T, bool HAS_BIAS, bool SOFTCAP>
+__global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
+  constexpr int E = sizeof(T);
+  const int L = xcd_logical_id(blockIdx.x, gridDim.x);
+  // the tile order of fwd_tiles_kernel: 4 token tiles x 8 splits on an XCD at a time
+  const int n_tt = (int)gridDim.x / a.S;
+  const bool grouped = a.S % 8 == 0 && n_tt % 4 == 0 && gridDim.x >= 256;
+  int tt, s;
+  if (grouped) {
+    grouped_tile(L, n_tt, a.S, 4, tt, s);
+  } else {
+    tt = L / a.S;
+    s = L % a.S;
+  }
+  const int vt_begin = (int)((int64_t)s * a.n_vt / a.S);
+  const int vt_end = (int)((int64_t)(s + 1) * a.n_vt / a.S);
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const int t0 = tt * 256;
+  if (blockIdx.x == 0 && tid == 0) a.status[0] = FLCE_OK;
+
+  // m and l in registers, T, the target's logit and the targets in LDS, where they
+  // wait out the main loop
+  static __shared__ float st_T[kWaves][kNI][64], st_yt[kWaves][kNI][64];
+  static __shared__ int tile_tgt[256];
+  float st_m[kNI], st_l[kNI];
+#pragma unroll
+  for (int ni = 0; ni < kNI; ni++) {
+    st_m[ni] = kMasked;
+    st_l[ni] = 0.0f;
+    st_T[wave][ni][lane] = 0.0f;
+    st_yt[wave][ni][lane] = -INFINITY;
+  }
+  if (tid < 256) {   // visible to all waves after the main loop's first barrier
+    const int t = t0 + tid;
+    const int64_t tv = t < a.N ? load_target(a.targets, t, a.tgt_i32) : a.ignore_index;
+    tile_tgt[tid] = (tv != a.ignore_index && tv >= 0 && tv < a.V) ? (int)tv : -1;
+  }
+
+  const uint32_t ld = (uint32_t)a.H * E;
+  OperandDesc db;     // hidden rows of this token tile
+  db.base = a.hidden + (size_t)t0 * ld;
+  db.ld_bytes = ld;
+  db.nrec = (uint32_t)min(a.N - t0, 256) * ld;
+  db.cols_valid = 0;
+  db.k_bytes = a.H * E;
+  const int KT = (a.H * E + kBKB - 1) / kBKB;
+
+  const int win = min(32, max(1, (int)gridDim.x / 8));
+  L2Share sh;
+  if (grouped) {
+    sh.a_n = 4;
+    sh.a_rank = tt & 3;
+    sh.b_n = 8;
+    sh.b_rank = s & 7;
+  } else {
+    sh.b_n = min(a.S, win);
+    sh.b_rank = s % sh.b_n;
+    sh.a_n = a.S <= win ? win / a.S : 1;
+    sh.a_rank = tt % sh.a_n;
+    if (sh.a_n < 2) sh.a_n = 0;
+    if (sh.b_n < 2) sh.b_n = 0;
+  }
+
+  // two buffers, by tile parity (see fwd_tiles_kernel)
+  static __shared__ __attribute__((aligned(16))) char bias_lds[2][256 * sizeof(T)];
+
+  // the accumulator times s_u is y, or with the cap 2 v log2(e) / cap, from which
+  // r = 1 / (2^u + 1) and y = cap log2(e) (1 - 2 r)
+  const float s_u = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e;
+
+  Acc acc[kMI][kNI];
+  for (int vt = vt_begin; vt < vt_end; ++vt) {
+    const int v0 = vt * 256;
+    const char* bias_tile = bias_lds[(vt - vt_begin) & 1];
+    if (HAS_BIAS && wave == 0)
+      dma_vector(reinterpret_cast<const T*>(a.bias) + v0, ((uint32_t)min(a.V - v0, 256) * E + 3u) & ~3u,
+                 bias_lds[(vt - vt_begin) & 1], 256 * E, lane);
+    OperandDesc da;     // weight rows of this vocabulary tile
+    da.base = a.weight + (size_t)v0 * ld;
+    da.ld_bytes = ld;
+    da.nrec = (uint32_t)min(a.V - v0, 256) * ld;
+    da.cols_valid = 0;
+    da.k_bytes = a.H * E;
+    zero_acc(acc);
+    tile_mainloop<T, true, true>(da, db, KT, sh, acc);
+
+    // per token column: pass 1 turns the accumulator into u and takes the maximum
+    // over the rows below V, pass 2 adds 2^x and x 2^x, x = y - m <= 0
+    const int vw = v0 + wm * kWaveM;
+    const int n_valid = a.V - vw;
+    const bool ragged = n_valid < kWaveM;
+    const int lane_row = acc_row(0, 0, lane);
+    const int lim = n_valid - lane_row;   // element (mi, r) is below V iff 16 mi + r < lim
+#pragma unroll
+    for (int ni = 0; ni < kNI; ni++) {
+      float mu = kMasked;
+#pragma unroll
+      for (int mi = 0; mi < kMI; mi++) {
+        float sb[4];
+        if constexpr (HAS_BIAS) {
+          lds_vec4<T>(bias_tile, wm * kWaveM + acc_row(mi, 0, lane), sb);
+#pragma unroll
+          for (int j = 0; j < 4; j++) sb[j] *= s_u;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+          acc[mi][ni][r] = HAS_BIAS ? fmaf(acc[mi][ni][r], s_u, sb[r]) : acc[mi][ni][r] * s_u;
+      }
+      if (ragged) {
+#pragma unroll
+        for (int mi = 0; mi < kMI; mi++)
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (16 * mi + r < lim) mu = fmaxf(mu, acc[mi][ni][r]);
+      } else {
+#pragma unroll
+        for (int mi = 0; mi < kMI; mi++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) mu = fmaxf(mu, acc[mi][ni][r]);
+      }
+      float mx = mu;   // a block without a finite logit keeps kMasked
+      if constexpr (SOFTCAP) mx = mu == kMasked ? kMasked : fmaf(-2.0f * cap2, fast_rcp(fast_exp2(mu) + 1.0f), cap2);
+      const int rel = tile_tgt[wn * kWaveN + acc_col(ni, lane)] - vw;
+      const bool hit = rel >= 0 && rel < kWaveM && ((rel >> 2) & 3) == (lane >> 4);
+      if (__builtin_amdgcn_ballot_w64(hit)) {
+        const int rel_l = rel - lane_row;
+        float ut = 0.0f;
+#pragma unroll
+        for (int mi = 0; mi < kMI; mi++)
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (16 * mi + r == rel_l) ut = acc[mi][ni][r];
+        if (hit) st_yt[wave][ni][lane] = SOFTCAP ? fmaf(-2.0f * cap2, fast_rcp(fast_exp2(ut) + 1.0f), cap2) : ut;
+      }
+      const float m_old = st_m[ni];
+      const float m_new = fmaxf(m_old, mx);
+      const float dm = st_l[ni] == 0.0f ? 0.0f : m_old - m_new;
+      const float alpha = fast_exp2(dm);
+      const float k0 = cap2 - m_new;
+      float se0 = 0.f, se1 = 0.f, sx0 = 0.f, sx1 = 0.f;
+#pragma unroll
+      for (int mi = 0; mi < kMI; mi++) {
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const float u = acc[mi][ni][r];
+          float x;
+          if constexpr (SOFTCAP) x = fmaf(fast_rcp(fast_exp2(u) + 1.0f), -2.0f * cap2, k0);
+          else x = u - m_new;
+          if (ragged && 16 * mi + r >= lim) x = kMasked;
+          const float e = fast_exp2(x);
+          // a logit of -inf has e = 0 and is to add 0, not 0 times infinity
+          const float xf = fmaxf(x, kMasked);
+          if (r & 1) {
+            se1 += e;
+            sx1 = fmaf(e, xf, sx1);
+          } else {
+            se0 += e;
+            sx0 = fmaf(e, xf, sx0);
+          }
+        }
+      }
+      st_T[wave][ni][lane] = fmaf(fmaf(dm, st_l[ni], st_T[wave][ni][lane]), alpha, sx0 + sx1);
+      st_l[ni] = fmaf(st_l[ni], alpha, se0 + se1);
+      st_m[ni] = m_new;
+    }
+  }
+
+  LpState st[kNI];
+#pragma unroll
+  for (int ni = 0; ni < kNI; ni++) {
+    st[ni].m = st_m[ni];
+    st[ni].l = st_l[ni];
+    st[ni].T = st_T[wave][ni][lane];
+    st[ni].yt = st_yt[wave][ni][lane];
+  }
+  // the four lanes of a token column hold disjoint rows
+#pragma unroll
+  for (int ni = 0; ni < kNI; ni++) {
+#pragma unroll
+    for (int x = 16; x <= 32; x <<= 1) {
+      LpState o;
+      o.m = __shfl_xor(st[ni].m, x);
+      o.l = __shfl_xor(st[ni].l, x);
+      o.T = __shfl_xor(st[ni].T, x);
+      o.yt = __shfl_xor(st[ni].yt, x);
+      lp_merge(st[ni], o);
+    }
+  }
+  // the two M waves, through LDS
+  static_assert(kWavesM == 2, "the merge below pairs two waves along M");
+  float* xs = reinterpret_cast<float*>(g_stage0);   // [wn][field][kWaveN]
+  if (wm == 1 && lane < 16) {
+#pragma unroll
+    for (int ni = 0; ni < kNI; ni++) {
+      float* p = xs + wn * 4 * kWaveN + acc_col(ni, lane);
+      p[0 * kWaveN] = st[ni].m;
+      p[1 * kWaveN] = st[ni].l;
+      p[2 * kWaveN] = st[ni].T;
+      p[3 * kWaveN] = st[ni].yt;
+    }
+  }
+  __syncthreads();
+  if (wm == 0 && lane < 16) {
+    const size_t plane = (size_t)a.S * a.N_pad;
+#pragma unroll
+    for (int ni = 0; ni < kNI; ni++) {
+      const int c = acc_col(ni, lane);
+      const float* p = xs + wn * 4 * kWaveN + c;
+      LpState o;
+      o.m = p[0 * kWaveN];
+      o.l = p[1 * kWaveN];
+      o.T = p[2 * kWaveN];
+      o.yt = p[3 * kWaveN];
+      lp_merge(st[ni], o);
+      float* out = a.part + (size_t)s * a.N_pad + t0 + wn * kWaveN + c;
+      out[0] = st[ni].m;
+      out[plane] = st[ni].l;
+      out[2 * plane] = st[ni].T;
+      out[3 * plane] = st[ni].yt;
+    }
+  }
+}
+
+// Merges each row's vocabulary splits, in order, and writes its outputs.
+struct LpRowArgs {
+  const void* targets;
+  int tgt_i32;
+  int N, V, S, N_pad;
+  int64_t ignore_index;
+  const float* part;
+  float* logps;
+  float* entropy;   // may be NULL
+  float* lse;
+  int* status;
+  int init_status;  // no tile kernel ran before (N = 0)
+};
+
+__global__ __launch_bounds__(256) void lp_rows_kernel(LpRowArgs a) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (a.init_status && i == 0) a.status[0] = FLCE_OK;
+  if (i >= a.N) return;
+  const size_t plane = (size_t)a.S * a.N_pad;
+  LpState r{kMasked, 0.0f, 0.0f, -INFINITY};
+  for (int s0 = 0; s0 < a.S; s0 += 8) {
+    LpState q[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {   // eight loads in flight; past the last split the last one, not merged
+      const float* p = a.part + (size_t)min(s0 + j, a.S - 1) * a.N_pad + i;
+      q[j].m = p[0];
+      q[j].l = p[plane];
+      q[j].T = p[2 * plane];
+      q[j].yt = p[3 * plane];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (s0 + j < a.S) lp_merge(r, q[j]);
+  }
+  const float l2 = fast_log2(r.l);
+  const int64_t t = load_target(a.targets, i, a.tgt_i32);
+  const bool in_range = t >= 0 && t < a.V, valid = t != a.ignore_index && in_range;
+  // (a row without any finite logit: l = 0, and every output is NaN or -inf)
+  a.lse[i] = (r.m + l2) * kLn2;
+  a.logps[i] = valid ? (r.yt - r.m - l2) * kLn2 : 0.0f;
+  if (a.entropy) a.entropy[i] = valid ? (l2 - r.T / r.l) * kLn2 : 0.0f;
+  if (t != a.ignore_index && !in_range) a.status[0] = FLCE_ERR_TARGET_OUT_OF_RANGE;   // every writer stores the same
+}
+
+template <typename T>
+static void launch_lp_tiles(const Plan& pl, const LpTileArgs& a, int nwg, hipStream_t st) {
+  if (pl.has_bias) {
+    if (pl.cap > 0) lp_tiles_kernel<T, true, true><<<nwg, kThreads, 0, st>>>(a);
+    else lp_tiles_kernel<T, true, false><<<nwg, kThreads, 0, st>>>(a);
+  } else {
+    if (pl.cap > 0) lp_tiles_kernel<T, false, true><<<nwg, kThreads, 0, st>>>(a);
+    else lp_tiles_kernel<T, false, false><<<nwg, kThreads, 0, st>>>(a);
+  }
+}
+
+hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weight, const void* bias,
+                           const void* targets, float* logps, float* entropy, float* lse, char* ws, hipStream_t st) {
+  float* part = reinterpret_cast<float*>(ws + kStatusBytes);
+  int* status = reinterpret_cast<int*>(ws);
+  if (pl.N > 0) {
+    LpTileArgs a;
+    a.hidden = static_cast<const char*>(hidden);
+    a.weight = static_cast<const char*>(weight);
+    a.bias = bias;
+    a.targets = targets;
+    a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
+    a.N = (int)pl.N;
+    a.H = (int)pl.H;
+    a.V = (int)pl.V;
+    a.ignore_index = pl.ignore_index;
+    a.scale = pl.scale;
+    a.cap = pl.cap;
+    a.two_log2e_over_cap = pl.cap > 0 ? 2.0f * kLog2e / pl.cap : 0.0f;
+    a.n_vt = (int)pl.n_vt;
+    a.S = pl.S;
+    a.N_pad = (int)pl.N_pad;
+    a.part = part;
+    a.status = status;
+    const int nwg = (int)pl.n_tt * pl.S;
+    if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
+    else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);
+    else launch_lp_tiles<float>(pl, a, nwg, st);
+  }
+  LpRowArgs r;
+  r.targets = targets;
+  r.tgt_i32 = pl.tgt_i32 ? 1 : 0;
+  r.N = (int)pl.N;
+  r.V = (int)pl.V;
+  r.S = pl.S;
+  r.N_pad = (int)pl.N_pad;
+  r.ignore_index = pl.ignore_index;
+  r.part = part;
+  r.logps = logps;
+  r.entropy = entropy;
+  r.lse = lse;
+  r.status = status;
+  r.init_status = pl.N == 0;
+  lp_rows_kernel<<<(unsigned)(pl.n_tt > 0 ? pl.n_tt : 1), 256, 0, st>>>(r);
+  return hipGetLastError();
+}
+
+size_t logprobs_forward_bytes(const Plan& pl) {
+  return (kStatusBytes + size_t(4) * pl.S * pl.N_pad * 4 + 255) / 256 * 256;
+}
+
+}  // namespace flce
