@@ -367,6 +367,35 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The same log-probabilities and entropies from 8-bit operands, for scorers
+ * that are not trained (a reference, the policy that sampled): half the weight
+ * bytes and twice the matrix rate of 16 bits.
+ *   z_ij = softcap(logit_scale (hidden_scale_i weight_scale_j sum_k hidden_ik weight_jk + bias_j)),
+ * the sum in int32 (exact), everything after it in fp32.  No backward.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Rows of x (rows x cols, contiguous, dtype) as 8-bit integers with a scale per
+ * row, x ~ scale q:  scale = max|x| fp32(1/127), q = rint(x fp32(1/scale)), in
+ * fp32.  Rows whose largest magnitude is below 1e-30 give scale 0 and q 0; rows
+ * that hold NaN or an infinity give scale NaN and q 0.  cols % 16 == 0; x and q
+ * 16-byte aligned.  For the weight once, for hidden states before each call.
+ */
+int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, void* q, float* scale, void* stream);
+
+/* Bytes of device workspace flce_logprobs_int8 needs.  Host only.  params as for
+ * flce_logprobs_forward, with hidden % 16 == 0 and at most 2^17; params->dtype
+ * (any valid one) and the gradient fields are not used. */
+int flce_logprobs_int8_workspace_size(const flce_params* p, size_t* bytes);
+
+/* hidden (N, H) and weight (V, H): device int8 within [-127, 127]; hidden_scale
+ * (N), weight_scale (V), bias (V, or NULL): device fp32; outputs and rows without
+ * a target as flce_logprobs_forward. */
+int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hidden_scale, const void* weight,
+                       const float* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Preference and policy losses over per-token log-probabilities (as
  * flce_logprobs_forward gives them), forward and backward.
  *

@@ -12,7 +12,8 @@ declared in ``include/flce.h``).  This module only marshals arguments:
   (``flce_chunked_linear_loss``) with a Python loss function or the built-in
   weighted squared error (``flce_weighted_mse_chunk``);
 * ``token_logprobs`` (``logprobs.py``) is a torch op for per-token log-probabilities
-  and entropies of the head (``flce_logprobs_*``);
+  and entropies of the head (``flce_logprobs_*``), ``token_logprobs_int8`` their form
+  for a frozen 8-bit head, whose weight ``quantize_int8`` makes;
 * ``preference_loss`` / ``policy_loss`` (``alignment.py``) are torch ops over
   per-token log-probabilities (``flce_preference_*``, ``flce_policy_*``).
 
@@ -55,7 +56,8 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_get_st
             "flce_forward_no_alloc", "flce_preference_workspace_size", "flce_preference_forward",
             "flce_preference_backward", "flce_policy_workspace_size", "flce_policy_forward",
             "flce_policy_backward", "flce_logprobs_workspace_size", "flce_logprobs_forward",
-            "flce_logprobs_backward")
+            "flce_logprobs_backward", "flce_quantize_int8", "flce_logprobs_int8_workspace_size",
+            "flce_logprobs_int8")
 
 FLCE_KERNEL_FORWARD_TILES = 1
 FLCE_KERNEL_DLOGITS = 2
@@ -224,6 +226,12 @@ def load(path: Optional[str] = None):
     lib.flce_logprobs_forward.restype = ctypes.c_int
     lib.flce_logprobs_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.flce_logprobs_backward.restype = ctypes.c_int
+    lib.flce_quantize_int8.argtypes = [ctypes.c_int, vp, i64, i64, vp, vp, vp]
+    lib.flce_quantize_int8.restype = ctypes.c_int
+    lib.flce_logprobs_int8_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+    lib.flce_logprobs_int8_workspace_size.restype = ctypes.c_int
+    lib.flce_logprobs_int8.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_logprobs_int8.restype = ctypes.c_int
     view, RP, LP = flce_token_view, ctypes.POINTER(flce_preference_params), ctypes.POINTER(flce_policy_params)
     lib.flce_preference_workspace_size.argtypes = [RP, ctypes.POINTER(sz)]
     lib.flce_preference_workspace_size.restype = ctypes.c_int
@@ -372,6 +380,24 @@ def flce_logprobs_backward(params, hidden, weight, bias, targets, lse, entropy, 
     return load().flce_logprobs_backward(ctypes.byref(params), hidden, weight, bias, targets, lse, entropy, grad_logps,
                                          grad_entropy, grad_hidden, grad_weight, grad_bias, workspace, workspace_bytes,
                                          stream)
+
+
+def flce_quantize_int8(dtype, x, rows, cols, q, scale, stream) -> int:
+    return load().flce_quantize_int8(dtype, x, rows, cols, q, scale, stream)
+
+
+def flce_logprobs_int8_workspace_size(params: flce_params) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_logprobs_int8_workspace_size(ctypes.byref(params), ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_logprobs_int8_workspace_size")
+    return out.value
+
+
+def flce_logprobs_int8(params, hidden, hidden_scale, weight, weight_scale, bias, targets, logps, entropy, lse, workspace,
+                       workspace_bytes, stream) -> int:
+    return load().flce_logprobs_int8(ctypes.byref(params), hidden, hidden_scale, weight, weight_scale, bias, targets,
+                                     logps, entropy, lse, workspace, workspace_bytes, stream)
 
 
 def flce_preference_workspace_size(params: flce_preference_params) -> int:
@@ -872,5 +898,5 @@ def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_ro
 
 # ----------------------------------------------------------------------------- alignment training
 
-from .logprobs import token_logprobs  # noqa: E402,F401
+from .logprobs import quantize_int8, token_logprobs, token_logprobs_int8  # noqa: E402,F401
 from .alignment import policy_loss, preference_loss  # noqa: E402,F401

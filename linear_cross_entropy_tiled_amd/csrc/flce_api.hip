@@ -457,7 +457,7 @@ int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* 
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) || !aligned16(targets))
     return FLCE_ERR_UNSUPPORTED;
   if (workspace_bytes < logprobs_forward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  const hipError_t e = launch_logprobs(pl, hidden, weight, bias, targets, logps, entropy, lse,
+  const hipError_t e = launch_logprobs(pl, hidden, weight, bias, nullptr, nullptr, targets, logps, entropy, lse,
                                        static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
@@ -486,6 +486,56 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
   pl.lg = &lg;
   const hipError_t e = launch_backward(pl, hidden, weight, bias, targets, lse, nullptr, grad_hidden, grad_weight,
                                        grad_bias, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+// The int32 sums of up to 2^17 products of magnitude at most 127^2 stay below 2^31.
+static constexpr int64_t kMaxInt8Hidden = int64_t(1) << 17;
+
+static int logprobs_int8_plan(const flce_params* p, Plan* pl) {
+  const int rc = logprobs_plan(p, pl);
+  if (rc != FLCE_OK) return rc;
+  if (pl->H % 16 != 0 || pl->H > kMaxInt8Hidden) return FLCE_ERR_UNSUPPORTED;
+  pl->int8 = true;
+  pl->esize = 1;
+  return FLCE_OK;
+}
+
+int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, void* q, float* scale, void* stream) {
+  if (!valid_dtype(dtype) || rows < 0 || cols <= 0) return FLCE_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !q || !scale)) return FLCE_ERR_INVALID_ARG;
+  if (cols % 16 != 0 || rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30) || !aligned16(x) || !aligned16(q) ||
+      (reinterpret_cast<uintptr_t>(scale) & 3) != 0)
+    return FLCE_ERR_UNSUPPORTED;
+  const hipError_t e = launch_quantize(dtype, x, rows, cols, static_cast<int8_t*>(q), scale,
+                                       static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+int flce_logprobs_int8_workspace_size(const flce_params* p, size_t* bytes) {
+  if (!bytes) return FLCE_ERR_INVALID_ARG;
+  Plan pl;
+  const int rc = logprobs_int8_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  *bytes = logprobs_forward_bytes(pl);
+  return FLCE_OK;
+}
+
+int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hidden_scale, const void* weight,
+                       const float* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  Plan pl;
+  const int rc = logprobs_int8_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  pl.has_bias = bias != nullptr;
+  if (!workspace || !weight || !weight_scale) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && (!hidden || !hidden_scale || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(weight_scale) ||
+      !aligned16(workspace) || !aligned16(targets) || (reinterpret_cast<uintptr_t>(hidden_scale) & 3) != 0)
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < logprobs_forward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = launch_logprobs(pl, hidden, weight, bias, hidden_scale, weight_scale, targets, logps, entropy,
+                                       lse, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 

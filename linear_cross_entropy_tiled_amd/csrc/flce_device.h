@@ -21,8 +21,12 @@
 // MNMAJOR fragments are read with ds_read_b64_tr_b16, which transposes
 // 16-bit elements across each group of 16 lanes.
 //
-// K order: a stage is 128 bytes of K per row (64 bf16 or fp16 / 32 fp32), eight
-// 16-byte chunks.  In sub-step s (0..1) the lanes of 16-lane group g (lane / 16)
+// 8-bit integer operands (KMAJOR only) run the same loop on the same bytes:
+// v_mfma_i32_16x16x64_i8 takes 16 bytes of K per lane, as the 16-bit
+// instructions do, with int32 sums in the accumulator's registers.
+//
+// K order: a stage is 128 bytes of K per row (128 int8 / 64 bf16 or fp16 / 32
+// fp32), eight 16-byte chunks.  In sub-step s (0..1) the lanes of 16-lane group g (lane / 16)
 // contract chunk 4s + g.  Any order is correct as long as both operands use the
 // same one.
 #pragma once
@@ -300,6 +304,7 @@ template <typename V8> struct Frag16K {
 };
 template <> struct Frag<bf16, true> : Frag16K<bf16x8> {};
 template <> struct Frag<f16, true> : Frag16K<f16x8> {};
+template <> struct Frag<int8_t, true> : Frag16K<i32x4> {};
 
 // MNMAJOR 16-bit rows are 512 B (256 elements); 8-byte unit u of row r sits at
 // unit u ^ ((r & 3) << 3) ^ (((r >> 3) & 1) << 2).  ds_read_b64_tr_b16 gives
@@ -359,6 +364,9 @@ __device__ __forceinline__ void mma(Acc& c, const bf16x8& a, const bf16x8& b) {
 __device__ __forceinline__ void mma(Acc& c, const f16x8& a, const f16x8& b) {
   c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ void mma(Acc& c, const i32x4& a, const i32x4& b) {
+  c = __builtin_bit_cast(Acc, __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, __builtin_bit_cast(i32x4, c), 0, 0, 0));
+}
 __device__ __forceinline__ void mma(Acc& c, const f32x4& a, const f32x4& b) {
 #pragma unroll
   for (int j = 0; j < 4; j++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
@@ -408,13 +416,13 @@ struct L2Share {
 constexpr int kPrefetchAhead = 3;
 static __shared__ __attribute__((aligned(256))) char g_prefetch_sink[256];
 
-// Issues this wave's share of the prefetch of stage kt (16-bit types only); returns
+// Issues this wave's share of the prefetch of stage kt (not for fp32); returns
 // whether the wave issued a load (wave-uniform).
 template <typename T, bool A_KMAJOR, bool B_KMAJOR>
 __device__ __forceinline__ bool prefetch_stage(const OperandLoader<T, A_KMAJOR>& la,
                                                const OperandLoader<T, B_KMAJOR>& lb, const L2Share& sh,
                                                int kt, int wave, int lane) {
-  if constexpr (sizeof(T) != 2) {
+  if constexpr (sizeof(T) > 2) {
     return false;
   } else {
     // the loading waves prefetch too: waves 0-1 take A's lines, waves 2-3

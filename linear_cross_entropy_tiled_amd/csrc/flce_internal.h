@@ -14,6 +14,7 @@ struct Plan {
   int64_t N, H, V, ignore_index;
   int dtype, gw_dtype, reduction;
   bool has_bias;
+  bool int8;                     // hidden and weight are 8-bit (log-probabilities only)
   bool accum_gw, accum_gb;       // backward adds into grad_weight / grad_bias
   bool tgt_i32;                  // targets are int32 (else int64)
   bool gw_accum_out;             // one-pass path: sum grad_weight over the blocks in its own dtype
@@ -188,8 +189,12 @@ hipError_t launch_forward_backward(const Plan& pl, const void* hidden, const voi
 
 // Log-probabilities and entropies of the targets (flce_logprobs_forward).
 size_t logprobs_forward_bytes(const Plan& pl);
+// pl.int8: 8-bit operands with their scales, bias in fp32.
 hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weight, const void* bias,
-                           const void* targets, float* logps, float* entropy, float* lse, char* ws, hipStream_t st);
+                           const float* hidden_scale, const float* weight_scale, const void* targets, float* logps,
+                           float* entropy, float* lse, char* ws, hipStream_t st);
+hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                           hipStream_t st);
 
 hipError_t launch_scale_gradients(const Plan& pl, const float* g, void* grad_hidden, void* grad_weight,
                                   void* grad_bias, hipStream_t st);

@@ -11,6 +11,10 @@
 // of the size of the logits, and a near-certain row's small entropy would be lost
 // in their rounding; log2 l and T / l both go to 0 there.  On a new maximum m' =
 // m + d, l' = l 2^-d and T' = (T - d l) 2^-d.
+//
+// With 8-bit operands (a frozen scorer's head) the accumulator is the exact int32
+// product; one multiplication by the vocabulary row's scale and one by the token's
+// turn it into the logit, and the rest is the same.
 #include "flce_device.h"
 #include "flce_internal.h"
 
@@ -19,7 +23,9 @@ namespace flce {
 struct LpTileArgs {
   const char* hidden;
   const char* weight;
-  const void* bias;
+  const void* bias;           // the operands' type; fp32 for int8
+  const float* hidden_scale;  // int8
+  const float* weight_scale;  // int8
   const void* targets;
   int tgt_i32;
   int N, H, V;
@@ -47,9 +53,15 @@ __device__ __forceinline__ void lp_merge(LpState& a, const LpState& b) {
   a.yt = fmaxf(a.yt, b.yt);
 }
 
+template <typename T> struct BiasOf { typedef T type; };
+template <> struct BiasOf<int8_t> { typedef float type; };
+
 template <typename T, bool HAS_BIAS, bool SOFTCAP>
 __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   constexpr int E = sizeof(T);
+  constexpr bool I8 = E == 1;
+  typedef typename BiasOf<T>::type B;
+  constexpr int BE = sizeof(B);
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   // the tile order of fwd_tiles_kernel: 4 token tiles x 8 splits on an XCD at a time
   const int n_tt = (int)gridDim.x / a.S;
@@ -72,6 +84,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   // wait out the main loop
   static __shared__ float st_T[kWaves][kNI][64], st_yt[kWaves][kNI][64];
   static __shared__ int tile_tgt[256];
+  static __shared__ float tile_scale[I8 ? 256 : 1];   // the tokens' scales
   float st_m[kNI], st_l[kNI];
 #pragma unroll
   for (int ni = 0; ni < kNI; ni++) {
@@ -84,6 +97,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
     const int t = t0 + tid;
     const int64_t tv = t < a.N ? load_target(a.targets, t, a.tgt_i32) : a.ignore_index;
     tile_tgt[tid] = (tv != a.ignore_index && tv >= 0 && tv < a.V) ? (int)tv : -1;
+    if (I8) tile_scale[tid] = t < a.N ? a.hidden_scale[t] : 0.0f;
   }
 
   const uint32_t ld = (uint32_t)a.H * E;
@@ -112,7 +126,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   }
 
   // two buffers, by tile parity (see fwd_tiles_kernel)
-  static __shared__ __attribute__((aligned(16))) char bias_lds[2][256 * sizeof(T)];
+  static __shared__ __attribute__((aligned(16))) char bias_lds[2][256 * BE], wscale_lds[2][I8 ? 1024 : 16];
 
   // the accumulator times s_u is y, or with the cap 2 v log2(e) / cap, from which
   // r = 1 / (2^u + 1) and y = cap log2(e) (1 - 2 r)
@@ -124,8 +138,10 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
     const int v0 = vt * 256;
     const char* bias_tile = bias_lds[(vt - vt_begin) & 1];
     if (HAS_BIAS && wave == 0)
-      dma_vector(reinterpret_cast<const T*>(a.bias) + v0, ((uint32_t)min(a.V - v0, 256) * E + 3u) & ~3u,
-                 bias_lds[(vt - vt_begin) & 1], 256 * E, lane);
+      dma_vector(reinterpret_cast<const B*>(a.bias) + v0, ((uint32_t)min(a.V - v0, 256) * BE + 3u) & ~3u,
+                 bias_lds[(vt - vt_begin) & 1], 256 * BE, lane);
+    if (I8 && wave == 1)
+      dma_vector(a.weight_scale + v0, (uint32_t)min(a.V - v0, 256) * 4, wscale_lds[(vt - vt_begin) & 1], 1024, lane);
     OperandDesc da;     // weight rows of this vocabulary tile
     da.base = a.weight + (size_t)v0 * ld;
     da.ld_bytes = ld;
@@ -142,20 +158,32 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
     const bool ragged = n_valid < kWaveM;
     const int lane_row = acc_row(0, 0, lane);
     const int lim = n_valid - lane_row;   // element (mi, r) is below V iff 16 mi + r < lim
+    if constexpr (I8) {
+#pragma unroll
+      for (int mi = 0; mi < kMI; mi++) {
+        const f32x4 ws =
+            *reinterpret_cast<const f32x4*>(wscale_lds[(vt - vt_begin) & 1] + 4 * (wm * kWaveM + acc_row(mi, 0, lane)));
+#pragma unroll
+        for (int ni = 0; ni < kNI; ni++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) acc[mi][ni][r] = (float)__builtin_bit_cast(int, (float)acc[mi][ni][r]) * ws[r];
+      }
+    }
 #pragma unroll
     for (int ni = 0; ni < kNI; ni++) {
+      const float s_a = I8 ? s_u * tile_scale[wn * kWaveN + acc_col(ni, lane)] : s_u;
       float mu = kMasked;
 #pragma unroll
       for (int mi = 0; mi < kMI; mi++) {
         float sb[4];
         if constexpr (HAS_BIAS) {
-          lds_vec4<T>(bias_tile, wm * kWaveM + acc_row(mi, 0, lane), sb);
+          lds_vec4<B>(bias_tile, wm * kWaveM + acc_row(mi, 0, lane), sb);
 #pragma unroll
           for (int j = 0; j < 4; j++) sb[j] *= s_u;
         }
 #pragma unroll
         for (int r = 0; r < 4; r++)
-          acc[mi][ni][r] = HAS_BIAS ? fmaf(acc[mi][ni][r], s_u, sb[r]) : acc[mi][ni][r] * s_u;
+          acc[mi][ni][r] = HAS_BIAS ? fmaf(acc[mi][ni][r], s_a, sb[r]) : acc[mi][ni][r] * s_a;
       }
       if (ragged) {
 #pragma unroll
@@ -327,8 +355,71 @@ static void launch_lp_tiles(const Plan& pl, const LpTileArgs& a, int nwg, hipStr
   }
 }
 
+// ---------------------------------------------------------------------------
+// Rows as 8-bit integers: s = max|x| / 127 and q = rint(x / s), in fp32 as
+// s = max|x| * fp32(1/127), q = rint(x * fp32(1/s)), so that every implementation
+// of the definition gives the same integers.  A row that is (nearly) all zero has
+// s = 0 and q = 0; a row that holds NaN or an infinity has s = NaN and q = 0.  One
+// workgroup a row; the second pass reads the row from cache.
+// ---------------------------------------------------------------------------
+constexpr float kQuantTiny = 1e-30f;   // 1 / s stays finite above it
+
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t cols, int8_t* q, float* scale) {
+  __shared__ float lds[4];
+  const int tid = threadIdx.x;
+  const T* row = x + (int64_t)blockIdx.x * cols;
+  int8_t* out = q + (int64_t)blockIdx.x * cols;
+  constexpr int kVec = 16 / sizeof(T);
+  typedef T TV __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef int8_t QV __attribute__((ext_vector_type(16 / sizeof(T))));
+  const int64_t n = cols / kVec;
+  float top = 0.0f;
+  bool bad = false;
+  for (int64_t i = tid; i < n; i += 256) {
+    const TV v = reinterpret_cast<const TV*>(row)[i];
+#pragma unroll
+    for (int j = 0; j < kVec; j++) {
+      const float f = fabsf((float)v[j]);
+      top = fmaxf(top, f);
+      bad = bad || !(f < INFINITY);
+    }
+  }
+  if (bad) top = INFINITY;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if ((tid & 63) == 0) lds[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+  const bool zero = !(top >= kQuantTiny && top < INFINITY);
+  const float s = top * (1.0f / 127.0f), r = zero ? 0.0f : 1.0f / s;
+  if (tid == 0) scale[blockIdx.x] = top == INFINITY ? __builtin_nanf("") : (zero ? 0.0f : s);
+  for (int64_t i = tid; i < n; i += 256) {
+    const TV v = reinterpret_cast<const TV*>(row)[i];
+    QV o;
+#pragma unroll
+    for (int j = 0; j < kVec; j++) {
+      const float f = zero ? 0.0f : rintf((float)v[j] * r);
+      o[j] = (int8_t)(int)fminf(fmaxf(f, -127.0f), 127.0f);
+    }
+    reinterpret_cast<QV*>(out)[i] = o;
+  }
+}
+
+hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                           hipStream_t st) {
+  if (rows > 0) {
+    const unsigned g = (unsigned)rows;
+    if (dtype == FLCE_BF16) quantize_rows_kernel<bf16><<<g, 256, 0, st>>>(static_cast<const bf16*>(x), cols, q, scale);
+    else if (dtype == FLCE_F16) quantize_rows_kernel<f16><<<g, 256, 0, st>>>(static_cast<const f16*>(x), cols, q, scale);
+    else quantize_rows_kernel<float><<<g, 256, 0, st>>>(static_cast<const float*>(x), cols, q, scale);
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weight, const void* bias,
-                           const void* targets, float* logps, float* entropy, float* lse, char* ws, hipStream_t st) {
+                           const float* hidden_scale, const float* weight_scale, const void* targets, float* logps,
+                           float* entropy, float* lse, char* ws, hipStream_t st) {
   float* part = reinterpret_cast<float*>(ws + kStatusBytes);
   int* status = reinterpret_cast<int*>(ws);
   if (pl.N > 0) {
@@ -336,6 +427,8 @@ hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weigh
     a.hidden = static_cast<const char*>(hidden);
     a.weight = static_cast<const char*>(weight);
     a.bias = bias;
+    a.hidden_scale = hidden_scale;
+    a.weight_scale = weight_scale;
     a.targets = targets;
     a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
     a.N = (int)pl.N;
@@ -351,7 +444,8 @@ hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weigh
     a.part = part;
     a.status = status;
     const int nwg = (int)pl.n_tt * pl.S;
-    if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
+    if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
+    else if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
     else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);
     else launch_lp_tiles<float>(pl, a, nwg, st);
   }

@@ -6,8 +6,9 @@ import contextlib
 import functools
 from typing import Optional
 
-from . import (FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError, _ptr, _stream_handle, _targets_int32,
-               _validate, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_workspace_size, make_params)
+from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError, _dtype_name, _ptr, _stream_handle,
+               _targets_int32, _validate, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_int8,
+               flce_logprobs_int8_workspace_size, flce_logprobs_workspace_size, flce_quantize_int8, make_params)
 
 
 def on_device(device):
@@ -90,4 +91,97 @@ def token_logprobs(hidden, weight, targets, bias=None, *, logit_scale: float = 1
                     softcap=softcap, ignore_index=ignore_index, reduction="none",
                     targets_int32=_targets_int32(targets), vocab_chunk=vocab_chunk)
     logps, entropy = _function().apply(hidden, weight, bias, targets, p)
+    return (logps, entropy) if return_entropy else logps
+
+
+# ----------------------------------------------------------------------------- 8-bit scoring
+
+def _quantize(x):
+    import torch
+    dev = x.device
+    with on_device(dev):
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        scale = torch.empty(x.shape[0], dtype=torch.float32, device=dev)
+        raise_for(flce_quantize_int8(DTYPES[_dtype_name(x)], _ptr(x), x.shape[0], x.shape[1], _ptr(q), _ptr(scale),
+                                     _stream_handle(dev)), "flce_quantize_int8")
+    return q, scale
+
+
+def quantize_int8(x):
+    """Rows of x (R, H) as 8-bit integers: (q int8 (R, H), scale fp32 (R,)), x ~ scale[:, None] * q, with
+    scale = max|row| / 127.  For a weight (V, H) once, when a scorer is loaded.  H must be a multiple of 16.
+    All-zero rows give scale 0, rows with NaN or infinities scale NaN."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    _dtype_name(x)
+    if x.shape[1] == 0 or x.shape[1] % 16:
+        raise ValueError(f"rows must be a multiple of 16 long, got {x.shape[1]}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if x.device.type != "cuda":
+        raise ValueError(f"x must be on a GPU, not {x.device}")
+    return _quantize(x.detach())
+
+
+def _check_int8(hidden, weight, weight_scale, targets, bias, hidden_scale):
+    import torch
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError(f"hidden and weight must be 2-D, got {tuple(hidden.shape)} and {tuple(weight.shape)}")
+    n, h = hidden.shape
+    v = weight.shape[0]
+    if weight.dtype != torch.int8:
+        raise TypeError(f"weight must be int8 (quantize_int8), not {weight.dtype}")
+    if hidden_scale is None:
+        _dtype_name(hidden)
+    elif hidden.dtype != torch.int8:
+        raise TypeError(f"hidden must be int8 with hidden_scale, not {hidden.dtype}")
+    if weight.shape[1] != h:
+        raise ValueError(f"weight has {weight.shape[1]} columns, hidden has {h}")
+    if h == 0 or h % 16:
+        raise ValueError(f"hidden size must be a multiple of 16, got {h}")
+    _targets_int32(targets)
+    if targets.dim() != 1 or targets.shape[0] != n:
+        raise ValueError(f"targets must have shape ({n},), got {tuple(targets.shape)}")
+    vectors = [("weight_scale", weight_scale, v), ("bias", bias, v), ("hidden_scale", hidden_scale, n)]
+    for name, t, size in vectors:
+        if t is None:
+            continue
+        if t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32, not {t.dtype}")
+        if t.dim() != 1 or t.shape[0] != size:
+            raise ValueError(f"{name} must have shape ({size},), got {tuple(t.shape)}")
+    named = [("hidden", hidden), ("weight", weight), ("targets", targets), *((k, t) for k, t, _ in vectors)]
+    for name, t in named:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t in named:
+        if t is not None and (t.device.type != "cuda" or t.device != hidden.device):
+            raise ValueError(f"{name} must be on hidden's GPU ({hidden.device}), not {t.device}")
+    if torch.is_grad_enabled():
+        for name, t in named:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"8-bit scores have no gradient: detach {name}, or use token_logprobs")
+
+
+def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
+                        logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
+                        return_entropy: bool = False):
+    """``token_logprobs`` of a frozen head held in 8 bits: weight int8 (V, H) and weight_scale fp32 (V,), from
+    ``quantize_int8``.  hidden is fp32, bf16 or fp16 and is quantized here, token by token, or is int8 with its
+    ``hidden_scale`` (N,).  The products are summed exactly, in int32.  bias (V,) is fp32.  No gradients."""
+    import torch
+    _check_int8(hidden, weight, weight_scale, targets, bias, hidden_scale)
+    n, h = hidden.shape
+    p = make_params(n, h, weight.shape[0], logit_scale=logit_scale, softcap=softcap, ignore_index=ignore_index,
+                    reduction="none", targets_int32=_targets_int32(targets))
+    dev = hidden.device
+    with on_device(dev):
+        ws_bytes = flce_logprobs_int8_workspace_size(p)
+        if hidden_scale is None:
+            hidden, hidden_scale = _quantize(hidden)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        logps, entropy, lse = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(3))
+        raise_for(flce_logprobs_int8(p, _ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale), _ptr(bias),
+                                     _ptr(targets), _ptr(logps), _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes,
+                                     _stream_handle(dev)), "flce_logprobs_int8")
     return (logps, entropy) if return_entropy else logps
