@@ -25,7 +25,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libflce.so")
 SOURCES = ["flce_api.hip", "flce_forward.hip", "flce_backward.hip", "flce_chunked.hip", "flce_fused.hip",
-           "flce_noalloc.hip", "flce_logprobs.hip",
+           "flce_noalloc.hip", "flce_logprobs.hip", "flce_small.hip",
            "flce_align.hip", "flce_align_api.hip"]
 ARCH = "gfx950"
 

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "flce_internal.h"
+#include "flce_logprobs.h"
 
 namespace flce {
 
@@ -280,6 +281,68 @@ int plan_forward_backward(Plan* pl, int64_t block_rows) {
   return FLCE_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Log-probabilities: large (256 x 256) or small (64 x 64, 64 x 16) tiles.  A kernel's
+// time is about its rounds of tiles over the CUs times a tile's work over the rate that
+// its tiles reach; the small tiles' rate is the share below of the large ones'.
+// ---------------------------------------------------------------------------
+static double small_rate(const Plan& P) { return P.int8 ? 0.35 : (P.dtype == FLCE_F32 ? 0.8 : 0.4); }
+
+static bool small_is_faster(const Plan& P, int64_t tiles256, int64_t tiles64, double k256, double k64) {
+  const double big = (double)((tiles256 + 255) / 256) * 65536.0 * k256;
+  const double small = (double)((tiles64 + 255) / 256) * 4096.0 * k64 / small_rate(P);
+  return small < big;
+}
+
+void plan_logprobs(const Plan& P, LpPlan* out) {
+  LpPlan& L = *out;
+  memset(&L, 0, sizeof(L));
+  const int64_t n64 = (P.N + 63) / 64, v64 = (P.V + 63) / 64, h64 = (P.H + 63) / 64;
+  const int64_t wg_target = 3 * kTargetWorkgroups;   // small workgroups that share the chip
+  if (P.N <= 16) L.bn = 16;
+  else if (small_is_faster(P, P.n_tt * P.n_vt, n64 * v64, 1.0, 1.0)) L.bn = 64;
+  if (L.bn) {
+    L.n_tt = (int)((P.N + L.bn - 1) / L.bn);
+    int64_t S = L.n_tt > 0 ? wg_target / L.n_tt : 1;
+    if (S < 1) S = 1;
+    if (S > v64) S = v64;
+    L.S = (int)S;
+    L.N_pad = L.n_tt * L.bn;
+  } else {
+    L.n_tt = (int)P.n_tt;
+    L.S = P.S;
+    L.N_pad = (int)P.N_pad;
+  }
+  L.f_bytes = align_up(kStatusBytes + size_t(4) * L.S * L.N_pad * 4, 256);
+
+  L.n64 = (int)n64;
+  L.N64 = (int)(n64 * 64);
+  const int64_t vc64 = P.Vc / 64, vc256 = P.Vc / 256;
+  L.d_small = P.N > 0 && small_is_faster(P, P.n_tt * vc256, n64 * vc64, 1.0, 1.0);
+  L.gw_small = small_is_faster(P, P.n_ht * vc256, h64 * vc64, 1.0, 1.0);
+  L.K_pad = L.d_small ? L.N64 : (int)P.N_pad;
+  // grad_hidden: split the vocabulary until the tiles fill the chip, at least 8 stages to a part
+  const int64_t stages = P.Vc * P.esize / 128, tiles = n64 * h64;
+  int64_t parts = tiles > 0 ? wg_target / tiles : 1;
+  if (parts > stages / kMinStagesPerPart) parts = stages / kMinStagesPerPart;
+  const size_t per_part = size_t(P.N) * P.H * 4;
+  if (per_part > 0 && parts > (int64_t)(kGhPartBudget / per_part)) parts = (int64_t)(kGhPartBudget / per_part);
+  if (parts < 1) parts = 1;
+  const int64_t kt = (stages + parts - 1) / parts;
+  L.gh_kt = (int)kt;
+  L.gh_parts = (int)((stages + kt - 1) / kt);
+  L.gh_small = P.N > 0 && small_is_faster(P, P.n_ht * P.n_tt * P.gh_parts, tiles * L.gh_parts,
+                                          (double)P.gh_kt_per_part, (double)kt);
+  size_t o = P.b_bytes;
+  L.b_coefE = o;
+  o = align_up(o + size_t(P.N_pad) * 4, 256);
+  L.b_gbpart = o;
+  if (L.d_small) o = align_up(o + size_t(n64) * P.V_pad * 4, 256);
+  L.b_ghpart = o;
+  if (L.gh_small && L.gh_parts > 1) o = align_up(o + size_t(L.gh_parts) * per_part, 256);
+  L.b_bytes = o;
+}
+
 }  // namespace flce
 
 using namespace flce;
@@ -424,23 +487,32 @@ int flce_scale_gradients(const flce_params* p, const float* g, void* grad_hidden
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 
+// The int32 sums of up to 2^17 products of magnitude at most 127^2 stay below 2^31.
+static constexpr int64_t kMaxInt8Hidden = int64_t(1) << 17;
+
 // The log-probability entry points take the loss's parameters, of which the
 // reduction and the z-loss have no meaning there.
-static int logprobs_plan(const flce_params* p, Plan* pl) {
+static int logprobs_plan(const flce_params* p, bool int8, Plan* pl, LpPlan* lp) {
   const int rc = make_plan(p, pl);
   if (rc != FLCE_OK) return rc;
-  return pl->reduction == FLCE_REDUCTION_NONE && pl->z_loss == 0.0f ? FLCE_OK : FLCE_ERR_INVALID_ARG;
+  if (pl->reduction != FLCE_REDUCTION_NONE || pl->z_loss != 0.0f) return FLCE_ERR_INVALID_ARG;
+  if (int8) {
+    if (pl->H % 16 != 0 || pl->H > kMaxInt8Hidden) return FLCE_ERR_UNSUPPORTED;
+    pl->int8 = true;
+    pl->esize = 1;
+  }
+  plan_logprobs(*pl, lp);
+  return FLCE_OK;
 }
-
-static size_t logprobs_backward_bytes(const Plan& pl) { return align_up(pl.b_bytes + size_t(pl.N_pad) * 4, 256); }
 
 int flce_logprobs_workspace_size(const flce_params* p, int pass, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   Plan pl;
-  const int rc = logprobs_plan(p, &pl);
+  LpPlan lp;
+  const int rc = logprobs_plan(p, false, &pl, &lp);
   if (rc != FLCE_OK) return rc;
-  if (pass == FLCE_PASS_FORWARD) *bytes = logprobs_forward_bytes(pl);
-  else if (pass == FLCE_PASS_BACKWARD) *bytes = logprobs_backward_bytes(pl);
+  if (pass == FLCE_PASS_FORWARD) *bytes = lp.f_bytes;
+  else if (pass == FLCE_PASS_BACKWARD) *bytes = lp.b_bytes;
   else return FLCE_ERR_INVALID_ARG;
   return FLCE_OK;
 }
@@ -449,15 +521,16 @@ int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* 
                           const void* targets, float* logps, float* entropy, float* lse, void* workspace,
                           size_t workspace_bytes, void* stream) {
   Plan pl;
-  const int rc = logprobs_plan(p, &pl);
+  LpPlan lp;
+  const int rc = logprobs_plan(p, false, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!workspace || !weight) return FLCE_ERR_INVALID_ARG;
   if (pl.N > 0 && (!hidden || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) || !aligned16(targets))
     return FLCE_ERR_UNSUPPORTED;
-  if (workspace_bytes < logprobs_forward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  const hipError_t e = launch_logprobs(pl, hidden, weight, bias, nullptr, nullptr, targets, logps, entropy, lse,
+  if (workspace_bytes < lp.f_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = launch_logprobs(pl, lp, hidden, weight, bias, nullptr, nullptr, targets, logps, entropy, lse,
                                        static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
@@ -467,7 +540,8 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
                            const float* grad_entropy, void* grad_hidden, void* grad_weight, void* grad_bias,
                            void* workspace, size_t workspace_bytes, void* stream) {
   Plan pl;
-  const int rc = logprobs_plan(p, &pl);
+  LpPlan lp;
+  const int rc = logprobs_plan(p, false, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!weight || !grad_weight || !workspace) return FLCE_ERR_INVALID_ARG;
@@ -477,28 +551,12 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) ||
       !aligned16(targets) || !aligned16(grad_hidden) || !aligned16(grad_weight) || !aligned16(grad_bias))
     return FLCE_ERR_UNSUPPORTED;
-  if (workspace_bytes < logprobs_backward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  LogprobGrad lg;
-  lg.grad_logps = grad_logps;
-  lg.grad_entropy = grad_entropy;
-  lg.entropy = entropy;
-  lg.coefE = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.b_bytes);
-  pl.lg = &lg;
-  const hipError_t e = launch_backward(pl, hidden, weight, bias, targets, lse, nullptr, grad_hidden, grad_weight,
-                                       grad_bias, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  if (workspace_bytes < lp.b_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const LpGrad g{grad_logps, grad_entropy, entropy};
+  const hipError_t e = launch_logprobs_backward(pl, lp, g, hidden, weight, bias, targets, lse, grad_hidden, grad_weight,
+                                                grad_bias, static_cast<char*>(workspace),
+                                                static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
-}
-
-// The int32 sums of up to 2^17 products of magnitude at most 127^2 stay below 2^31.
-static constexpr int64_t kMaxInt8Hidden = int64_t(1) << 17;
-
-static int logprobs_int8_plan(const flce_params* p, Plan* pl) {
-  const int rc = logprobs_plan(p, pl);
-  if (rc != FLCE_OK) return rc;
-  if (pl->H % 16 != 0 || pl->H > kMaxInt8Hidden) return FLCE_ERR_UNSUPPORTED;
-  pl->int8 = true;
-  pl->esize = 1;
-  return FLCE_OK;
 }
 
 int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, void* q, float* scale, void* stream) {
@@ -515,9 +573,10 @@ int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, voi
 int flce_logprobs_int8_workspace_size(const flce_params* p, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   Plan pl;
-  const int rc = logprobs_int8_plan(p, &pl);
+  LpPlan lp;
+  const int rc = logprobs_plan(p, true, &pl, &lp);
   if (rc != FLCE_OK) return rc;
-  *bytes = logprobs_forward_bytes(pl);
+  *bytes = lp.f_bytes;
   return FLCE_OK;
 }
 
@@ -525,7 +584,8 @@ int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hi
                        const float* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   Plan pl;
-  const int rc = logprobs_int8_plan(p, &pl);
+  LpPlan lp;
+  const int rc = logprobs_plan(p, true, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!workspace || !weight || !weight_scale) return FLCE_ERR_INVALID_ARG;
@@ -533,8 +593,8 @@ int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hi
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(weight_scale) ||
       !aligned16(workspace) || !aligned16(targets) || (reinterpret_cast<uintptr_t>(hidden_scale) & 3) != 0)
     return FLCE_ERR_UNSUPPORTED;
-  if (workspace_bytes < logprobs_forward_bytes(pl)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  const hipError_t e = launch_logprobs(pl, hidden, weight, bias, hidden_scale, weight_scale, targets, logps, entropy,
+  if (workspace_bytes < lp.f_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = launch_logprobs(pl, lp, hidden, weight, bias, hidden_scale, weight_scale, targets, logps, entropy,
                                        lse, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }

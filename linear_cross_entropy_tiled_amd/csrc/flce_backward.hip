@@ -122,91 +122,6 @@ __global__ __launch_bounds__(1024) void bwd_prep_kernel(PrepArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The same constants for log-probabilities and entropies: with upstream gradients
-// g of log p_t and h of H,
-//   d / d z_j = g [j = t] - p_j (g + h (H + log p_j))
-//             = coefA p_j + coefE p_j log2 p_j - coefB [j = t],
-// coefA = -(g + h H), coefE = -h ln 2, coefB = -g.
-// ---------------------------------------------------------------------------
-struct LpPrepArgs {
-  const void* targets;
-  int tgt_i32;
-  const float* lse;
-  const float* entropy;
-  const float* grad_logps;
-  const float* grad_entropy;
-  int N, V, N_pad;
-  int64_t ignore_index;
-  float* coefA;
-  float* coefB;
-  float* coefE;
-  float* lseL;
-  int* tgt;
-  int* status;
-  float* dscale;
-  int f16_d;
-  float abs_scale;
-};
-
-__global__ __launch_bounds__(1024) void lp_prep_kernel(LpPrepArgs a) {
-  __shared__ float sm[1024];
-  __shared__ int sb[1024];
-  const int tid = threadIdx.x;
-  float dmax = 0.0f;
-  int bad = 0;
-  for (int i = tid; i < a.N_pad; i += 1024) {
-    // padding and ignored rows: coefficients 0 and an LSE beyond any logit, so that p = 0,
-    // but finite, so that coefE log2 p is 0 too
-    float ca = 0.0f, cb = 0.0f, ce = 0.0f, ll = -kMasked;
-    int tg = -1;
-    if (i < a.N) {
-      const int64_t t = load_target(a.targets, i, a.tgt_i32);
-      const bool in_range = t >= 0 && t < a.V;
-      bad |= (t != a.ignore_index && !in_range) ? 1 : 0;
-      if (t != a.ignore_index && in_range) {
-        ll = a.lse[i] * kLog2e;
-        const float g = a.grad_logps ? a.grad_logps[i] : 0.0f;
-        const float h = a.grad_entropy ? a.grad_entropy[i] : 0.0f;
-        cb = -g;
-        ca = a.grad_entropy ? -fmaf(h, a.entropy[i], g) : -g;
-        if (isnan(ll)) ca = ll;
-        ce = -h * kLn2;
-        tg = (int)t;
-      }
-    }
-    a.coefA[i] = ca;
-    a.coefB[i] = cb;
-    a.coefE[i] = ce;
-    a.lseL[i] = ll;
-    a.tgt[i] = tg;
-    // |p log2 p| < 0.54
-    dmax = fmaxf(dmax, fabsf(ca) + fabsf(cb) + 0.54f * fabsf(ce));
-  }
-  sm[tid] = dmax;
-  sb[tid] = bad;
-  __syncthreads();
-  for (int w = 512; w > 0; w >>= 1) {
-    if (tid < w) {
-      sm[tid] = fmaxf(sm[tid], sm[tid + w]);
-      sb[tid] |= sb[tid + w];
-    }
-    __syncthreads();
-  }
-  if (tid == 0) {
-    a.status[0] = sb[0] ? FLCE_ERR_TARGET_OUT_OF_RANGE : FLCE_OK;
-    int s = 0;
-    const float bound = a.f16_d ? sm[0] * a.abs_scale : 0.0f;   // >= every |D|
-    if (bound > 0.0f && isfinite(bound)) {
-      int e;
-      frexpf(bound, &e);
-      s = min(max(14 - e, -120), 120);
-    }
-    a.dscale[0] = ldexpf(1.0f, s);
-    a.dscale[1] = ldexpf(1.0f, -s);
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Stores of 4 consecutive values (one lane, 4 consecutive rows of a tile),
 // rounded to nearest even.
 // ---------------------------------------------------------------------------
@@ -270,29 +185,8 @@ __device__ __forceinline__ void update4(void* base, size_t o, int type, bool acc
 }
 
 // ---------------------------------------------------------------------------
-// dlogits: one 256 (vocab) x 256 (token) tile per workgroup.
+// dlogits: one 256 (vocab) x 256 (token) tile per workgroup (DlogitsArgs).
 // ---------------------------------------------------------------------------
-struct DlogitsArgs {
-  const char* hidden;
-  const char* weight;
-  const void* bias;
-  int N, H, V;
-  float scale, cap, two_log2e_over_cap, two_cap;
-  int cv0;          // first vocabulary row of the chunk
-  int n_vt_c;       // vocabulary tiles in the chunk
-  int n_tt;
-  const float* coefA;
-  const float* coefB;
-  const float* lseL;
-  const int* tgt;
-  void* D;          // D[t][v - cv0], row stride ldD elements
-  int ldD;
-  float* gb_part;   // [n_tt][ld_gb]
-  int ld_gb;
-  const float* dscale;   // [0]: factor D is stored with
-  const float* coefE;    // ENTROPY only
-};
-
 // DPP lane permutations within each 16-lane row, each an involution that
 // pairs lanes differing in one bit of the lane index (and keeps the bits
 // above it): row mirror (i <-> 15 - i: bit 3), half-row mirror (i <-> 7 - i
@@ -859,31 +753,6 @@ void launch_prep_rows(const Plan& pl, const void* targets, const float* lse, con
   bwd_prep_kernel<<<1, 1024, 0, st>>>(pa);
 }
 
-static void launch_lp_prep(const Plan& pl, const void* targets, const float* lse, float* coefA, float* coefB,
-                           float* lseL, int* tgt, int* status, float* dscale, hipStream_t st) {
-  LpPrepArgs a;
-  a.targets = targets;
-  a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
-  a.lse = lse;
-  a.entropy = pl.lg->entropy;
-  a.grad_logps = pl.lg->grad_logps;
-  a.grad_entropy = pl.lg->grad_entropy;
-  a.N = (int)pl.N;
-  a.V = (int)pl.V;
-  a.N_pad = (int)pl.N_pad;
-  a.ignore_index = pl.ignore_index;
-  a.coefA = coefA;
-  a.coefB = coefB;
-  a.coefE = pl.lg->coefE;
-  a.lseL = lseL;
-  a.tgt = tgt;
-  a.status = status;
-  a.dscale = dscale;
-  a.f16_d = pl.dtype == FLCE_F16;
-  a.abs_scale = fabsf(pl.scale);
-  lp_prep_kernel<<<1, 1024, 0, st>>>(a);
-}
-
 template <typename T, bool ENTROPY>
 static void launch_dlogits(const Plan& pl, const DlogitsArgs& d, int nwg, hipStream_t st) {
   if (pl.has_bias) {
@@ -908,15 +777,11 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
   float* gb_part = reinterpret_cast<float*>(ws + pl.b_gbpart);
 
   float* dscale = reinterpret_cast<float*>(ws + kDscaleOffset);
-  if (pl.lg)
-    launch_lp_prep(pl, targets, lse, coefA, coefB, lseL, tgt, reinterpret_cast<int*>(ws), dscale, st);
-  else
-    launch_prep_rows(pl, targets, lse, grad_loss, coefA, coefB, lseL, tgt, reinterpret_cast<int*>(ws), dscale, 0,
-                     pl.N_pad, st);
+  launch_prep_rows(pl, targets, lse, grad_loss, coefA, coefB, lseL, tgt, reinterpret_cast<int*>(ws), dscale, 0,
+                   pl.N_pad, st);
 
   T* hiddenT = reinterpret_cast<T*>(ws + pl.b_xt);
-  if (pl.N > 0) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, (int)pl.N_pad, hiddenT, st,
-                                         pl.lg ? tgt : nullptr);
+  if (pl.N > 0) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, (int)pl.N_pad, hiddenT, st);
   const bool gh_f32 = pl.dtype == FLCE_F32;
   float* accb = gh_f32 ? reinterpret_cast<float*>(grad_hidden) : reinterpret_cast<float*>(ws + pl.b_ghacc);
   const int ldD = (int)pl.Vc;
@@ -942,7 +807,7 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
       d.n_tt = (int)pl.n_tt;
       d.coefA = coefA;
       d.coefB = coefB;
-      d.coefE = pl.lg ? pl.lg->coefE : nullptr;
+      d.coefE = nullptr;
       d.lseL = lseL;
       d.tgt = tgt;
       d.D = D;
@@ -952,8 +817,7 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
       d.dscale = dscale;
       const int nwg = n_vt_c * (int)pl.n_tt;
       time_begin(pl, st);
-      if (pl.lg) launch_dlogits<T, true>(pl, d, nwg, st);
-      else launch_dlogits<T, false>(pl, d, nwg, st);
+      launch_dlogits<T, false>(pl, d, nwg, st);
       time_end(pl, FLCE_KERNEL_DLOGITS, st);
     }
     {
@@ -1011,6 +875,13 @@ static hipError_t launch_backward_t(const Plan& pl, const void* hidden, const vo
   return hipGetLastError();
 }
 
+void launch_lp_dlogits(const Plan& pl, const DlogitsArgs& d, hipStream_t st) {
+  const int nwg = d.n_vt_c * d.n_tt;
+  if (pl.dtype == FLCE_BF16) launch_dlogits<bf16, true>(pl, d, nwg, st);
+  else if (pl.dtype == FLCE_F16) launch_dlogits<f16, true>(pl, d, nwg, st);
+  else launch_dlogits<float, true>(pl, d, nwg, st);
+}
+
 void launch_gb_reduce(int dtype, const float* part, int n_tt, int ld, int V, void* gb, int accumulate,
                       const float* dscale, hipStream_t st) {
   const int nwg = (V + 255) / 256;
@@ -1045,13 +916,21 @@ void launch_gw(int dtype, const GwArgs& g, hipStream_t st) {
 }
 
 template <typename T>
+static void launch_gh_reduce_t(const GhArgs& h, hipStream_t st) {
+  const int64_t nh = (int64_t)h.N * h.H, n4 = nh / 4;
+  bwd_gh_reduce<T><<<(int)((n4 + 255) / 256), 256, 0, st>>>(h.part, h.parts, n4, nh, h.accb, h.out, h.out_f32, h.mode);
+}
+
+void launch_gh_reduce(int dtype, const GhArgs& h, hipStream_t st) {
+  if (dtype == FLCE_BF16) launch_gh_reduce_t<bf16>(h, st);
+  else if (dtype == FLCE_F16) launch_gh_reduce_t<f16>(h, st);
+  else launch_gh_reduce_t<float>(h, st);
+}
+
+template <typename T>
 static void launch_gh_t(const GhArgs& h, hipStream_t st) {
   bwd_gh_kernel<T><<<h.n_ht * h.n_tt * h.parts, kThreads, 0, st>>>(h);
-  if (h.parts > 1) {
-    const int64_t nh = (int64_t)h.N * h.H, n4 = nh / 4;
-    bwd_gh_reduce<T><<<(int)((n4 + 255) / 256), 256, 0, st>>>(h.part, h.parts, n4, nh, h.accb, h.out, h.out_f32,
-                                                              h.mode);
-  }
+  if (h.parts > 1) launch_gh_reduce_t<T>(h, st);
 }
 
 void launch_gh(int dtype, const GhArgs& h, hipStream_t st) {

@@ -19,7 +19,6 @@ struct Plan {
   bool tgt_i32;                  // targets are int32 (else int64)
   bool gw_accum_out;             // one-pass path: sum grad_weight over the blocks in its own dtype
   float scale, cap, z_loss;
-  const struct LogprobGrad* lg;  // backward of the log-probabilities and entropies (else of the loss)
   flce_launch_timer* timer;      // optional event pairs around the matrix-core launches (caller-owned)
 
   int64_t n_tt, n_vt, n_ht;      // 256-wide tiles over tokens, vocabulary, hidden
@@ -45,14 +44,6 @@ struct Plan {
   bool fb_gw_acc32;              // grad_weight summed over the blocks in an fp32 workspace accumulator
   size_t fb_part, fb_blk, fb_coefA, fb_coefB, fb_lseL, fb_tgt, fb_Z, fb_xt, fb_ghacc, fb_gwacc, fb_ghpart,
       fb_gbpart, fb_bytes;
-};
-
-// Upstream gradients of flce_logprobs_backward.  coefE: N_pad fp32 of workspace.
-struct LogprobGrad {
-  const float* grad_logps;       // NULL: zero
-  const float* grad_entropy;     // NULL: zero
-  const float* entropy;          // the forward's entropies (with grad_entropy)
-  float* coefE;
 };
 
 // Vocabulary splits of the forward tile kernel for n_tt token tiles: about
@@ -92,6 +83,28 @@ struct BlockPart {
   int n_correct;
   int bad_target;
   int pad;
+};
+
+// One vocabulary chunk of the logit gradient.
+struct DlogitsArgs {
+  const char* hidden;
+  const char* weight;
+  const void* bias;
+  int N, H, V;
+  float scale, cap, two_log2e_over_cap, two_cap;
+  int cv0;          // first vocabulary row of the chunk
+  int n_vt_c;       // vocabulary tiles in the chunk
+  int n_tt;
+  const float* coefA;
+  const float* coefB;
+  const float* lseL;
+  const int* tgt;
+  void* D;          // D[t][v - cv0], row stride ldD elements
+  int ldD;
+  float* gb_part;   // [n_tt][ld_gb]
+  int ld_gb;
+  const float* dscale;   // [0]: factor D is stored with
+  const float* coefE;    // ENTROPY only
 };
 
 // ---------------------------------------------------------------------------
@@ -146,6 +159,9 @@ void launch_transpose_hidden(int dtype, const void* hidden, int N, int H, int N_
                              hipStream_t st, const int* tgt = nullptr);
 void launch_gw(int dtype, const GwArgs& g, hipStream_t st);
 void launch_gh(int dtype, const GhArgs& h, hipStream_t st);
+void launch_gh_reduce(int dtype, const GhArgs& h, hipStream_t st);
+// The logit gradient with the entropy term (log-probabilities).
+void launch_lp_dlogits(const Plan& pl, const DlogitsArgs& d, hipStream_t st);
 // grad_hidden K-split planning (parts, 64-row stages per part) for a chunk of
 // width cvn over n_tiles output tiles.
 void plan_gh_split(int64_t n_tiles, int64_t cvn, int esize, int64_t N, int64_t H, int* parts, int* kt_per_part);
@@ -186,15 +202,6 @@ hipError_t launch_forward_backward(const Plan& pl, const void* hidden, const voi
                                    const void* targets, const float* grad_loss, float* loss, float* lse,
                                    int64_t* num_correct, float* entropy_sum, void* grad_hidden, void* grad_weight,
                                    void* grad_bias, char* ws, hipStream_t st);
-
-// Log-probabilities and entropies of the targets (flce_logprobs_forward).
-size_t logprobs_forward_bytes(const Plan& pl);
-// pl.int8: 8-bit operands with their scales, bias in fp32.
-hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weight, const void* bias,
-                           const float* hidden_scale, const float* weight_scale, const void* targets, float* logps,
-                           float* entropy, float* lse, char* ws, hipStream_t st);
-hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
-                           hipStream_t st);
 
 hipError_t launch_scale_gradients(const Plan& pl, const float* g, void* grad_hidden, void* grad_weight,
                                   void* grad_bias, hipStream_t st);

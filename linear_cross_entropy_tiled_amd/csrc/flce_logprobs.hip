@@ -15,46 +15,13 @@
 // With 8-bit operands (a frozen scorer's head) the accumulator is the exact int32
 // product; one multiplication by the vocabulary row's scale and one by the token's
 // turn it into the logit, and the rest is the same.
+#include <math.h>
+
 #include "flce_device.h"
-#include "flce_internal.h"
+#include "flce_logprobs.h"
+#include "flce_lp_state.h"
 
 namespace flce {
-
-struct LpTileArgs {
-  const char* hidden;
-  const char* weight;
-  const void* bias;           // the operands' type; fp32 for int8
-  const float* hidden_scale;  // int8
-  const float* weight_scale;  // int8
-  const void* targets;
-  int tgt_i32;
-  int N, H, V;
-  int64_t ignore_index;
-  float scale, cap, two_log2e_over_cap;
-  int n_vt, S, N_pad;
-  float* part;      // [4][S][N_pad]: m, l, T, y_t
-  int* status;      // set to FLCE_OK here; lp_rows_kernel reports bad targets
-};
-
-// A row's state over some of its logits.  With nothing seen: m = kMasked, l = T = 0.
-struct LpState {
-  float m, l, T, yt;
-};
-
-__device__ __forceinline__ void lp_merge(LpState& a, const LpState& b) {
-  const float mn = fmaxf(a.m, b.m);
-  // a state without any finite logit (l = 0) may have m = -inf or kMasked: its shift
-  // is not used, so that 0 times it is no NaN
-  const float da = a.l == 0.0f ? 0.0f : a.m - mn, db = b.l == 0.0f ? 0.0f : b.m - mn;
-  const float fa = fast_exp2(da), fb = fast_exp2(db);
-  a.T = fmaf(da, a.l, a.T) * fa + fmaf(db, b.l, b.T) * fb;
-  a.l = a.l * fa + b.l * fb;
-  a.m = mn;
-  a.yt = fmaxf(a.yt, b.yt);
-}
-
-template <typename T> struct BiasOf { typedef T type; };
-template <> struct BiasOf<int8_t> { typedef float type; };
 
 template <typename T, bool HAS_BIAS, bool SOFTCAP>
 __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
@@ -300,11 +267,14 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   }
 }
 
-// Merges each row's vocabulary splits, in order, and writes its outputs.
+// Merges each row's vocabulary splits and writes its outputs: `group` lanes a row
+// (a power of two up to 64), each taking every group-th split, then a tree, so that
+// the order depends on the sizes alone.  Few rows have hundreds of splits, and a lane
+// on its own would wait for one load after the other (38 us for 4 rows of 256 splits).
 struct LpRowArgs {
   const void* targets;
   int tgt_i32;
-  int N, V, S, N_pad;
+  int N, V, S, N_pad, group;
   int64_t ignore_index;
   const float* part;
   float* logps;
@@ -315,25 +285,35 @@ struct LpRowArgs {
 };
 
 __global__ __launch_bounds__(256) void lp_rows_kernel(LpRowArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (a.init_status && i == 0) a.status[0] = FLCE_OK;
-  if (i >= a.N) return;
+  const int i = ((int)blockIdx.x * 256 + (int)threadIdx.x) / a.group, sub = threadIdx.x & (a.group - 1);
+  if (a.init_status && blockIdx.x == 0 && threadIdx.x == 0) a.status[0] = FLCE_OK;
+  const int row = min(i, a.N - 1);   // whole groups past the last row stay in step
+  if (a.N == 0) return;
   const size_t plane = (size_t)a.S * a.N_pad;
   LpState r{kMasked, 0.0f, 0.0f, -INFINITY};
-  for (int s0 = 0; s0 < a.S; s0 += 8) {
-    LpState q[8];
+  for (int s0 = sub; s0 < a.S; s0 += 4 * a.group) {
+    LpState q[4];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {   // eight loads in flight; past the last split the last one, not merged
-      const float* p = a.part + (size_t)min(s0 + j, a.S - 1) * a.N_pad + i;
+    for (int j = 0; j < 4; j++) {   // four loads in flight; past the last split the last one, not merged
+      const float* p = a.part + (size_t)min(s0 + j * a.group, a.S - 1) * a.N_pad + row;
       q[j].m = p[0];
       q[j].l = p[plane];
       q[j].T = p[2 * plane];
       q[j].yt = p[3 * plane];
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (s0 + j < a.S) lp_merge(r, q[j]);
+    for (int j = 0; j < 4; j++)
+      if (s0 + j * a.group < a.S) lp_merge(r, q[j]);
   }
+  for (int o = 1; o < a.group; o <<= 1) {
+    LpState q;
+    q.m = __shfl_xor(r.m, o);
+    q.l = __shfl_xor(r.l, o);
+    q.T = __shfl_xor(r.T, o);
+    q.yt = __shfl_xor(r.yt, o);
+    lp_merge(r, q);
+  }
+  if (sub != 0 || i >= a.N) return;
   const float l2 = fast_log2(r.l);
   const int64_t t = load_target(a.targets, i, a.tgt_i32);
   const bool in_range = t >= 0 && t < a.V, valid = t != a.ignore_index && in_range;
@@ -417,7 +397,7 @@ hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols,
   return hipGetLastError();
 }
 
-hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weight, const void* bias,
+hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden, const void* weight, const void* bias,
                            const float* hidden_scale, const float* weight_scale, const void* targets, float* logps,
                            float* entropy, float* lse, char* ws, hipStream_t st) {
   float* part = reinterpret_cast<float*>(ws + kStatusBytes);
@@ -438,13 +418,14 @@ hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weigh
     a.scale = pl.scale;
     a.cap = pl.cap;
     a.two_log2e_over_cap = pl.cap > 0 ? 2.0f * kLog2e / pl.cap : 0.0f;
-    a.n_vt = (int)pl.n_vt;
-    a.S = pl.S;
-    a.N_pad = (int)pl.N_pad;
+    a.n_vt = lp.bn ? (int)((pl.V + 63) / 64) : (int)pl.n_vt;
+    a.S = lp.S;
+    a.N_pad = lp.N_pad;
     a.part = part;
     a.status = status;
-    const int nwg = (int)pl.n_tt * pl.S;
-    if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
+    const int nwg = lp.n_tt * lp.S;
+    if (lp.bn) launch_lp_small(pl, lp.bn, a, lp.n_tt, st);
+    else if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
     else if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
     else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);
     else launch_lp_tiles<float>(pl, a, nwg, st);
@@ -454,8 +435,10 @@ hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weigh
   r.tgt_i32 = pl.tgt_i32 ? 1 : 0;
   r.N = (int)pl.N;
   r.V = (int)pl.V;
-  r.S = pl.S;
-  r.N_pad = (int)pl.N_pad;
+  r.S = lp.S;
+  r.N_pad = lp.N_pad;
+  r.group = 1;
+  while (r.group < 64 && r.group < lp.S) r.group *= 2;
   r.ignore_index = pl.ignore_index;
   r.part = part;
   r.logps = logps;
@@ -463,12 +446,206 @@ hipError_t launch_logprobs(const Plan& pl, const void* hidden, const void* weigh
   r.lse = lse;
   r.status = status;
   r.init_status = pl.N == 0;
-  lp_rows_kernel<<<(unsigned)(pl.n_tt > 0 ? pl.n_tt : 1), 256, 0, st>>>(r);
+  const int64_t blocks = (pl.N * r.group + 255) / 256;
+  lp_rows_kernel<<<(unsigned)(blocks > 0 ? blocks : 1), 256, 0, st>>>(r);
   return hipGetLastError();
 }
 
-size_t logprobs_forward_bytes(const Plan& pl) {
-  return (kStatusBytes + size_t(4) * pl.S * pl.N_pad * 4 + 255) / 256 * 256;
+// ---------------------------------------------------------------------------
+// Backward: the loss's, with these per-row constants.
+// ---------------------------------------------------------------------------
+// With upstream gradients
+// g of log p_t and h of H,
+//   d / d z_j = g [j = t] - p_j (g + h (H + log p_j))
+//             = coefA p_j + coefE p_j log2 p_j - coefB [j = t],
+// coefA = -(g + h H), coefE = -h ln 2, coefB = -g.
+struct LpPrepArgs {
+  const void* targets;
+  int tgt_i32;
+  const float* lse;
+  const float* entropy;
+  const float* grad_logps;
+  const float* grad_entropy;
+  int N, V, N_pad;
+  int64_t ignore_index;
+  float* coefA;
+  float* coefB;
+  float* coefE;
+  float* lseL;
+  int* tgt;
+  int* status;
+  float* dscale;
+  int f16_d;
+  float abs_scale;
+};
+
+__global__ __launch_bounds__(1024) void lp_prep_kernel(LpPrepArgs a) {
+  __shared__ float sm[1024];
+  __shared__ int sb[1024];
+  const int tid = threadIdx.x;
+  float dmax = 0.0f;
+  int bad = 0;
+  for (int i = tid; i < a.N_pad; i += 1024) {
+    // padding and ignored rows: coefficients 0 and an LSE beyond any logit, so that p = 0,
+    // but finite, so that coefE log2 p is 0 too
+    float ca = 0.0f, cb = 0.0f, ce = 0.0f, ll = -kMasked;
+    int tg = -1;
+    if (i < a.N) {
+      const int64_t t = load_target(a.targets, i, a.tgt_i32);
+      const bool in_range = t >= 0 && t < a.V;
+      bad |= (t != a.ignore_index && !in_range) ? 1 : 0;
+      if (t != a.ignore_index && in_range) {
+        ll = a.lse[i] * kLog2e;
+        const float g = a.grad_logps ? a.grad_logps[i] : 0.0f;
+        const float h = a.grad_entropy ? a.grad_entropy[i] : 0.0f;
+        cb = -g;
+        ca = a.grad_entropy ? -fmaf(h, a.entropy[i], g) : -g;
+        if (isnan(ll)) ca = ll;
+        ce = -h * kLn2;
+        tg = (int)t;
+      }
+    }
+    a.coefA[i] = ca;
+    a.coefB[i] = cb;
+    a.coefE[i] = ce;
+    a.lseL[i] = ll;
+    a.tgt[i] = tg;
+    // |p log2 p| < 0.54
+    dmax = fmaxf(dmax, fabsf(ca) + fabsf(cb) + 0.54f * fabsf(ce));
+  }
+  sm[tid] = dmax;
+  sb[tid] = bad;
+  __syncthreads();
+  for (int w = 512; w > 0; w >>= 1) {
+    if (tid < w) {
+      sm[tid] = fmaxf(sm[tid], sm[tid + w]);
+      sb[tid] |= sb[tid + w];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.status[0] = sb[0] ? FLCE_ERR_TARGET_OUT_OF_RANGE : FLCE_OK;
+    int s = 0;
+    const float bound = a.f16_d ? sm[0] * a.abs_scale : 0.0f;   // >= every |D|
+    if (bound > 0.0f && isfinite(bound)) {
+      int e;
+      frexpf(bound, &e);
+      s = min(max(14 - e, -120), 120);
+    }
+    a.dscale[0] = ldexpf(1.0f, s);
+    a.dscale[1] = ldexpf(1.0f, -s);
+  }
+}
+
+// The gradients, one vocabulary chunk after the other: the logit gradient, then the
+// two contractions, each with large or small tiles as the plan says (D has one layout).
+hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGrad& g, const void* hidden,
+                                    const void* weight, const void* bias, const void* targets, const float* lse,
+                                    void* grad_hidden, void* grad_weight, void* grad_bias, char* ws, hipStream_t st) {
+  LpPrepArgs a;
+  a.targets = targets;
+  a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
+  a.lse = lse;
+  a.entropy = g.entropy;
+  a.grad_logps = g.grad_logps;
+  a.grad_entropy = g.grad_entropy;
+  a.N = (int)pl.N;
+  a.V = (int)pl.V;
+  a.N_pad = (int)pl.N_pad;
+  a.ignore_index = pl.ignore_index;
+  a.coefA = reinterpret_cast<float*>(ws + pl.b_coefA);
+  a.coefB = reinterpret_cast<float*>(ws + pl.b_coefB);
+  a.coefE = reinterpret_cast<float*>(ws + lp.b_coefE);
+  a.lseL = reinterpret_cast<float*>(ws + pl.b_lseL);
+  a.tgt = reinterpret_cast<int*>(ws + pl.b_tgt);
+  a.status = reinterpret_cast<int*>(ws);
+  a.dscale = reinterpret_cast<float*>(ws + kDscaleOffset);
+  a.f16_d = pl.dtype == FLCE_F16;
+  a.abs_scale = fabsf(pl.scale);
+  lp_prep_kernel<<<1, 1024, 0, st>>>(a);
+
+  char* hiddenT = ws + pl.b_xt;
+  if (pl.N > 0) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, lp.K_pad, hiddenT, st, a.tgt);
+  float* gb_part = reinterpret_cast<float*>(ws + (lp.d_small ? lp.b_gbpart : pl.b_gbpart));
+  const bool f32 = pl.dtype == FLCE_F32;
+  for (int c = 0; c < pl.n_chunks; c++) {
+    const int cv0 = (int)(c * pl.Vc);
+    const int cvn = (int)(pl.V_pad - cv0 < pl.Vc ? pl.V_pad - cv0 : pl.Vc);
+    if (pl.N > 0) {
+      DlogitsArgs d;
+      d.hidden = static_cast<const char*>(hidden);
+      d.weight = static_cast<const char*>(weight);
+      d.bias = bias;
+      d.N = (int)pl.N;
+      d.H = (int)pl.H;
+      d.V = (int)pl.V;
+      d.scale = pl.scale;
+      d.cap = pl.cap;
+      d.two_log2e_over_cap = pl.cap > 0 ? 2.0f * kLog2e / pl.cap : 0.0f;
+      d.two_cap = 2.0f * pl.cap;
+      d.cv0 = cv0;
+      d.n_vt_c = lp.d_small ? cvn / 64 : cvn / 256;
+      d.n_tt = lp.d_small ? lp.n64 : (int)pl.n_tt;
+      d.coefA = a.coefA;
+      d.coefB = a.coefB;
+      d.coefE = a.coefE;
+      d.lseL = a.lseL;
+      d.tgt = a.tgt;
+      d.D = ws + pl.b_D;
+      d.ldD = (int)pl.Vc;
+      d.gb_part = gb_part;
+      d.ld_gb = (int)pl.V_pad;
+      d.dscale = a.dscale;
+      if (lp.d_small) launch_dlogits_small(pl, d, st);
+      else launch_lp_dlogits(pl, d, st);
+    }
+    GwArgs w;
+    w.hiddenT = hiddenT;
+    w.D = ws + pl.b_D;
+    w.ldD = (int)pl.Vc;
+    w.N = (int)pl.N;
+    w.H = (int)pl.H;
+    w.V = (int)pl.V;
+    w.N_pad = lp.K_pad;
+    w.cv0 = cv0;
+    w.n_ht = lp.gw_small ? (int)((pl.H + 63) / 64) : (int)pl.n_ht;
+    w.n_vt_c = lp.gw_small ? cvn / 64 : cvn / 256;
+    w.gw = grad_weight;
+    w.gw_type = pl.gw_dtype;
+    w.dscale = a.dscale;
+    w.accumulate = pl.accum_gw ? 1 : 0;
+    w.acc32 = nullptr;
+    w.mode = 3;
+    if (lp.gw_small) launch_gw_small(pl.dtype, w, st);
+    else launch_gw(pl.dtype, w, st);
+    if (pl.N > 0) {
+      GhArgs h;
+      h.weight = static_cast<const char*>(weight);
+      h.D = ws + pl.b_D;
+      h.ldD = (int)pl.Vc;
+      h.N = (int)pl.N;
+      h.H = (int)pl.H;
+      h.V = (int)pl.V;
+      h.cv0 = cv0;
+      h.cvn = cvn;
+      h.n_ht = lp.gh_small ? (int)((pl.H + 63) / 64) : (int)pl.n_ht;
+      h.n_tt = lp.gh_small ? lp.n64 : (int)pl.n_tt;
+      h.accb = f32 ? reinterpret_cast<float*>(grad_hidden) : reinterpret_cast<float*>(ws + pl.b_ghacc);
+      h.out = grad_hidden;
+      h.out_f32 = f32;
+      h.mode = pl.n_chunks == 1 ? 3 : (c == 0 ? 0 : (c == pl.n_chunks - 1 ? 2 : 1));
+      h.parts = lp.gh_small ? lp.gh_parts : pl.gh_parts;
+      h.kt_per_part = lp.gh_small ? lp.gh_kt : pl.gh_kt_per_part;
+      h.part = reinterpret_cast<float*>(ws + (lp.gh_small ? lp.b_ghpart : pl.b_ghpart));
+      h.dscale = a.dscale;
+      if (lp.gh_small) launch_gh_small(pl.dtype, h, st);
+      else launch_gh(pl.dtype, h, st);
+    }
+  }
+  if (grad_bias)
+    launch_gb_reduce(pl.dtype, gb_part, lp.d_small ? lp.n64 : (int)pl.n_tt, (int)pl.V_pad, (int)pl.V, grad_bias,
+                     pl.accum_gb ? 1 : 0, a.dscale, st);
+  return hipGetLastError();
 }
 
 }  // namespace flce

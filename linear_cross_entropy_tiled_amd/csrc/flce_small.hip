@@ -1,0 +1,426 @@
+// The log-probability kernels with small tiles (flce_small.h), for problems whose
+// 256 x 256 tiles would leave most CUs idle: few tokens, short vocabularies, and fp32,
+// where one large tile takes a CU 0.2 ms per 1024 of hidden size.  The arithmetic of
+// the epilogues is that of the large kernels (flce_logprobs.hip, flce_backward.hip).
+#include "flce_logprobs.h"
+#include "flce_lp_state.h"
+#include "flce_small.h"
+
+namespace flce {
+
+using small::Shape;
+
+// Token tiles are the fast index: workgroups that share a weight tile run together.
+template <typename T, bool HAS_BIAS, bool SOFTCAP, int BN>
+__global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a, int n_tt) {
+  typedef Shape<BN> Sh;
+  constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
+  constexpr bool I8 = E == 1;
+  typedef typename BiasOf<T>::type B;
+  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(BN)];
+  static __shared__ float xs[Sh::WM][4][BN];
+  const int L = xcd_logical_id(blockIdx.x, gridDim.x);
+  const int tt = L % n_tt, s = L / n_tt;
+  const int vt_begin = (int)((int64_t)s * a.n_vt / a.S), vt_end = (int)((int64_t)(s + 1) * a.n_vt / a.S);
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+  const int t0 = tt * BN;
+  if (blockIdx.x == 0 && tid == 0) a.status[0] = FLCE_OK;
+
+  const float s_u = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e;
+  LpState st[NI];
+  int tgt[NI];
+  float s_a[NI];
+#pragma unroll
+  for (int ni = 0; ni < NI; ni++) {
+    st[ni] = LpState{kMasked, 0.0f, 0.0f, -INFINITY};
+    const int t = t0 + (wn * NI + ni) * 16 + (lane & 15);
+    const int64_t tv = t < a.N ? load_target(a.targets, t, a.tgt_i32) : a.ignore_index;
+    tgt[ni] = (tv != a.ignore_index && tv >= 0 && tv < a.V) ? (int)tv : -1;
+    s_a[ni] = I8 ? s_u * (t < a.N ? a.hidden_scale[t] : 0.0f) : s_u;
+  }
+
+  const uint32_t ld = (uint32_t)a.H * E;
+  OperandDesc db;
+  db.base = a.hidden + (size_t)t0 * ld;
+  db.ld_bytes = ld;
+  db.nrec = (uint32_t)min(a.N - t0, BN) * ld;
+  db.cols_valid = 0;
+  db.k_bytes = a.H * E;
+  const int KT = (a.H * E + kBKB - 1) / kBKB;
+
+  for (int vt = vt_begin; vt < vt_end; ++vt) {
+    const int v0 = vt * 64;
+    OperandDesc da;
+    da.base = a.weight + (size_t)v0 * ld;
+    da.ld_bytes = ld;
+    da.nrec = (uint32_t)min(a.V - v0, 64) * ld;
+    da.cols_valid = 0;
+    da.k_bytes = a.H * E;
+    Acc acc[MI][NI];
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+      for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();   // every wave has read the last tile's stages
+    small::mainloop<T, true, true, BN>(da, db, KT, lds, acc);
+
+    float sb[MI][4], ws[MI][4];
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int v = min(v0 + (wm * MI + mi) * 16 + 4 * (lane >> 4) + r, a.V - 1);
+        if (HAS_BIAS) sb[mi][r] = (float)reinterpret_cast<const B*>(a.bias)[v] * s_u;
+        if (I8) ws[mi][r] = a.weight_scale[v];
+      }
+#pragma unroll
+    for (int ni = 0; ni < NI; ni++) {
+      float mu = kMasked;
+#pragma unroll
+      for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          float u = I8 ? (float)__builtin_bit_cast(int, (float)acc[mi][ni][r]) * ws[mi][r] : acc[mi][ni][r];
+          u = HAS_BIAS ? fmaf(u, s_a[ni], sb[mi][r]) : u * s_a[ni];
+          if constexpr (SOFTCAP) u = fmaf(-2.0f * cap2, fast_rcp(fast_exp2(u) + 1.0f), cap2);
+          const int v = v0 + (wm * MI + mi) * 16 + 4 * (lane >> 4) + r;
+          if (v == tgt[ni]) st[ni].yt = u;
+          if (v >= a.V) u = 2.0f * kMasked;   // below every running maximum: adds 0
+          acc[mi][ni][r] = u;
+          mu = fmaxf(mu, u);
+        }
+      const float m_new = fmaxf(st[ni].m, mu);
+      const float dm = st[ni].l == 0.0f ? 0.0f : st[ni].m - m_new;
+      const float alpha = fast_exp2(dm);
+      float se = 0.0f, sx = 0.0f;
+#pragma unroll
+      for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const float x = acc[mi][ni][r] - m_new, e = fast_exp2(x);
+          se += e;
+          sx = fmaf(e, fmaxf(x, kMasked), sx);
+        }
+      st[ni].T = fmaf(fmaf(dm, st[ni].l, st[ni].T), alpha, sx);
+      st[ni].l = fmaf(st[ni].l, alpha, se);
+      st[ni].m = m_new;
+    }
+  }
+
+#pragma unroll
+  for (int ni = 0; ni < NI; ni++) {
+#pragma unroll
+    for (int x = 16; x <= 32; x <<= 1) {
+      LpState o;
+      o.m = __shfl_xor(st[ni].m, x);
+      o.l = __shfl_xor(st[ni].l, x);
+      o.T = __shfl_xor(st[ni].T, x);
+      o.yt = __shfl_xor(st[ni].yt, x);
+      lp_merge(st[ni], o);
+    }
+    if (lane < 16) {
+      const int c = (wn * NI + ni) * 16 + lane;
+      xs[wm][0][c] = st[ni].m;
+      xs[wm][1][c] = st[ni].l;
+      xs[wm][2][c] = st[ni].T;
+      xs[wm][3][c] = st[ni].yt;
+    }
+  }
+  __syncthreads();
+  if (tid < BN) {
+    LpState r{xs[0][0][tid], xs[0][1][tid], xs[0][2][tid], xs[0][3][tid]};
+#pragma unroll
+    for (int w = 1; w < Sh::WM; w++) lp_merge(r, LpState{xs[w][0][tid], xs[w][1][tid], xs[w][2][tid], xs[w][3][tid]});
+    const size_t plane = (size_t)a.S * a.N_pad;
+    float* out = a.part + (size_t)s * a.N_pad + t0 + tid;
+    out[0] = r.m;
+    out[plane] = r.l;
+    out[2 * plane] = r.T;
+    out[3 * plane] = r.yt;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Logit gradient (with the entropy term): one 64 (vocabulary) x 64 (token) tile.
+// ---------------------------------------------------------------------------
+template <typename T> __device__ __forceinline__ void put4(T* p, const float* v) {
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  V4 o;
+#pragma unroll
+  for (int j = 0; j < 4; j++) o[j] = (T)v[j];
+  *reinterpret_cast<V4*>(p) = o;
+}
+template <typename T> __device__ __forceinline__ void get4(const T* p, float* v) {
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  const V4 o = *reinterpret_cast<const V4*>(p);
+#pragma unroll
+  for (int j = 0; j < 4; j++) v[j] = (float)o[j];
+}
+
+template <typename T, bool HAS_BIAS, bool SOFTCAP>
+__global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(DlogitsArgs a) {
+  typedef Shape<64> Sh;
+  constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
+  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(64)];
+  static __shared__ float gbs[Sh::WN][64];
+  const int L = xcd_logical_id(blockIdx.x, gridDim.x);
+  const int tt = L % a.n_tt, vt = L / a.n_tt;
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+  const int v0 = a.cv0 + vt * 64, t0 = tt * 64;
+  const uint32_t ld = (uint32_t)a.H * E;
+  OperandDesc da, db;
+  da.base = a.weight + (size_t)v0 * ld;
+  da.ld_bytes = ld;
+  da.nrec = (uint32_t)max(min(a.V - v0, 64), 0) * ld;
+  da.cols_valid = 0;
+  da.k_bytes = a.H * E;
+  db.base = a.hidden + (size_t)t0 * ld;
+  db.ld_bytes = ld;
+  db.nrec = (uint32_t)max(min(a.N - t0, 64), 0) * ld;
+  db.cols_valid = 0;
+  db.k_bytes = a.H * E;
+  Acc acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+    for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
+  small::mainloop<T, true, true, 64>(da, db, (a.H * E + kBKB - 1) / kBKB, lds, acc);
+
+  const float s2 = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale;
+  const float k1 = -a.two_cap * kLog2e;
+  const float cmul = (SOFTCAP ? 4.0f * a.scale : a.scale) * a.dscale[0];
+  T* D = reinterpret_cast<T*>(a.D);
+  float cs[MI][4];
+#pragma unroll
+  for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+    for (int r = 0; r < 4; r++) cs[mi][r] = 0.0f;
+#pragma unroll
+  for (int ni = 0; ni < NI; ni++) {
+    const int t = t0 + (wn * NI + ni) * 16 + (lane & 15);   // the per-token arrays hold whole 256-token tiles
+    const float cA = a.coefA[t] * cmul, cB = a.coefB[t] * cmul, cE = a.coefE[t] * cmul, lL = a.lseL[t];
+    const float k0 = SOFTCAP ? fmaf(a.cap, kLog2e, -lL) : -lL;
+    const int tg = a.tgt[t];
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++) {
+      const int vl = (wm * MI + mi) * 16 + 4 * (lane >> 4);
+      float d[4];
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int v = v0 + vl + r;
+        float u = acc[mi][ni][r] * s2;
+        if (HAS_BIAS) u = fmaf(acc[mi][ni][r], s2, (float)reinterpret_cast<const T*>(a.bias)[min(v, a.V - 1)] * s2);
+        if constexpr (SOFTCAP) {
+          u = fmaxf(u, kMasked);
+          const float rr = fast_rcp(fast_exp2(u) + 1.0f), x = fmaf(rr, k1, k0), f = fmaf(-rr, rr, rr);
+          d[r] = (fast_exp2(x) * fmaf(x, cE, cA)) * f;
+          if (v == tg) d[r] -= cB * f;
+        } else {
+          const float x = fmaxf(fmaf(u, kLog2e, k0), kMasked);
+          d[r] = fast_exp2(x) * fmaf(x, cE, cA);
+          if (v == tg) d[r] -= cB;
+        }
+        if (v >= a.V) d[r] = 0.0f;
+        cs[mi][r] += d[r];
+      }
+      put4<T>(D + (size_t)t * a.ldD + (v0 - a.cv0) + vl, d);
+    }
+  }
+  if constexpr (HAS_BIAS) {
+    // column sums over the tile's 64 tokens: 16 lanes, then the two token waves
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        float x = cs[mi][r];
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);
+        if ((lane & 15) == 0) gbs[wn][(wm * MI + mi) * 16 + 4 * (lane >> 4) + r] = x;
+      }
+    __syncthreads();
+    if (tid < 64) a.gb_part[(size_t)tt * a.ld_gb + v0 + tid] = gbs[0][tid] + gbs[1][tid];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// grad_weight[v][h] = sum_t hidden[t][h] D[t][v]: a 64 (h) x 64 (v) tile.
+// ---------------------------------------------------------------------------
+template <typename T, typename OutT>
+__global__ __launch_bounds__(small::kThreadsS) void gw_small_kernel(GwArgs a) {
+  typedef Shape<64> Sh;
+  constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
+  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(64)];
+  const int L = xcd_logical_id(blockIdx.x, gridDim.x);
+  const int ht = L % a.n_ht, vt = L / a.n_ht;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+  const int h0 = ht * 64, vl0 = vt * 64;
+  OperandDesc da, db;
+  const uint32_t ldt = (uint32_t)a.N_pad * E, ldd = (uint32_t)a.ldD * E;
+  da.base = a.hiddenT + (size_t)h0 * ldt;
+  da.ld_bytes = ldt;
+  da.nrec = (uint32_t)min(a.H - h0, 64) * ldt;
+  da.cols_valid = 0;
+  da.k_bytes = a.N_pad * E;
+  db.base = a.D + (size_t)vl0 * E;
+  db.ld_bytes = ldd;
+  db.nrec = a.N_pad > 0 ? (uint32_t)((size_t)a.N_pad * ldd - (size_t)vl0 * E) : 0u;
+  db.cols_valid = a.ldD - vl0;
+  db.k_bytes = 0;
+  Acc acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+    for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
+  small::mainloop<T, true, false, 64>(da, db, (a.N_pad * E + kBKB - 1) / kBKB, lds, acc);
+  const float inv = a.dscale[1];
+  OutT* gw = reinterpret_cast<OutT*>(a.gw);
+#pragma unroll
+  for (int ni = 0; ni < NI; ni++) {
+    const int v = a.cv0 + vl0 + (wn * NI + ni) * 16 + (lane & 15);
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++) {
+      const int h = h0 + (wm * MI + mi) * 16 + 4 * (lane >> 4);   // 4 consecutive h; H % 8 == 0
+      if (v >= a.V || h >= a.H) continue;
+      float c[4], prev[4];
+#pragma unroll
+      for (int r = 0; r < 4; r++) c[r] = acc[mi][ni][r] * inv;
+      if (a.accumulate) {
+        get4<OutT>(gw + (size_t)v * a.H + h, prev);
+#pragma unroll
+        for (int r = 0; r < 4; r++) c[r] += prev[r];
+      }
+      put4<OutT>(gw + (size_t)v * a.H + h, c);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// grad_hidden[t][h] = sum_v weight[v][h] D[t][v] over a chunk: a 64 (h) x 64 (t) tile
+// of one split of the vocabulary; modes and parts as bwd_gh_kernel.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(small::kThreadsS) void gh_small_kernel(GhArgs a) {
+  typedef Shape<64> Sh;
+  constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
+  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(64)];
+  const int L = xcd_logical_id(blockIdx.x, gridDim.x);
+  const int n_tiles = a.n_ht * a.n_tt, split = L / n_tiles, in = L - split * n_tiles;
+  const int tt = in % a.n_tt, ht = in / a.n_tt;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+  const int h0 = ht * 64, t0 = tt * 64;
+  const int KT_all = (a.cvn * E + kBKB - 1) / kBKB;
+  const int kt0 = split * a.kt_per_part;
+  const int KT = max(min(KT_all - kt0, a.kt_per_part), 0);
+  const int v_off = kt0 * (kBKB / E);
+  OperandDesc da, db;
+  const uint32_t ldw = (uint32_t)a.H * E, ldd = (uint32_t)a.ldD * E;
+  const int vrows = max(min(a.V - a.cv0, a.cvn) - v_off, 0);
+  da.base = a.weight + ((size_t)(a.cv0 + v_off) * a.H + h0) * E;
+  da.ld_bytes = ldw;
+  da.nrec = vrows > 0 ? (uint32_t)((size_t)vrows * ldw - (size_t)h0 * E) : 0u;
+  da.cols_valid = a.H - h0;
+  da.k_bytes = 0;
+  db.base = a.D + (size_t)t0 * ldd + (size_t)v_off * E;
+  db.ld_bytes = ldd;
+  db.nrec = 64u * ldd - (uint32_t)v_off * E;
+  db.cols_valid = 0;
+  db.k_bytes = (a.cvn - v_off) * E;
+  Acc acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+    for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
+  small::mainloop<T, false, true, 64>(da, db, KT, lds, acc);
+  const float inv = a.dscale[1];
+#pragma unroll
+  for (int ni = 0; ni < NI; ni++) {
+    const int t = t0 + (wn * NI + ni) * 16 + (lane & 15);
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++) {
+      const int h = h0 + (wm * MI + mi) * 16 + 4 * (lane >> 4);
+      if (t >= a.N || h >= a.H) continue;
+      const size_t o = (size_t)t * a.H + h;
+      float c[4], prev[4];
+#pragma unroll
+      for (int r = 0; r < 4; r++) c[r] = acc[mi][ni][r] * inv;
+      if (a.parts > 1) {   // partial of this split; the reduction applies the mode
+        put4<float>(a.part + (size_t)split * a.N * a.H + o, c);
+        continue;
+      }
+      if (a.mode == 1 || a.mode == 2) {
+        get4<float>(a.accb + o, prev);
+#pragma unroll
+        for (int r = 0; r < 4; r++) c[r] += prev[r];
+      }
+      if (a.mode <= 1 || a.out_f32) put4<float>((a.mode <= 1 ? a.accb : reinterpret_cast<float*>(a.out)) + o, c);
+      else put4<T>(reinterpret_cast<T*>(a.out) + o, c);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+template <typename T, int BN> static void lp_small_t(const Plan& pl, const LpTileArgs& a, int n_tt, hipStream_t st) {
+  const int nwg = n_tt * a.S;
+  if (pl.has_bias) {
+    if (pl.cap > 0) lp_small_kernel<T, true, true, BN><<<nwg, small::kThreadsS, 0, st>>>(a, n_tt);
+    else lp_small_kernel<T, true, false, BN><<<nwg, small::kThreadsS, 0, st>>>(a, n_tt);
+  } else {
+    if (pl.cap > 0) lp_small_kernel<T, false, true, BN><<<nwg, small::kThreadsS, 0, st>>>(a, n_tt);
+    else lp_small_kernel<T, false, false, BN><<<nwg, small::kThreadsS, 0, st>>>(a, n_tt);
+  }
+}
+template <typename T> static void lp_small_bn(const Plan& pl, int bn, const LpTileArgs& a, int n_tt, hipStream_t st) {
+  if (bn == 16) lp_small_t<T, 16>(pl, a, n_tt, st);
+  else lp_small_t<T, 64>(pl, a, n_tt, st);
+}
+void launch_lp_small(const Plan& pl, int bn, const LpTileArgs& a, int n_tt, hipStream_t st) {
+  if (pl.int8) lp_small_bn<int8_t>(pl, bn, a, n_tt, st);
+  else if (pl.dtype == FLCE_BF16) lp_small_bn<bf16>(pl, bn, a, n_tt, st);
+  else if (pl.dtype == FLCE_F16) lp_small_bn<f16>(pl, bn, a, n_tt, st);
+  else lp_small_bn<float>(pl, bn, a, n_tt, st);
+}
+
+template <typename T> static void dlogits_small_t(const Plan& pl, const DlogitsArgs& d, hipStream_t st) {
+  const int nwg = d.n_vt_c * d.n_tt;
+  if (pl.has_bias) {
+    if (pl.cap > 0) dlogits_small_kernel<T, true, true><<<nwg, small::kThreadsS, 0, st>>>(d);
+    else dlogits_small_kernel<T, true, false><<<nwg, small::kThreadsS, 0, st>>>(d);
+  } else {
+    if (pl.cap > 0) dlogits_small_kernel<T, false, true><<<nwg, small::kThreadsS, 0, st>>>(d);
+    else dlogits_small_kernel<T, false, false><<<nwg, small::kThreadsS, 0, st>>>(d);
+  }
+}
+void launch_dlogits_small(const Plan& pl, const DlogitsArgs& d, hipStream_t st) {
+  if (pl.dtype == FLCE_BF16) dlogits_small_t<bf16>(pl, d, st);
+  else if (pl.dtype == FLCE_F16) dlogits_small_t<f16>(pl, d, st);
+  else dlogits_small_t<float>(pl, d, st);
+}
+
+template <typename T> static void gw_small_t(const GwArgs& g, hipStream_t st) {
+  const int nwg = g.n_ht * g.n_vt_c;
+  if (g.gw_type == FLCE_BF16) gw_small_kernel<T, bf16><<<nwg, small::kThreadsS, 0, st>>>(g);
+  else if (g.gw_type == FLCE_F16) gw_small_kernel<T, f16><<<nwg, small::kThreadsS, 0, st>>>(g);
+  else gw_small_kernel<T, float><<<nwg, small::kThreadsS, 0, st>>>(g);
+}
+void launch_gw_small(int dtype, const GwArgs& g, hipStream_t st) {
+  if (dtype == FLCE_BF16) gw_small_t<bf16>(g, st);
+  else if (dtype == FLCE_F16) gw_small_t<f16>(g, st);
+  else gw_small_t<float>(g, st);
+}
+
+void launch_gh_small(int dtype, const GhArgs& h, hipStream_t st) {
+  const int nwg = h.n_ht * h.n_tt * h.parts;
+  if (dtype == FLCE_BF16) gh_small_kernel<bf16><<<nwg, small::kThreadsS, 0, st>>>(h);
+  else if (dtype == FLCE_F16) gh_small_kernel<f16><<<nwg, small::kThreadsS, 0, st>>>(h);
+  else gh_small_kernel<float><<<nwg, small::kThreadsS, 0, st>>>(h);
+  if (h.parts > 1) launch_gh_reduce(dtype, h, st);
+}
+
+}  // namespace flce
