@@ -15,10 +15,10 @@ import functools
 import math
 from typing import Optional
 
-from . import (DTYPES, REDUCTIONS, _dtype_name, _ptr, _stream_handle, flce_policy_backward,
+from . import (DTYPES, REDUCTIONS, _dtype_name, _ptr, flce_policy_backward,
                flce_policy_forward, flce_policy_params, flce_policy_workspace_size, flce_preference_backward,
                flce_preference_forward, flce_preference_params, flce_preference_workspace_size, flce_token_view)
-from .logprobs import on_device, raise_for
+from .logprobs import differentiable, on_device, raise_for, stream_handle
 
 PREFERENCE_TYPES = {"sigmoid": 0, "hinge": 1, "squared": 2}
 POLICY_REDUCTIONS = {**REDUCTIONS, "sequence_mean": 3}
@@ -46,43 +46,55 @@ def _check_tokens(logps, others, offsets, mask, constants, per_sequence=()):
     """Types, shapes, layout and device of the token tensors.  The kernels trust all of them.
     Returns (n_seqs, length, flags)."""
     import torch
+    dtype, shape, dev = logps.dtype, logps.shape, logps.device
     _dtype_name(logps)
-    for name, t in others:
-        if t is not None and t.dtype != logps.dtype:
-            raise TypeError(f"{name} dtype {t.dtype} differs from logps' {logps.dtype}")
-    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
-        raise TypeError(f"mask must be bool or uint8, not {mask.dtype}")
+    named = [("logps", logps), *((name, t) for name, t in others if t is not None)]
+    for name, t in named:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} dtype {t.dtype} differs from logps' {dtype}")
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"mask must be bool or uint8, not {mask.dtype}")
+        named.append(("mask", mask))
     flags = 0
     if offsets is None:
-        if logps.dim() != 2:
-            raise ValueError(f"logps must be (S, L), or (T,) with offsets, got {tuple(logps.shape)}")
-        n_seqs, length = logps.shape
+        if len(shape) != 2:
+            raise ValueError(f"logps must be (S, L), or (T,) with offsets, got {tuple(shape)}")
+        n_seqs, length = shape
     else:
         if offsets.dtype not in (torch.int64, torch.int32):
             raise TypeError(f"offsets must be int64 or int32, not {offsets.dtype}")
         if offsets.dim() != 1 or offsets.shape[0] < 1:
             raise ValueError(f"offsets must hold S + 1 values, got shape {tuple(offsets.shape)}")
-        if logps.dim() != 1:
-            raise ValueError(f"packed logps must be (T,), got {tuple(logps.shape)}")
-        n_seqs, length = offsets.shape[0] - 1, logps.shape[0]
-        flags |= FLCE_OFFSETS_INT32 if offsets.dtype == torch.int32 else 0
-    named = [("logps", logps), *others, ("mask", mask)]
+        if len(shape) != 1:
+            raise ValueError(f"packed logps must be (T,), got {tuple(shape)}")
+        n_seqs, length = offsets.shape[0] - 1, shape[0]
+        flags = FLCE_OFFSETS_INT32 if offsets.dtype == torch.int32 else 0
+        if not offsets.is_contiguous():
+            raise ValueError("offsets must be contiguous")
     for name, t in named:
-        if t is not None and t.shape != logps.shape:
-            raise ValueError(f"{name} must have logps' shape {tuple(logps.shape)}, got {tuple(t.shape)}")
-    for name, t in named:
-        if t is not None:
+        if t.shape != shape:
+            raise ValueError(f"{name} must have logps' shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
             _check_rows(t, name)
-    if offsets is not None and not offsets.is_contiguous():
-        raise ValueError("offsets must be contiguous")
-    for name, t in [*named, ("offsets", offsets), *per_sequence]:
-        if t is not None and (t.device.type != "cuda" or t.device != logps.device):
-            raise ValueError(f"{name} must be on logps' GPU ({logps.device}), not {t.device}")
+    for name, t in (*named, ("offsets", offsets), *per_sequence):
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError(f"{name} must be on logps' GPU ({dev}), not {t.device}")
     if torch.is_grad_enabled():
         for name, t in constants:
             if t is not None and t.requires_grad:
                 raise ValueError(f"{name} is a constant of the loss and gets no gradient: detach it")
     return n_seqs, length, flags
+
+
+@functools.lru_cache(maxsize=1024)
+def _preference_workspace(n_seqs, length):
+    return flce_preference_workspace_size(flce_preference_params(n_seqs, length, beta=1.0))
+
+
+@functools.lru_cache(maxsize=1024)
+def _policy_workspace(n_seqs, length):
+    return flce_policy_workspace_size(flce_policy_params(n_seqs, length))
 
 
 # ----------------------------------------------------------------------------- preference loss
@@ -92,14 +104,14 @@ def _preference_forward(p, logps, ref, mask, offsets):
     dev = logps.device
     pairs = p.n_seqs // 2
     with on_device(dev):
-        ws_bytes = flce_preference_workspace_size(p)
+        ws_bytes = _preference_workspace(p.n_seqs, p.length)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         loss = torch.empty((pairs,) if p.reduction == 0 else (), dtype=torch.float32, device=dev)
         rewards = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
         seq_grad = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
         raise_for(flce_preference_forward(p, _view(logps), _view(ref), _view(mask), _ptr(offsets), _ptr(loss),
                                            _ptr(rewards), _ptr(seq_grad), _ptr(workspace), ws_bytes,
-                                           _stream_handle(dev)), "flce_preference_forward")
+                                           stream_handle(dev)), "flce_preference_forward")
     return loss, rewards, seq_grad
 
 
@@ -129,7 +141,7 @@ def _preference_function():
             grad = torch.empty(shape, dtype=dtype, device=dev)
             with on_device(dev):
                 raise_for(flce_preference_backward(ctx.p, _ptr(g), _ptr(seq_grad), _view(mask), _ptr(offsets),
-                                                    _ptr(grad), _stream_handle(dev)), "flce_preference_backward")
+                                                    _ptr(grad), stream_handle(dev)), "flce_preference_backward")
             return grad, None, None, None, None
 
     return PreferenceLoss
@@ -167,7 +179,10 @@ def preference_loss(logps, ref_logps=None, *, offsets=None, mask=None, beta: flo
     p = flce_preference_params(n_seqs, length, DTYPES[_dtype_name(logps)], REDUCTIONS[reduction],
                                PREFERENCE_TYPES[loss_type], flags, 1 if length_normalize else 0, 0, beta,
                                label_smoothing, margin)
-    loss, rewards = _preference_function().apply(logps, ref_logps, mask, offsets, p)
+    if differentiable(logps):
+        loss, rewards = _preference_function().apply(logps, ref_logps, mask, offsets, p)
+    else:
+        loss, rewards, _ = _preference_forward(p, logps, ref_logps, mask, offsets)
     if not return_metrics:
         return loss
     return loss, {"chosen_rewards": rewards[:n_seqs // 2], "rejected_rewards": rewards[n_seqs // 2:]}
@@ -179,7 +194,7 @@ def _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets, need
     import torch
     dev = logps.device
     with on_device(dev):
-        ws_bytes = flce_policy_workspace_size(p)
+        ws_bytes = _policy_workspace(p.n_seqs, p.length)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         loss = torch.empty(logps.shape if p.reduction == 0 else (), dtype=torch.float32, device=dev)
         unit = torch.empty(logps.shape, dtype=torch.float32, device=dev) if needs_grad else None
@@ -188,7 +203,7 @@ def _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets, need
         adv = flce_token_view(advantages.data_ptr(), 0) if per_seq else _view(advantages)
         raise_for(flce_policy_forward(p, _view(logps), _view(old), _view(ref), _view(entropy), adv, _view(mask),
                                        _ptr(offsets), _ptr(loss), _ptr(unit), _ptr(weights), _ptr(metrics),
-                                       _ptr(workspace), ws_bytes, _stream_handle(dev)), "flce_policy_forward")
+                                       _ptr(workspace), ws_bytes, stream_handle(dev)), "flce_policy_forward")
     return loss, unit, weights
 
 
@@ -216,7 +231,7 @@ def _policy_function():
                      for need in ctx.needs_input_grad[:2]]
             with on_device(dev):
                 raise_for(flce_policy_backward(ctx.p, _ptr(g), _ptr(unit), _ptr(weights), _view(mask),
-                                                _ptr(offsets), _ptr(grads[0]), _ptr(grads[1]), _stream_handle(dev)),
+                                                _ptr(offsets), _ptr(grads[0]), _ptr(grads[1]), stream_handle(dev)),
                            "flce_policy_backward")
             return (*grads, None, None, None, None, None, None, None)
 
@@ -275,7 +290,10 @@ def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, o
     p = flce_policy_params(n_seqs, length, DTYPES[_dtype_name(logps)], POLICY_REDUCTIONS[reduction], flags, 0,
                            clip_low, clip_high, dual_clip or 0.0, kl_coef, entropy_coef)
     metrics = torch.empty(2, dtype=torch.int64, device=logps.device) if return_metrics else None
-    loss = _policy_function().apply(logps, entropy, old_logps, ref_logps, advantages, mask, offsets, p, metrics)
+    if differentiable(logps, entropy):
+        loss = _policy_function().apply(logps, entropy, old_logps, ref_logps, advantages, mask, offsets, p, metrics)
+    else:
+        loss, _, _ = _policy_forward(p, logps, old_logps, ref_logps, entropy, advantages, mask, offsets, False, metrics)
     if not return_metrics:
         return loss
     both = metrics.view(torch.float32)

@@ -255,9 +255,16 @@ __device__ __forceinline__ void sequence_sum(const Seqs& q, const SeqPart* slots
   }
   double x = 0.0;
   int64_t n = 0;
-  for (int64_t i = b + (lane & (group - 1)); i < e; i += group) {
-    x += slots[i].sum;
-    n += slots[i].count;
+  for (int64_t i = b + (lane & (group - 1)); i < e; i += 4 * group) {
+    SeqPart p[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) p[j] = slots[i + j * group < e ? i + j * group : i];   // four loads in flight
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (i + j * group < e) {
+        x += p[j].sum;
+        n += p[j].count;
+      }
   }
   for (int o = 1; o < group; o <<= 1) {
     x += __shfl_xor(x, o);
@@ -267,23 +274,29 @@ __device__ __forceinline__ void sequence_sum(const Seqs& q, const SeqPart* slots
   count = n;
 }
 
-// Sum of x over the 1024 threads of a workgroup, in a fixed order; every thread gets it.
-__device__ __forceinline__ double block_sum(double x, double* lds) {
+// Sums of N values over the 1024 threads of a workgroup, in a fixed order; every thread gets them.
+template <int N> __device__ __forceinline__ void block_sums(double (&x)[N], double (&lds)[16][4]) {
+  static_assert(N <= 4, "");
   const int tid = threadIdx.x;
-  x = wave_sum(x);
-  __syncthreads();
-  if ((tid & 63) == 0) lds[tid >> 6] = x;
-  __syncthreads();
-  double r = 0.0;
 #pragma unroll
-  for (int i = 0; i < 16; i++) r += lds[i];
-  return r;
+  for (int k = 0; k < N; k++) x[k] = wave_sum(x[k]);
+  __syncthreads();
+  if ((tid & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < N; k++) lds[tid >> 6][k] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; k++) {
+    x[k] = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; i++) x[k] += lds[i][k];
+  }
 }
 
 // Per pair: the margin, its loss, and the factor its two sequences' tokens get in
 // the gradient.  One workgroup: pairs are few next to tokens.
 __global__ __launch_bounds__(1024) void preference_pairs_kernel(PreferenceArgs a) {
-  __shared__ double lds[16];
+  __shared__ double lds[16][4];
   const int lane = lane_id();
   const int64_t P = a.q.S / 2;
   const int groups = 1024 / a.group, g = threadIdx.x / a.group;
@@ -327,9 +340,10 @@ __global__ __launch_bounds__(1024) void preference_pairs_kernel(PreferenceArgs a
       total += loss;
     }
   }
-  total = block_sum(total, lds);
+  double all[1] = {total};
+  block_sums(all, lds);
   if (threadIdx.x == 0 && a.reduction != FLCE_REDUCTION_NONE)
-    a.loss[0] = a.reduction == FLCE_REDUCTION_MEAN && P == 0 ? __builtin_nanf("") : (float)(total * over_pairs);
+    a.loss[0] = a.reduction == FLCE_REDUCTION_MEAN && P == 0 ? __builtin_nanf("") : (float)(all[0] * over_pairs);
 }
 
 // The gradient of a token is its sequence's factor times the upstream value.
@@ -477,10 +491,10 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(PolicyArgs a) {
 
 // The sum or mean, the weights of the tokens' losses in it, and the metrics.
 __global__ __launch_bounds__(1024) void policy_merge_kernel(PolicyArgs a) {
-  __shared__ double lds[16];
+  __shared__ double lds[16][4];
   const int tid = threadIdx.x, lane = lane_id();
   const Seqs& q = a.q;
-  double kl = 0.0, clipped = 0.0, kept = 0.0, total = 0.0;
+  double kl = 0.0, clipped = 0.0, kept = 0.0, total = 0.0, filled = 0.0;
   const bool sums = a.reduction == FLCE_REDUCTION_SEQUENCE_MEAN;
   for (int64_t w = tid; w < q.waves; w += 1024) {
     kl += a.parts[w].kl;
@@ -488,15 +502,10 @@ __global__ __launch_bounds__(1024) void policy_merge_kernel(PolicyArgs a) {
     kept += (double)a.parts[w].kept;
     if (!sums) total += a.slots[w].sum;
   }
-  kl = block_sum(kl, lds);
-  clipped = block_sum(clipped, lds);
-  kept = block_sum(kept, lds);
-  double weight = 1.0;
   if (sums) {
     const int groups = 1024 / a.group, g = tid / a.group;
     const bool lead = (tid & (a.group - 1)) == 0;
-    double filled = 0.0;
-    for (int64_t s0 = 0; s0 < q.S; s0 += groups) {
+    for (int64_t s0 = 0; s0 < q.S; s0 += groups) {   // whole waves stay in the loop
       const int64_t s = s0 + g < q.S ? s0 + g : q.S - 1;
       double x;
       int64_t n;
@@ -506,16 +515,25 @@ __global__ __launch_bounds__(1024) void policy_merge_kernel(PolicyArgs a) {
           total += x / (double)n;
           filled += 1.0;
         }
-        // the number of sequences is known only after this loop: its factor follows
+        // the number of sequences is known only after this loop: weights[0] holds its factor
         a.weights[1 + s] = n > 0 ? (float)(1.0 / (double)n) : 0.0f;
       }
     }
-    filled = block_sum(filled, lds);
-    weight = filled > 0.0 ? 1.0 / filled : 0.0;
+  }
+  double all[4] = {kl, clipped, kept, total};
+  block_sums(all, lds);
+  kl = all[0];
+  clipped = all[1];
+  kept = all[2];
+  total = all[3];
+  double weight = 1.0;
+  if (sums) {
+    double f[1] = {filled};
+    block_sums(f, lds);
+    weight = f[0] > 0.0 ? 1.0 / f[0] : 0.0;
   } else if (a.reduction == FLCE_REDUCTION_MEAN) {
     weight = kept > 0.0 ? 1.0 / kept : 0.0;
   }
-  total = block_sum(total, lds);
   if (tid == 0) {
     a.weights[0] = (float)weight;
     if (a.reduction != FLCE_REDUCTION_NONE) a.loss[0] = weight > 0.0 ? (float)(total * weight) : __builtin_nanf("");

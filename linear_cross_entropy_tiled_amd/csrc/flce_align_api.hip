@@ -35,11 +35,12 @@ static int plan_seqs(int64_t S, int64_t length, bool packed, Seqs* q) {
 
 static int64_t slot_count(const Seqs& q) { return q.waves + (q.packed ? q.S : 0); }
 
-// Lanes that add one sequence's slots: the average number of slots, as a power of two.
+// Lanes that add one sequence's slots, a power of two: four slots to a lane on average,
+// whose loads it has in flight together.
 static int slot_group(const Seqs& q) {
   const int64_t each = q.S > 0 ? (q.waves + q.S - 1) / q.S : 1;
   int g = 1;
-  while (g < 64 && g < each) g *= 2;
+  while (g < 64 && 4 * g < each) g *= 2;
   return g;
 }
 

@@ -303,10 +303,11 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   else if (small_is_faster(P, P.n_tt * P.n_vt, n64 * v64, 1.0, 1.0)) L.bn = 64;
   if (L.bn) {
     L.n_tt = (int)((P.N + L.bn - 1) / L.bn);
-    int64_t S = L.n_tt > 0 ? wg_target / L.n_tt : 1;
-    if (S < 1) S = 1;
-    if (S > v64) S = v64;
-    L.S = (int)S;
+    // whole vocabulary tiles to a workgroup, rounded down: more workgroups than fit at once
+    // even out, a workgroup with one tile more than the others is waited for
+    int64_t each = v64 * L.n_tt / wg_target;
+    if (each < 1) each = 1;
+    L.S = (int)((v64 + each - 1) / each);
     L.N_pad = L.n_tt * L.bn;
   } else {
     L.n_tt = (int)P.n_tt;

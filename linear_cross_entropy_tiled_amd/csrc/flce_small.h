@@ -3,9 +3,8 @@
 // by 4 waves, BN 64 (2 x 2 waves of 32 x 32) or 16 (4 x 1 waves of 16 x 16).
 //
 // Operands, fragments and accumulator layout are those of the large loop (stages of
-// 128 bytes of K per row, K-major or M/N-major); kStages stage buffers keep kStages - 1
-// stages of loads in flight under one barrier a stage, and several workgroups share a
-// CU.  A 64 x 64 tile reads its fragments twice as often per matrix operation as the
+// 128 bytes of K per row, K-major or M/N-major); n stage buffers keep n - 1 stages of
+// loads in flight under one barrier a stage, and several workgroups share a CU.  A 64 x 64 tile reads its fragments twice as often per matrix operation as the
 // large tile, which costs the 16-bit types about half their rate and fp32, whose
 // matrix instructions take 16 times as long per byte, nothing.
 #pragma once
@@ -17,9 +16,12 @@ namespace small {
 
 constexpr int kBMs = 64;
 constexpr int kThreadsS = 256;
-constexpr int kStages = 4;
 constexpr int kStageA = kBMs * kBKB;                             // 8 KiB
+// Stage buffers: BN 16 streams the weight and wants loads in flight (40 KiB, four
+// workgroups to a CU); BN 64 wants a third workgroup on the CU more (48 KiB).
+constexpr int stages(int bn) { return bn == 16 ? 4 : 3; }
 constexpr int stage_bytes(int bn) { return (kBMs + bn) * kBKB; }
+constexpr int lds_bytes(int bn) { return stages(bn) * stage_bytes(bn); }
 
 template <int BN> struct Shape {
   static constexpr int WM = BN == 64 ? 2 : 4, WN = 4 / WM;       // waves
@@ -126,14 +128,14 @@ template <int N> __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | N);
 }
 
-// The loop.  lds: kStages x stage_bytes(BN).  No load is in flight and every wave has
+// The loop.  lds: lds_bytes(BN).  No load is in flight and every wave has
 // passed its last LDS read when it returns after the caller's next barrier; acc must be
 // zeroed by the caller.
 template <typename T, bool A_KMAJOR, bool B_KMAJOR, int BN>
 __device__ __forceinline__ void mainloop(const OperandDesc& da, const OperandDesc& db, int KT, char* lds,
                                          Acc (&acc)[Shape<BN>::MI][Shape<BN>::NI]) {
   typedef Shape<BN> S;
-  constexpr int SB = stage_bytes(BN);
+  constexpr int SB = stage_bytes(BN), kStages = stages(BN);
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -17,7 +17,7 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
   constexpr bool I8 = E == 1;
   typedef typename BiasOf<T>::type B;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(BN)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(BN)];
   static __shared__ float xs[Sh::WM][4][BN];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int tt = L % n_tt, s = L / n_tt;
@@ -163,7 +163,7 @@ template <typename T, bool HAS_BIAS, bool SOFTCAP>
 __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(DlogitsArgs a) {
   typedef Shape<64> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(64)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(64)];
   static __shared__ float gbs[Sh::WN][64];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int tt = L % a.n_tt, vt = L / a.n_tt;
@@ -252,7 +252,7 @@ template <typename T, typename OutT>
 __global__ __launch_bounds__(small::kThreadsS) void gw_small_kernel(GwArgs a) {
   typedef Shape<64> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(64)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(64)];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int ht = L % a.n_ht, vt = L / a.n_ht;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -306,7 +306,7 @@ template <typename T>
 __global__ __launch_bounds__(small::kThreadsS) void gh_small_kernel(GhArgs a) {
   typedef Shape<64> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::kStages * small::stage_bytes(64)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(64)];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int n_tiles = a.n_ht * a.n_tt, split = L / n_tiles, in = L - split * n_tiles;
   const int tt = in % a.n_tt, ht = in / a.n_tt;

@@ -11,12 +11,28 @@ from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError
                flce_logprobs_int8_workspace_size, flce_logprobs_workspace_size, flce_quantize_int8, make_params)
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def on_device(device):
     """The library launches on the current device: makes it the tensors'."""
     import torch
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _SAME_DEVICE
     return torch.cuda.device(device)
+
+
+def stream_handle(device):
+    """The current stream of a GPU, without a torch.cuda.Stream object around it (3 us)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _stream_handle(device) if raw is None or device.index is None else raw(device.index)
+
+
+def differentiable(*tensors) -> bool:
+    """Whether autograd records this call (without, the autograd op's own cost is saved)."""
+    import torch
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def raise_for(rc, where):
@@ -32,7 +48,7 @@ def _forward(p, hidden, weight, bias, targets):
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         logps, entropy, lse = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(3))
         raise_for(flce_logprobs_forward(p, _ptr(hidden), _ptr(weight), _ptr(bias), _ptr(targets), _ptr(logps),
-                                        _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes, _stream_handle(dev)),
+                                        _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes, stream_handle(dev)),
                   "flce_logprobs_forward")
     return logps, entropy, lse
 
@@ -71,7 +87,7 @@ def _function():
                 gb = None if bias is None else torch.empty_like(bias)
                 raise_for(flce_logprobs_backward(ctx.p, _ptr(hidden), _ptr(weight), _ptr(bias), _ptr(targets),
                                                  _ptr(lse), _ptr(entropy), _ptr(g), _ptr(h), _ptr(gh), _ptr(gw),
-                                                 _ptr(gb), _ptr(workspace), ws_bytes, _stream_handle(dev)),
+                                                 _ptr(gb), _ptr(workspace), ws_bytes, stream_handle(dev)),
                           "flce_logprobs_backward")
             return gh, gw, gb, None, None
 
@@ -90,7 +106,10 @@ def token_logprobs(hidden, weight, targets, bias=None, *, logit_scale: float = 1
     p = make_params(hidden.shape[0], hidden.shape[1], weight.shape[0], dtype=dt, logit_scale=logit_scale,
                     softcap=softcap, ignore_index=ignore_index, reduction="none",
                     targets_int32=_targets_int32(targets), vocab_chunk=vocab_chunk)
-    logps, entropy = _function().apply(hidden, weight, bias, targets, p)
+    if differentiable(hidden, weight, bias):
+        logps, entropy = _function().apply(hidden, weight, bias, targets, p)
+    else:
+        logps, entropy, _ = _forward(p, hidden, weight, bias, targets)
     return (logps, entropy) if return_entropy else logps
 
 
@@ -103,7 +122,7 @@ def _quantize(x):
         q = torch.empty(x.shape, dtype=torch.int8, device=dev)
         scale = torch.empty(x.shape[0], dtype=torch.float32, device=dev)
         raise_for(flce_quantize_int8(DTYPES[_dtype_name(x)], _ptr(x), x.shape[0], x.shape[1], _ptr(q), _ptr(scale),
-                                     _stream_handle(dev)), "flce_quantize_int8")
+                                     stream_handle(dev)), "flce_quantize_int8")
     return q, scale
 
 
@@ -183,5 +202,5 @@ def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hid
         logps, entropy, lse = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(3))
         raise_for(flce_logprobs_int8(p, _ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale), _ptr(bias),
                                      _ptr(targets), _ptr(logps), _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes,
-                                     _stream_handle(dev)), "flce_logprobs_int8")
+                                     stream_handle(dev)), "flce_logprobs_int8")
     return (logps, entropy) if return_entropy else logps
