@@ -288,33 +288,59 @@ int plan_forward_backward(Plan* pl, int64_t block_rows) {
 // ---------------------------------------------------------------------------
 static double small_rate(const Plan& P) { return P.int8 ? 0.35 : (P.dtype == FLCE_F32 ? 0.8 : 0.4); }
 
+// Time of tiles in units of (rows x columns of a large tile's pass over K by one CU).
+static double large_time(int64_t tiles256) { return (double)((tiles256 + 255) / 256) * 65536.0; }
+static double small_time(const Plan& P, int64_t tiles64) {
+  return (double)((tiles64 + 255) / 256) * 4096.0 / small_rate(P);
+}
+
 static bool small_is_faster(const Plan& P, int64_t tiles256, int64_t tiles64, double k256, double k64) {
-  const double big = (double)((tiles256 + 255) / 256) * 65536.0 * k256;
-  const double small = (double)((tiles64 + 255) / 256) * 4096.0 * k64 / small_rate(P);
-  return small < big;
+  return small_time(P, tiles64) * k64 < large_time(tiles256) * k256;
+}
+
+// How many of n_vt vocabulary tiles to run large, the others (and the ragged last one's
+// rows) small: all, none, or as many as fill whole rounds of the CUs, so that a last
+// round of few large tiles (3.06 rounds take as long as 4) becomes a short one of small
+// tiles.  A second launch costs about 4 us, and a round of large tiles 13 ns per byte of
+// hidden size (16 and 8 bits; fp32 rounds are longer still).
+static int64_t large_vocab_tiles(const Plan& P, int64_t V) {
+  const int64_t n_tt = P.n_tt, n_vt = (V + 255) / 256, n64 = (P.N + 63) / 64;
+  const double launch = 65536.0 * 300.0 / ((double)P.H * P.esize);
+  int64_t best = n_vt;
+  double time = large_time(n_tt * n_vt);
+  const int64_t whole = n_tt > 0 ? n_tt * n_vt / 256 : 0;   // whole rounds
+  const int64_t tried[3] = {0, whole - 1, whole};
+  for (int k = 0; k < 3; k++) {
+    const int64_t n = tried[k] > 0 ? tried[k] * 256 / n_tt : 0;
+    if (n >= n_vt) break;
+    const double t = large_time(n_tt * n) + small_time(P, n64 * ((V - n * 256 + 63) / 64)) + (n > 0 ? launch : 0.0);
+    if (t < time) {
+      best = n;
+      time = t;
+    }
+  }
+  return best;
 }
 
 void plan_logprobs(const Plan& P, LpPlan* out) {
   LpPlan& L = *out;
   memset(&L, 0, sizeof(L));
-  const int64_t n64 = (P.N + 63) / 64, v64 = (P.V + 63) / 64, h64 = (P.H + 63) / 64;
+  const int64_t n64 = (P.N + 63) / 64, h64 = (P.H + 63) / 64;
   const int64_t wg_target = 3 * kTargetWorkgroups;   // small workgroups that share the chip
-  if (P.N <= 16) L.bn = 16;
-  else if (small_is_faster(P, P.n_tt * P.n_vt, n64 * v64, 1.0, 1.0)) L.bn = 64;
-  if (L.bn) {
-    L.n_tt = (int)((P.N + L.bn - 1) / L.bn);
+  L.bn = P.N <= 16 ? 16 : 64;
+  L.vt_large = P.N <= 16 ? 0 : (int)large_vocab_tiles(P, P.V);
+  if (L.vt_large > 0) L.S_large = forward_splits(P.n_tt, L.vt_large);
+  const int64_t rest = P.V - int64_t(L.vt_large) * 256;
+  if (rest > 0) {
     // whole vocabulary tiles to a workgroup, rounded down: more workgroups than fit at once
     // even out, a workgroup with one tile more than the others is waited for
-    int64_t each = v64 * L.n_tt / wg_target;
+    const int64_t v64 = (rest + 63) / 64;
+    int64_t each = v64 * ((P.N + L.bn - 1) / L.bn) / wg_target;
     if (each < 1) each = 1;
-    L.S = (int)((v64 + each - 1) / each);
-    L.N_pad = L.n_tt * L.bn;
-  } else {
-    L.n_tt = (int)P.n_tt;
-    L.S = P.S;
-    L.N_pad = (int)P.N_pad;
+    L.S_small = (int)((v64 + each - 1) / each);
   }
-  L.f_bytes = align_up(kStatusBytes + size_t(4) * L.S * L.N_pad * 4, 256);
+  L.N_pad = L.vt_large > 0 ? (int)P.N_pad : (int)((P.N + L.bn - 1) / L.bn * L.bn);
+  L.f_bytes = align_up(kStatusBytes + size_t(4) * (L.S_large + L.S_small) * L.N_pad * 4, 256);
 
   L.n64 = (int)n64;
   L.N64 = (int)(n64 * 64);

@@ -8,8 +8,11 @@ namespace flce {
 // How a log-probability call runs: which kernels, and its workspace (offsets; the
 // backward's regions follow the loss backward's, b_*).
 struct LpPlan {
-  int bn;                 // forward: 0 = 256 x 256 tiles, else 64 x bn
-  int S, N_pad, n_tt;     // vocabulary splits, padded tokens, token tiles
+  // forward: the first vt_large vocabulary tiles run as 256 x 256 tiles in S_large
+  // splits, the rest of the vocabulary as 64 x bn tiles in S_small splits
+  int bn;
+  int vt_large, S_large, S_small;
+  int N_pad;
   size_t f_bytes;
 
   bool d_small, gw_small, gh_small;
@@ -37,8 +40,10 @@ struct LpTileArgs {
   int N, H, V;
   int64_t ignore_index;
   float scale, cap, two_log2e_over_cap;
-  int n_vt, S, N_pad;         // vocabulary tiles (256 or 64 rows)
-  float* part;                // [4][S][N_pad]: m, l, T, y_t
+  int v_first;                // first vocabulary row of the launch
+  int n_vt, S;                // its vocabulary tiles (256 or 64 rows) and splits
+  int S_all, s_first, N_pad;
+  float* part;                // [4][S_all][N_pad]: m, l, T, y_t; this launch's splits from s_first on
   int* status;                // set to FLCE_OK here; lp_rows_kernel reports bad targets
 };
 

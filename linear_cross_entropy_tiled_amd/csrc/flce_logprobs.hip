@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
 
   Acc acc[kMI][kNI];
   for (int vt = vt_begin; vt < vt_end; ++vt) {
-    const int v0 = vt * 256;
+    const int v0 = a.v_first + vt * 256;
     const char* bias_tile = bias_lds[(vt - vt_begin) & 1];
     if (HAS_BIAS && wave == 0)
       dma_vector(reinterpret_cast<const B*>(a.bias) + v0, ((uint32_t)min(a.V - v0, 256) * BE + 3u) & ~3u,
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   }
   __syncthreads();
   if (wm == 0 && lane < 16) {
-    const size_t plane = (size_t)a.S * a.N_pad;
+    const size_t plane = (size_t)a.S_all * a.N_pad;
 #pragma unroll
     for (int ni = 0; ni < kNI; ni++) {
       const int c = acc_col(ni, lane);
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
       o.T = p[2 * kWaveN];
       o.yt = p[3 * kWaveN];
       lp_merge(st[ni], o);
-      float* out = a.part + (size_t)s * a.N_pad + t0 + wn * kWaveN + c;
+      float* out = a.part + (size_t)(a.s_first + s) * a.N_pad + t0 + wn * kWaveN + c;
       out[0] = st[ni].m;
       out[plane] = st[ni].l;
       out[2 * plane] = st[ni].T;
@@ -418,27 +418,38 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
     a.scale = pl.scale;
     a.cap = pl.cap;
     a.two_log2e_over_cap = pl.cap > 0 ? 2.0f * kLog2e / pl.cap : 0.0f;
-    a.n_vt = lp.bn ? (int)((pl.V + 63) / 64) : (int)pl.n_vt;
-    a.S = lp.S;
+    a.S_all = lp.S_large + lp.S_small;
     a.N_pad = lp.N_pad;
     a.part = part;
     a.status = status;
-    const int nwg = lp.n_tt * lp.S;
-    if (lp.bn) launch_lp_small(pl, lp.bn, a, lp.n_tt, st);
-    else if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
-    else if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
-    else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);
-    else launch_lp_tiles<float>(pl, a, nwg, st);
+    if (lp.vt_large > 0) {
+      a.v_first = 0;
+      a.n_vt = lp.vt_large;
+      a.S = lp.S_large;
+      a.s_first = 0;
+      const int nwg = (int)pl.n_tt * a.S;
+      if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
+      else if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
+      else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);
+      else launch_lp_tiles<float>(pl, a, nwg, st);
+    }
+    if (lp.S_small > 0) {
+      a.v_first = lp.vt_large * 256;
+      a.n_vt = (a.V - a.v_first + 63) / 64;
+      a.S = lp.S_small;
+      a.s_first = lp.S_large;
+      launch_lp_small(pl, lp.bn, a, (a.N + lp.bn - 1) / lp.bn, st);
+    }
   }
   LpRowArgs r;
   r.targets = targets;
   r.tgt_i32 = pl.tgt_i32 ? 1 : 0;
   r.N = (int)pl.N;
   r.V = (int)pl.V;
-  r.S = lp.S;
+  r.S = lp.S_large + lp.S_small;
   r.N_pad = lp.N_pad;
   r.group = 1;
-  while (r.group < 64 && r.group < lp.S) r.group *= 2;
+  while (r.group < 64 && r.group < r.S) r.group *= 2;
   r.ignore_index = pl.ignore_index;
   r.part = part;
   r.logps = logps;

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
   const int KT = (a.H * E + kBKB - 1) / kBKB;
 
   for (int vt = vt_begin; vt < vt_end; ++vt) {
-    const int v0 = vt * 64;
+    const int v0 = a.v_first + vt * 64;
     OperandDesc da;
     da.base = a.weight + (size_t)v0 * ld;
     da.ld_bytes = ld;
@@ -133,8 +133,8 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
     LpState r{xs[0][0][tid], xs[0][1][tid], xs[0][2][tid], xs[0][3][tid]};
 #pragma unroll
     for (int w = 1; w < Sh::WM; w++) lp_merge(r, LpState{xs[w][0][tid], xs[w][1][tid], xs[w][2][tid], xs[w][3][tid]});
-    const size_t plane = (size_t)a.S * a.N_pad;
-    float* out = a.part + (size_t)s * a.N_pad + t0 + tid;
+    const size_t plane = (size_t)a.S_all * a.N_pad;
+    float* out = a.part + (size_t)(a.s_first + s) * a.N_pad + t0 + tid;
     out[0] = r.m;
     out[plane] = r.l;
     out[2 * plane] = r.T;

@@ -179,3 +179,17 @@ def test_empty_batch_streams_and_capture(flce_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(outs, ref)), rep
+
+
+def test_last_round_of_tiles_runs_small(flce_lib):
+    """As in test_gpu_token_logprobs.py: 282 large tiles, the last 26 of them run as small ones."""
+    n, h, v = 300, 1024, 36000
+    x, w, b, t = _problem(n, h, v, seed=22)
+    t[0], t[1], t[2] = v - 1, 33000, 32767
+    p = flce_lib.make_params(n, h, v, reduction="none")
+    assert (flce_lib.flce_logprobs_int8_workspace_size(p) - 256) / 16 / 512 > 128
+    wq, ws = flce_lib.quantize_int8(w.cuda())
+    lp, ent = flce_lib.token_logprobs_int8(x.cuda(), wq, ws, t.cuda(), b.cuda(), return_entropy=True)
+    q, s = ao.quantize_int8(x.float().numpy())
+    _check(_np(lp), _np(ent), q, s.astype(np.float64), wq.cpu().numpy(), _np(ws), _np(b), t.numpy(),
+           rows=np.r_[0:3, 3:300:17])

@@ -322,3 +322,20 @@ def test_ordinary_head_on_sampled_rows(flce_lib, dtype):
     lp, ent = flce_lib.token_logprobs(d["hidden"], d["weight"], d["targets"], d["bias"], return_entropy=True)
     rows = np.arange(0, 2000, 37)
     _check_values(_np(lp)[rows], _np(ent)[rows], X[rows], W, B, inp["targets"][rows], dtype, {})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_last_round_of_tiles_runs_small(flce_lib, dtype):
+    """N = 300 or 512, V = 36000: 282 large tiles on 256 CUs, of which whole rounds run large and the rest of
+    the vocabulary small, in splits of its own (seen in the workspace: 16 bytes per split and padded row; fp32
+    would run all of N = 300 small)."""
+    import torch
+    n, h, v = 512 if dtype == "f32" else 300, 512, 36000
+    x, w, b, t = _tensors(n, h, v, dtype, seed=21)
+    t[:4] = torch.tensor([v - 1, 0, 33000, 32767])          # on both sides of the seam
+    p = flce_lib.make_params(n, h, v, dtype=dtype, reduction="none")
+    splits = (flce_lib.flce_logprobs_workspace_size(p, 0) - 256) / 16 / 512
+    assert splits > 128, splits
+    lp, ent = flce_lib.token_logprobs(x.cuda(), w.cuda(), t.cuda(), b.cuda(), return_entropy=True)
+    rows = np.r_[0:4, 4:n:17]
+    _check_values(_np(lp)[rows], _np(ent)[rows], _np(x)[rows], _np(w), _np(b), t.numpy()[rows], dtype, {})
