@@ -194,8 +194,9 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
           else x = u - m_new;
           if (ragged && 16 * mi + r >= lim) x = kMasked;
           const float e = fast_exp2(x);
-          // a logit of -inf has e = 0 and is to add 0, not 0 times infinity
-          const float xf = fmaxf(x, kMasked);
+          // a logit of -inf (there is none with the cap, nor of 8-bit products without a
+          // bias) has e = 0 and is to add 0, not 0 times infinity
+          const float xf = SOFTCAP || (I8 && !HAS_BIAS) ? x : fmaxf(x, kMasked);
           if (r & 1) {
             se1 += e;
             sx1 = fmaf(e, xf, sx1);
