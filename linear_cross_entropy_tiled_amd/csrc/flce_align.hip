@@ -130,28 +130,33 @@ __device__ __forceinline__ void store_tokens(T* p, int n, int lane, const float*
       if (tok<VEC>(j, lane) < n) p[tok<VEC>(j, lane)] = (T)v[j];
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load_mask(const uint8_t* p, int n, int lane, bool* keep) {
-  if (VEC && tok<true>(3, lane) < n) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p + 4 * lane);
+// The lane's four mask bytes, one above the other.
+template <bool VEC> __device__ __forceinline__ uint32_t load_mask(const uint8_t* p, int n, int lane) {
+  if (VEC && tok<true>(3, lane) < n) return *reinterpret_cast<const uint32_t*>(p + 4 * lane);
+  uint32_t v = 0;
 #pragma unroll
-    for (int j = 0; j < 4; j++) keep[j] = keep[j] && ((v >> (8 * j)) & 0xFF) != 0;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; j++) keep[j] = keep[j] && tok<VEC>(j, lane) < n && p[tok<VEC>(j, lane)] != 0;
-  }
+  for (int j = 0; j < 4; j++)
+    if (tok<VEC>(j, lane) < n) v |= (uint32_t)p[tok<VEC>(j, lane)] << (8 * j);
+  return v;
 }
+
+// A step's inputs: up to K token tensors and the mask, loaded one step ahead of their
+// use (a step's arithmetic is short next to a load's latency).
+template <int K> struct StepIn {
+  float x[K][4];
+  uint32_t mask;
+};
 
 // The step's tokens: which count, and (packed, when `walk` is used) in which
 // sequence each lies.  Moves the walk to the sequence of the step's last token.
 template <bool PACKED, bool VEC>
-__device__ __forceinline__ void step_tokens(const Seqs& q, const Chunk& c, int64_t t, int n, bool by_seq, SeqWalk& walk,
-                                            int64_t first, int64_t last, int lane, bool (&keep)[4],
+__device__ __forceinline__ void step_tokens(const Seqs& q, const Chunk& c, int64_t t, int n, uint32_t mask, bool by_seq,
+                                            SeqWalk& walk, int64_t first, int64_t last, int lane, bool (&keep)[4],
                                             int64_t (&seq)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     const int64_t at = t + tok<VEC>(j, lane);
-    keep[j] = tok<VEC>(j, lane) < n && (!PACKED || (at >= first && at < last));
+    keep[j] = tok<VEC>(j, lane) < n && (!PACKED || (at >= first && at < last)) && ((mask >> (8 * j)) & 0xFF) != 0;
     seq[j] = PACKED ? walk.s : c.row;
   }
   if (PACKED && by_seq) {
@@ -162,7 +167,14 @@ __device__ __forceinline__ void step_tokens(const Seqs& q, const Chunk& c, int64
         if (t + tok<VEC>(j, lane) >= edge) seq[j] = walk.s;
     }
   }
-  if (q.mask) load_mask<VEC>(q.mask + c.row * q.ld_mask + t, n, lane, keep);
+}
+
+// Tokens of the step at t (0 past the chunk), and their mask bytes (no mask: all set).
+__device__ __forceinline__ int step_size(const Chunk& c, int64_t t) {
+  return (int)(c.end - t < 256 ? (c.end > t ? c.end - t : 0) : 256);
+}
+template <bool VEC> __device__ __forceinline__ uint32_t step_mask(const Seqs& q, const Chunk& c, int64_t t, int n, int lane) {
+  return q.mask ? load_mask<VEC>(q.mask + c.row * q.ld_mask + t, n, lane) : 0x01010101u;
 }
 
 // Running sum of the sequence a wave is in, and its flush into a slot.
@@ -219,17 +231,24 @@ __global__ __launch_bounds__(256) void preference_tokens_kernel(PreferenceArgs a
   acc.clear();
   const T* lp = reinterpret_cast<const T*>(a.logps) + c.row * a.ld_logps;
   const T* ref = a.ref ? reinterpret_cast<const T*>(a.ref) + c.row * a.ld_ref : nullptr;
-  for (int64_t t = c.begin; t < c.end; t += 256) {
-    const int n = (int)(c.end - t < 256 ? c.end - t : 256);
-    float x[4], r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    load_tokens<T, VEC>(lp + t, n, lane, x);
-    if (ref) load_tokens<T, VEC>(ref + t, n, lane, r);
+  auto load = [&](int64_t t, StepIn<2>& in) {
+    const int n = step_size(c, t);
+    load_tokens<T, VEC>(lp + t, n, lane, in.x[0]);
+    if (ref) load_tokens<T, VEC>(ref + t, n, lane, in.x[1]);
+    in.mask = step_mask<VEC>(q, c, t, n, lane);
+  };
+  StepIn<2> in, ahead;
+  load(c.begin, in);
+  for (int64_t t = c.begin; t < c.end; t += 256, in = ahead) {
+    load(t + 256, ahead);
+    const int n = step_size(c, t);
     bool keep[4];
     int64_t seq[4];
     const int64_t from = walk.s;
-    step_tokens<PACKED, VEC>(q, c, t, n, true, walk, first, last, lane, keep, seq);
+    step_tokens<PACKED, VEC>(q, c, t, n, in.mask, true, walk, first, last, lane, keep, seq);
+    float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) x[j] -= r[j];
+    for (int j = 0; j < 4; j++) x[j] = ref ? in.x[0][j] - in.x[1][j] : in.x[0][j];
     acc.add(q, a.slots, w, from, PACKED ? walk.s : from, keep, seq, x, lane);
   }
   if (PACKED) {
@@ -361,11 +380,14 @@ __global__ __launch_bounds__(256) void preference_grad_kernel(PreferenceGradArgs
   walk.s = 0;
   if (PACKED) walk.seek(q, c.begin, lane);
   T* out = reinterpret_cast<T*>(a.grad_logps) + c.row * q.length;
+  uint32_t ahead = step_mask<VEC>(q, c, c.begin, step_size(c, c.begin), lane);
   for (int64_t t = c.begin; t < c.end; t += 256) {
-    const int n = (int)(c.end - t < 256 ? c.end - t : 256);
+    const int n = step_size(c, t);
+    const uint32_t mask = ahead;
+    ahead = step_mask<VEC>(q, c, t + 256, step_size(c, t + 256), lane);
     bool keep[4];
     int64_t seq[4];
-    step_tokens<PACKED, VEC>(q, c, t, n, true, walk, first, last, lane, keep, seq);
+    step_tokens<PACKED, VEC>(q, c, t, n, mask, true, walk, first, last, lane, keep, seq);
     float d[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -421,21 +443,28 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(PolicyArgs a) {
   const T* ref = a.ref ? reinterpret_cast<const T*>(a.ref) + c.row * a.ld_ref : nullptr;
   const T* ent = a.entropy ? reinterpret_cast<const T*>(a.entropy) + c.row * a.ld_entropy : nullptr;
   const float* adv = a.adv_per_seq ? a.adv : a.adv + c.row * a.ld_adv;
-  for (int64_t t = c.begin; t < c.end; t += 256) {
-    const int n = (int)(c.end - t < 256 ? c.end - t : 256);
-    float x[4], o[4], r[4] = {0.0f, 0.0f, 0.0f, 0.0f}, h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A[4];
-    load_tokens<T, VEC>(lp + t, n, lane, x);
-    load_tokens<T, VEC>(old + t, n, lane, o);
-    if (ref) load_tokens<T, VEC>(ref + t, n, lane, r);
-    if (ent) load_tokens<T, VEC>(ent + t, n, lane, h);
-    if (!a.adv_per_seq) load_tokens<float, VEC>(adv + t, n, lane, A);
+  auto load = [&](int64_t t, StepIn<5>& in) {
+    const int n = step_size(c, t);
+    load_tokens<T, VEC>(lp + t, n, lane, in.x[0]);
+    load_tokens<T, VEC>(old + t, n, lane, in.x[1]);
+    if (!a.adv_per_seq) load_tokens<float, VEC>(adv + t, n, lane, in.x[2]);
+    if (ref) load_tokens<T, VEC>(ref + t, n, lane, in.x[3]);
+    if (ent) load_tokens<T, VEC>(ent + t, n, lane, in.x[4]);
+    in.mask = step_mask<VEC>(q, c, t, n, lane);
+  };
+  StepIn<5> in, ahead;
+  load(c.begin, in);
+  for (int64_t t = c.begin; t < c.end; t += 256, in = ahead) {
+    load(t + 256, ahead);
+    const int n = step_size(c, t);
+    const float(&x)[4] = in.x[0], (&o)[4] = in.x[1], (&A)[4] = in.x[2], (&r)[4] = in.x[3], (&h)[4] = in.x[4];
     bool keep[4];
     int64_t seq[4];
     const int64_t from = walk.s;
-    step_tokens<PACKED, VEC>(q, c, t, n, by_seq, walk, first, last, lane, keep, seq);
+    step_tokens<PACKED, VEC>(q, c, t, n, in.mask, by_seq, walk, first, last, lane, keep, seq);
     if (a.adv_per_seq) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) A[j] = keep[j] ? adv[seq[j]] : 0.0f;
+      for (int j = 0; j < 4; j++) in.x[2][j] = keep[j] ? adv[seq[j]] : 0.0f;
     }
     float loss[4], grad[4];
 #pragma unroll
@@ -460,7 +489,7 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(PolicyArgs a) {
         d = fmaf(-a.kl_coef, em1, d);
         if (keep[j]) kl += (double)k;
       }
-      l = fmaf(-a.entropy_coef, h[j], l);
+      if (ent) l = fmaf(-a.entropy_coef, h[j], l);
       loss[j] = keep[j] ? l : 0.0f;
       grad[j] = keep[j] ? d : 0.0f;
       if (keep[j]) {
@@ -559,24 +588,27 @@ __global__ __launch_bounds__(256) void policy_grad_kernel(PolicyGradArgs a) {
   walk.s = 0;
   if (by_seq) walk.seek(q, c.begin, lane);
   const int64_t row = c.row * q.length;
-  for (int64_t t = c.begin; t < c.end; t += 256) {
-    const int n = (int)(c.end - t < 256 ? c.end - t : 256);
-    float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, g[4] = {g0, g0, g0, g0};
-    if (a.grad_logps) load_tokens<float, VEC>(a.unit_grad + row + t, n, lane, u);
-    if (a.per_token) {
-      load_tokens<float, VEC>(a.grad_loss + row + t, n, lane, g);
-#pragma unroll
-      for (int j = 0; j < 4; j++) g[j] *= g0;
-    }
+  auto load = [&](int64_t t, StepIn<2>& in) {
+    const int n = step_size(c, t);
+    if (a.grad_logps) load_tokens<float, VEC>(a.unit_grad + row + t, n, lane, in.x[0]);
+    if (a.per_token) load_tokens<float, VEC>(a.grad_loss + row + t, n, lane, in.x[1]);
+    in.mask = step_mask<VEC>(q, c, t, n, lane);
+  };
+  StepIn<2> in, ahead;
+  load(c.begin, in);
+  for (int64_t t = c.begin; t < c.end; t += 256, in = ahead) {
+    load(t + 256, ahead);
+    const int n = step_size(c, t);
     bool keep[4];
     int64_t seq[4];
-    step_tokens<PACKED, VEC>(q, c, t, n, by_seq, walk, first, last, lane, keep, seq);
+    step_tokens<PACKED, VEC>(q, c, t, n, in.mask, by_seq, walk, first, last, lane, keep, seq);
     float d[4], e[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      if (a.seq_weights) g[j] *= keep[j] ? a.weights[1 + seq[j]] : 0.0f;
-      d[j] = keep[j] ? g[j] * u[j] : 0.0f;
-      e[j] = keep[j] ? g[j] * -a.entropy_coef : 0.0f;
+      float g = a.per_token ? in.x[1][j] * g0 : g0;
+      if (a.seq_weights) g *= keep[j] ? a.weights[1 + seq[j]] : 0.0f;
+      d[j] = keep[j] && a.grad_logps ? g * in.x[0][j] : 0.0f;
+      e[j] = keep[j] ? g * -a.entropy_coef : 0.0f;
     }
     if (a.grad_logps) store_tokens<T, VEC>(reinterpret_cast<T*>(a.grad_logps) + row + t, n, lane, d);
     if (a.grad_entropy) store_tokens<T, VEC>(reinterpret_cast<T*>(a.grad_entropy) + row + t, n, lane, e);

@@ -190,7 +190,7 @@ def test_policy_abi_pointers_and_workspace():
 
 
 def test_workspace_counts_one_partial_sum_per_chunk_and_sequence():
-    # 16 bytes for each (chunk, sequence) pair that can meet: chunks of 256 tokens up to 4096 x 256 tokens
+    # 16 bytes for each (chunk, sequence) pair that can meet: chunks of 256 tokens up to 8192 x 256 tokens
     assert flce.flce_preference_workspace_size(_pp(n_seqs=2, length=256)) == 256
     assert flce.flce_preference_workspace_size(_pp(n_seqs=1000, length=512)) == (2000 * 16 + 255) // 256 * 256
     p = _pp(n_seqs=0, length=0)
