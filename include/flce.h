@@ -359,7 +359,8 @@ int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* 
  * Gradients of  sum_i grad_logps_i logp_i + grad_entropy_i H_i.
  *  lse, entropy: from the forward (entropy may be NULL without grad_entropy).
  *  grad_logps, grad_entropy: device fp32 (N); NULL = zeros.
- *  grad_hidden, grad_weight, grad_bias, flags: as flce_backward.
+ *  grad_hidden, grad_weight, grad_bias, flags: as flce_backward, except that each
+ *  may be NULL where it is not wanted (a frozen head, say), which saves its work.
  */
 int flce_logprobs_backward(const flce_params* p, const void* hidden, const void* weight, const void* bias,
                            const void* targets, const float* lse, const float* entropy, const float* grad_logps,

@@ -571,8 +571,8 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
   const int rc = logprobs_plan(p, false, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
-  if (!weight || !grad_weight || !workspace) return FLCE_ERR_INVALID_ARG;
-  if (pl.N > 0 && (!hidden || !targets || !lse || !grad_hidden)) return FLCE_ERR_INVALID_ARG;
+  if (!weight || !workspace) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && (!hidden || !targets || !lse)) return FLCE_ERR_INVALID_ARG;
   if (pl.N > 0 && grad_entropy && !entropy) return FLCE_ERR_INVALID_ARG;
   if (grad_bias && !bias) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) ||

@@ -577,7 +577,7 @@ hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGr
   lp_prep_kernel<<<1, 1024, 0, st>>>(a);
 
   char* hiddenT = ws + pl.b_xt;
-  if (pl.N > 0) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, lp.K_pad, hiddenT, st, a.tgt);
+  if (pl.N > 0 && grad_weight) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, lp.K_pad, hiddenT, st, a.tgt);
   float* gb_part = reinterpret_cast<float*>(ws + (lp.d_small ? lp.b_gbpart : pl.b_gbpart));
   const bool f32 = pl.dtype == FLCE_F32;
   for (int c = 0; c < pl.n_chunks; c++) {
@@ -628,9 +628,11 @@ hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGr
     w.accumulate = pl.accum_gw ? 1 : 0;
     w.acc32 = nullptr;
     w.mode = 3;
-    if (lp.gw_small) launch_gw_small(pl.dtype, w, st);
-    else launch_gw(pl.dtype, w, st);
-    if (pl.N > 0) {
+    if (grad_weight) {
+      if (lp.gw_small) launch_gw_small(pl.dtype, w, st);
+      else launch_gw(pl.dtype, w, st);
+    }
+    if (pl.N > 0 && grad_hidden) {
       GhArgs h;
       h.weight = static_cast<const char*>(weight);
       h.D = ws + pl.b_D;

@@ -83,8 +83,8 @@ def _function():
             with on_device(dev):
                 ws_bytes = flce_logprobs_workspace_size(ctx.p, FLCE_PASS_BACKWARD)
                 workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-                gh, gw = torch.empty_like(hidden), torch.empty_like(weight)
-                gb = None if bias is None else torch.empty_like(bias)
+                gh, gw, gb = (torch.empty_like(t) if need else None     # a frozen head's are not computed
+                              for t, need in zip((hidden, weight, bias), ctx.needs_input_grad))
                 raise_for(flce_logprobs_backward(ctx.p, _ptr(hidden), _ptr(weight), _ptr(bias), _ptr(targets),
                                                  _ptr(lse), _ptr(entropy), _ptr(g), _ptr(h), _ptr(gh), _ptr(gw),
                                                  _ptr(gb), _ptr(workspace), ws_bytes, stream_handle(dev)),

@@ -325,3 +325,27 @@ def test_gradients_against_differences(flce_lib):
             d[i, j] = eps
             diff = (f(lp + d).item() - f(lp - d).item()) / (2 * eps)
             assert abs(diff - grad[i, j].item()) <= 4e-4
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sequence_mean", "none"])
+def test_gradients_of_one_input_alone(flce_lib, reduction):
+    """Only the entropies, or only the log-probabilities, take part in autograd: the same bits."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(6)
+    lp, ent = -torch.rand(5, 333, generator=g, device="cuda"), torch.rand(5, 333, generator=g, device="cuda")
+    adv, mask = torch.randn(5, 333, generator=g, device="cuda"), torch.rand(5, 333, generator=g, device="cuda") < 0.6
+
+    def grads(a, b):
+        x, y = lp.clone().requires_grad_(a), ent.clone().requires_grad_(b)
+        loss = flce_lib.policy_loss(x, lp + 0.1, adv, entropy=y, entropy_coef=0.3, mask=mask, reduction=reduction)
+        return torch.autograd.grad(loss.sum(), [t for t in (x, y) if t.requires_grad])
+
+    both = grads(True, True)
+    assert torch.equal(grads(True, False)[0], both[0]) and torch.equal(grads(False, True)[0], both[1])
+    with torch.no_grad():
+        loss = flce_lib.policy_loss(lp.requires_grad_(True), lp + 0.1, adv, mask=mask)
+    assert not loss.requires_grad
+    with pytest.raises(RuntimeError):      # there is no second derivative
+        x = lp.detach().clone().requires_grad_(True)
+        d, = torch.autograd.grad(flce_lib.policy_loss(x, lp.detach(), adv), x, create_graph=True)
+        torch.autograd.grad(d.sum(), x)

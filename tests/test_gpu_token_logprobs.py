@@ -339,3 +339,58 @@ def test_last_round_of_tiles_runs_small(flce_lib, dtype):
     lp, ent = flce_lib.token_logprobs(x.cuda(), w.cuda(), t.cuda(), b.cuda(), return_entropy=True)
     rows = np.r_[0:4, 4:n:17]
     _check_values(_np(lp)[rows], _np(ent)[rows], _np(x)[rows], _np(w), _np(b), t.numpy()[rows], dtype, {})
+
+
+@pytest.mark.parametrize("n,h,v", [(300, 64, 1000), (700, 264, 9000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_only_the_wanted_gradients(flce_lib, n, h, v, dtype):
+    """A frozen head, frozen states, a frozen bias: the other gradients' bits stay."""
+    import torch
+    x, w, b, t = _tensors(n, h, v, dtype, seed=31)
+    ones = torch.ones(n, device="cuda")
+
+    def grads(wanted):
+        leaves = [a.cuda().requires_grad_(k in wanted) for k, a in zip("xwb", (x, w, b))]
+        lp, ent = flce_lib.token_logprobs(leaves[0], leaves[1], t.cuda(), leaves[2], return_entropy=True)
+        got = torch.autograd.grad((lp, ent), [a for a in leaves if a.requires_grad], (ones, ones))
+        return dict(zip((k for k in "xwb" if k in wanted), got))
+
+    full = grads("xwb")
+    for wanted in ("x", "w", "b", "xb", "xw"):
+        got = grads(wanted)
+        assert list(got) == list(wanted)
+        for k in wanted:
+            assert torch.equal(got[k], full[k]), (wanted, k)
+
+
+@pytest.mark.parametrize("n,h,v", [(70, 64, 500), (700, 264, 9000)])
+@pytest.mark.parametrize("gw_dtype", ["f32", "bf16", "f16"])
+def test_accumulated_gradients(flce_lib, n, h, v, gw_dtype):
+    """FLCE_ACCUMULATE_GRAD_WEIGHT / _BIAS and a weight gradient of another type, through the C entry points:
+    fp32 sums of the contraction and the buffer's contents, rounded once."""
+    import torch
+    x, w, b, t = (a.cuda() for a in _tensors(n, h, v, "bf16", seed=33))
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[gw_dtype]
+    P = lambda a: a.data_ptr()  # noqa: E731
+    st = torch.cuda.current_stream().cuda_stream
+    lp, ent, lse = (torch.empty(n, device="cuda") for _ in range(3))
+    ones = torch.ones(n, device="cuda")
+
+    def run(acc, gw_type, gw, gb):
+        p = flce_lib.make_params(n, h, v, dtype="bf16", grad_weight_dtype=gw_type, reduction="none",
+                                 accumulate_grad_weight=acc, accumulate_grad_bias=acc)
+        ws = torch.empty(flce_lib.flce_logprobs_workspace_size(p, 1), dtype=torch.uint8, device="cuda")
+        assert flce_lib.flce_logprobs_forward(p, P(x), P(w), P(b), P(t), P(lp), P(ent), P(lse), P(ws), ws.numel(), st) == 0
+        gx = torch.empty(n, h, dtype=torch.bfloat16, device="cuda")
+        assert flce_lib.flce_logprobs_backward(p, P(x), P(w), P(b), P(t), P(lse), P(ent), P(ones), P(ones), P(gx), P(gw),
+                                               P(gb), P(ws), ws.numel(), st) == 0
+        return gw, gb
+
+    exact, gb0 = run(False, "f32", torch.empty(v, h, device="cuda"), torch.empty_like(b))
+    rounded, _ = run(False, gw_dtype, torch.empty(v, h, dtype=dt, device="cuda"), torch.empty_like(b))
+    assert torch.equal(rounded, exact.to(dt))
+    prior = torch.randn(v, h, device="cuda").to(dt)
+    prior_b = torch.randn(v, device="cuda").bfloat16()
+    gw, gb = run(True, gw_dtype, prior.clone(), prior_b.clone())
+    assert torch.equal(gw, (exact + prior.float()).to(dt))
+    assert torch.all((gb.float() - gb0.float() - prior_b.float()).abs() <= 2.0 ** -7 * (gb0.float().abs() + prior_b.float().abs()))
