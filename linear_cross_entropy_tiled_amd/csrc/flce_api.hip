@@ -332,10 +332,18 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   if (L.vt_large > 0) L.S_large = forward_splits(P.n_tt, L.vt_large);
   const int64_t rest = P.V - int64_t(L.vt_large) * 256;
   if (rest > 0) {
-    // whole vocabulary tiles to a workgroup, rounded down: more workgroups than fit at once
-    // even out, a workgroup with one tile more than the others is waited for
+    // whole vocabulary tiles to a workgroup, so that about three workgroups a CU share
+    // them.  One token tile in 16 or 8 bits (and BN 16 in any type) streams the weight:
+    // rounded up, so that all workgroups run at once and their loads never run dry (64
+    // tokens at H = 4096, V = 128256 in 8 bits: 130 us, rounded down 154; 40 at H = 2048,
+    // V = 50000 in bf16: 60 against 68).  Otherwise the matrix instructions bound it, and it
+    // is rounded down: more workgroups than fit at once even out, while one with a tile more
+    // than the others is waited for (64 fp32 tokens, same head: 604 us, rounded up 642).
     const int64_t v64 = (rest + 63) / 64;
-    int64_t each = v64 * ((P.N + L.bn - 1) / L.bn) / wg_target;
+    const bool streams = L.bn == 16 || (P.N <= 64 && (P.int8 || P.dtype != FLCE_F32));
+    int64_t each = streams ? (v64 + wg_target - 1) / wg_target : v64 * ((P.N + 63) / 64) / wg_target;
+    const int64_t most = ((int64_t(1) << 31) - 1) / (64 * P.H * P.esize);   // a workgroup's rows: 32-bit offsets
+    if (each > most) each = most;
     if (each < 1) each = 1;
     L.S_small = (int)((v64 + each - 1) / each);
   }

@@ -17,11 +17,12 @@ namespace small {
 constexpr int kBMs = 64;
 constexpr int kThreadsS = 256;
 constexpr int kStageA = kBMs * kBKB;                             // 8 KiB
-// Stage buffers: BN 16 streams the weight and wants loads in flight (40 KiB, four
-// workgroups to a CU); BN 64 wants a third workgroup on the CU more (48 KiB).
-constexpr int stages(int bn) { return bn == 16 ? 4 : 3; }
+// Stage buffers: three, so that three workgroups (BN 64, 48 KiB) or five (BN 16) share a
+// CU; two for fp32 at BN 64, whose stage takes 1024 cycles of matrix instructions, and
+// where a fourth workgroup is worth 5%.
+template <typename T> constexpr int stages(int bn) { return bn == 16 ? 4 : (sizeof(T) == 4 ? 2 : 3); }
 constexpr int stage_bytes(int bn) { return (kBMs + bn) * kBKB; }
-constexpr int lds_bytes(int bn) { return stages(bn) * stage_bytes(bn); }
+template <typename T> constexpr int lds_bytes(int bn) { return stages<T>(bn) * stage_bytes(bn); }
 
 template <int BN> struct Shape {
   static constexpr int WM = BN == 64 ? 2 : 4, WN = 4 / WM;       // waves
@@ -70,14 +71,15 @@ template <typename T, bool KMAJOR, int ROWS> struct Loader {
     }
   }
 
-  __device__ __forceinline__ void load(int kt, uint32_t lds) const {
+  // (K-major: rows starting `row_off` bytes after the descriptor's)
+  __device__ __forceinline__ void load(int kt, uint32_t lds, uint32_t row_off = 0) const {
     if (!loads) return;
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       if constexpr (KMAJOR) {
         const uint32_t k0 = (uint32_t)kt * kBKB;
         dma16(rsrc, __builtin_amdgcn_readfirstlane(lds + (first + i) * 1024),
-              (int)k0 + kc[i] < k_bytes ? voff[i] : kOob, k0);
+              (int)k0 + kc[i] < k_bytes ? voff[i] : kOob, __builtin_amdgcn_readfirstlane(k0 + row_off));
       } else {
         dma16(rsrc, __builtin_amdgcn_readfirstlane(lds + (first + i) * 1024), voff[i],
               (uint32_t)kt * (kBKB / sizeof(T)) * ld);
@@ -128,14 +130,44 @@ template <int N> __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | N);
 }
 
-// The loop.  lds: lds_bytes(BN).  No load is in flight and every wave has
+// One stage's matrix instructions.
+template <typename T, bool A_KMAJOR, bool B_KMAJOR, int BN>
+__device__ __forceinline__ void stage_mma(const char* st, int wm, int wn, int lane,
+                                          Acc (&acc)[Shape<BN>::MI][Shape<BN>::NI]) {
+  typedef Shape<BN> S;
+#pragma unroll
+  for (int s = 0; s < kSubsteps; s++) {
+    typename Frags<T, A_KMAJOR>::type a[S::MI];
+    typename Frags<T, B_KMAJOR>::type b[S::NI];
+#pragma unroll
+    for (int mi = 0; mi < S::MI; mi++) a[mi] = Frags<T, A_KMAJOR>::read(st, (wm * S::MI + mi) * 16, s, lane);
+#pragma unroll
+    for (int ni = 0; ni < S::NI; ni++)
+      b[ni] = Frags<T, B_KMAJOR>::read(st + kStageA, (wn * S::NI + ni) * 16, s, lane);
+#pragma unroll
+    for (int mi = 0; mi < S::MI; mi++)
+#pragma unroll
+      for (int ni = 0; ni < S::NI; ni++) mma(acc[mi][ni], a[mi], b[ni]);
+  }
+}
+
+// Waits until at most the loads of `later` stages are outstanding (a wave that has issued
+// others since waits for a little more).
+template <typename T, bool A_KMAJOR, bool B_KMAJOR, int BN, int LATER>
+__device__ __forceinline__ void wait_stage(bool b_loads) {
+  constexpr int A = Loader<T, A_KMAJOR, kBMs>::PER, B = Loader<T, B_KMAJOR, BN>::PER;
+  if (b_loads) wait_vmcnt<LATER * (A + B)>();
+  else wait_vmcnt<LATER * A>();
+}
+
+// The loop.  lds: lds_bytes<T>(BN).  No load is in flight and every wave has
 // passed its last LDS read when it returns after the caller's next barrier; acc must be
 // zeroed by the caller.
 template <typename T, bool A_KMAJOR, bool B_KMAJOR, int BN>
 __device__ __forceinline__ void mainloop(const OperandDesc& da, const OperandDesc& db, int KT, char* lds,
                                          Acc (&acc)[Shape<BN>::MI][Shape<BN>::NI]) {
   typedef Shape<BN> S;
-  constexpr int SB = stage_bytes(BN), kStages = stages(BN);
+  constexpr int SB = stage_bytes(BN), kStages = stages<T>(BN);
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -154,34 +186,15 @@ __device__ __forceinline__ void mainloop(const OperandDesc& da, const OperandDes
   int buf = 0;
   for (int kt = 0; kt < KT; ++kt) {
     // stage kt has landed when at most the later stages' loads are outstanding
-    if (kt + kStages - 2 < KT) {
-      constexpr int A = Loader<T, A_KMAJOR, kBMs>::PER, B = Loader<T, B_KMAJOR, BN>::PER;
-      if (lb.loads) wait_vmcnt<(kStages - 2) * (A + B)>();
-      else wait_vmcnt<(kStages - 2) * A>();
-    } else {
-      wait_loads();
-    }
+    if (kt + kStages - 2 < KT) wait_stage<T, A_KMAJOR, B_KMAJOR, BN, kStages - 2>(lb.loads);
+    else wait_loads();
     __syncthreads();   // and every wave has read stage kt - 1, whose buffer is loaded next
     if (kt + kStages - 1 < KT) {
       const int nb = buf == 0 ? kStages - 1 : buf - 1;
       la.load(kt + kStages - 1, base + nb * SB);
       lb.load(kt + kStages - 1, base + nb * SB + kStageA);
     }
-    const char* st = lds + buf * SB;
-#pragma unroll
-    for (int s = 0; s < kSubsteps; s++) {
-      typename Frags<T, A_KMAJOR>::type a[S::MI];
-      typename Frags<T, B_KMAJOR>::type b[S::NI];
-#pragma unroll
-      for (int mi = 0; mi < S::MI; mi++) a[mi] = Frags<T, A_KMAJOR>::read(st, (wm * S::MI + mi) * 16, s, lane);
-#pragma unroll
-      for (int ni = 0; ni < S::NI; ni++)
-        b[ni] = Frags<T, B_KMAJOR>::read(st + kStageA, (wn * S::NI + ni) * 16, s, lane);
-#pragma unroll
-      for (int mi = 0; mi < S::MI; mi++)
-#pragma unroll
-        for (int ni = 0; ni < S::NI; ni++) mma(acc[mi][ni], a[mi], b[ni]);
-    }
+    stage_mma<T, A_KMAJOR, B_KMAJOR, BN>(lds + buf * SB, wm, wn, lane, acc);
     buf = buf == kStages - 1 ? 0 : buf + 1;
   }
 }

@@ -10,15 +10,24 @@ namespace flce {
 
 using small::Shape;
 
-// Token tiles are the fast index: workgroups that share a weight tile run together.
+// A workgroup's vocabulary tiles are one run of stages: the loads of the next tile's
+// first stages are in flight during a tile's epilogue (4 tokens at H = 4096, V = 128256
+// in 8 bits read 0.5 GB in 114 us with the merge, 4.6 TB/s; 136 us when the loads ran dry
+// at every tile and workgroups came in more than one round).  Rows
+// past V lie past the descriptor's end and read as 0.  Token tiles are the fast index:
+// workgroups that share a weight tile run together.
 template <typename T, bool HAS_BIAS, bool SOFTCAP, int BN>
 __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a, int n_tt) {
   typedef Shape<BN> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
+  constexpr int kStages = small::stages<T>(BN), SB = small::stage_bytes(BN);
   constexpr bool I8 = E == 1;
   typedef typename BiasOf<T>::type B;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(BN)];
-  static __shared__ float xs[Sh::WM][4][BN];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes<T>(BN)];
+  // a tile's bias and scales arrive with its first stage, up to kStages - 1 stages and so
+  // as many tiles ahead of the tile in work
+  static __shared__ __attribute__((aligned(256))) char bias_lds[kStages][256], scale_lds[kStages][256];
+  float(&xs)[Sh::WM][4][BN] = *reinterpret_cast<float(*)[Sh::WM][4][BN]>(lds);   // after the last stage
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int tt = L % n_tt, s = L / n_tt;
   const int vt_begin = (int)((int64_t)s * a.n_vt / a.S), vt_end = (int)((int64_t)(s + 1) * a.n_vt / a.S);
@@ -42,39 +51,76 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
   }
 
   const uint32_t ld = (uint32_t)a.H * E;
-  OperandDesc db;
+  const int v_begin = a.v_first + vt_begin * 64, v_end = min(a.v_first + vt_end * 64, a.V);
+  OperandDesc da, db;
+  da.base = a.weight + (size_t)v_begin * ld;
+  da.ld_bytes = ld;
+  da.nrec = (uint32_t)(v_end - v_begin) * ld;
+  da.cols_valid = 0;
+  da.k_bytes = a.H * E;
   db.base = a.hidden + (size_t)t0 * ld;
   db.ld_bytes = ld;
   db.nrec = (uint32_t)min(a.N - t0, BN) * ld;
   db.cols_valid = 0;
   db.k_bytes = a.H * E;
-  const int KT = (a.H * E + kBKB - 1) / kBKB;
+  const int KT = (a.H * E + kBKB - 1) / kBKB, tiles = vt_end - vt_begin;
+  small::Loader<T, true, small::kBMs> la;
+  small::Loader<T, true, BN> lb;
+  la.init(da, tid);
+  lb.init(db, tid);
+  const uint32_t lds0 = lds_addr_of(lds);
 
-  for (int vt = vt_begin; vt < vt_end; ++vt) {
-    const int v0 = a.v_first + vt * 64;
-    OperandDesc da;
-    da.base = a.weight + (size_t)v0 * ld;
-    da.ld_bytes = ld;
-    da.nrec = (uint32_t)min(a.V - v0, 64) * ld;
-    da.cols_valid = 0;
-    da.k_bytes = a.H * E;
+  int l_tile = 0, l_kt = 0, l_buf = 0, l_side = 0;   // the next stage to load
+  auto load_next = [&]() {
+    if (l_tile >= tiles) return;
+    if (l_kt == 0) {   // (bytes past the last row's arrive as 0, whole words: see fwd_tiles_kernel)
+      const int v = v_begin + l_tile * 64, rows = min(v_end - v, 64);
+      if (HAS_BIAS && wave == 2)
+        dma_vector(reinterpret_cast<const B*>(a.bias) + v, ((uint32_t)rows * sizeof(B) + 3u) & ~3u, bias_lds[l_side],
+                   256, lane);
+      if (I8 && wave == 3) dma_vector(a.weight_scale + v, (uint32_t)rows * 4, scale_lds[l_side], 256, lane);
+    }
+    const uint32_t to = lds0 + l_buf * SB;
+    la.load(l_kt, to, (uint32_t)l_tile * 64u * ld);
+    lb.load(l_kt, to + small::kStageA);
+    l_buf = l_buf == kStages - 1 ? 0 : l_buf + 1;
+    if (++l_kt == KT) {
+      l_kt = 0;
+      l_tile++;
+      l_side = l_side == kStages - 1 ? 0 : l_side + 1;
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < kStages - 1; p++) load_next();
+
+  int buf = 0, left = tiles * KT;   // stages not yet consumed
+  for (int tile = 0, side = 0; tile < tiles; tile++, side = side == kStages - 1 ? 0 : side + 1) {
+    const int v0 = v_begin + tile * 64;
     Acc acc[MI][NI];
 #pragma unroll
     for (int mi = 0; mi < MI; mi++)
 #pragma unroll
       for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
-    __syncthreads();   // every wave has read the last tile's stages
-    small::mainloop<T, true, true, BN>(da, db, KT, lds, acc);
+    for (int kt = 0; kt < KT; kt++, left--) {
+      if (left >= kStages - 1) small::wait_stage<T, true, true, BN, kStages - 2>(lb.loads);
+      else wait_loads();
+      __syncthreads();   // the stage has landed for every wave, and every wave has read the one before
+      load_next();       // into the buffer of the one before
+      small::stage_mma<T, true, true, BN>(lds + buf * SB, wm, wn, lane, acc);
+      buf = buf == kStages - 1 ? 0 : buf + 1;
+    }
 
     float sb[MI][4], ws[MI][4];
 #pragma unroll
-    for (int mi = 0; mi < MI; mi++)
+    for (int mi = 0; mi < MI; mi++) {
+      const int row = (wm * MI + mi) * 16 + 4 * (lane >> 4);
+      if constexpr (HAS_BIAS) {
+        lds_vec4<B>(bias_lds[side], row, sb[mi]);
 #pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int v = min(v0 + (wm * MI + mi) * 16 + 4 * (lane >> 4) + r, a.V - 1);
-        if (HAS_BIAS) sb[mi][r] = (float)reinterpret_cast<const B*>(a.bias)[v] * s_u;
-        if (I8) ws[mi][r] = a.weight_scale[v];
+        for (int r = 0; r < 4; r++) sb[mi][r] *= s_u;
       }
+      if constexpr (I8) lds_vec4<float>(scale_lds[side], row, ws[mi]);
+    }
 #pragma unroll
     for (int ni = 0; ni < NI; ni++) {
       float mu = kMasked;
@@ -109,6 +155,7 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
     }
   }
 
+  __syncthreads();   // every wave has read the last stage
 #pragma unroll
   for (int ni = 0; ni < NI; ni++) {
 #pragma unroll
@@ -163,7 +210,7 @@ template <typename T, bool HAS_BIAS, bool SOFTCAP>
 __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(DlogitsArgs a) {
   typedef Shape<64> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(64)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes<T>(64)];
   static __shared__ float gbs[Sh::WN][64];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int tt = L % a.n_tt, vt = L / a.n_tt;
@@ -252,7 +299,7 @@ template <typename T, typename OutT>
 __global__ __launch_bounds__(small::kThreadsS) void gw_small_kernel(GwArgs a) {
   typedef Shape<64> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(64)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes<T>(64)];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int ht = L % a.n_ht, vt = L / a.n_ht;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -306,7 +353,7 @@ template <typename T>
 __global__ __launch_bounds__(small::kThreadsS) void gh_small_kernel(GhArgs a) {
   typedef Shape<64> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
-  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes(64)];
+  static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes<T>(64)];
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
   const int n_tiles = a.n_ht * a.n_tt, split = L / n_tiles, in = L - split * n_tiles;
   const int tt = in % a.n_tt, ht = in / a.n_tt;
