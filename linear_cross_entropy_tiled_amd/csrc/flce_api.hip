@@ -353,11 +353,12 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   L.n64 = (int)n64;
   L.N64 = (int)(n64 * 64);
   const int64_t vc64 = P.Vc / 64, vc256 = P.Vc / 256;
-  L.d_small = P.N > 0 && small_is_faster(P, P.n_tt * vc256, n64 * vc64, 1.0, 1.0);
+  L.split = P.N > 0 && P.N <= 64 && P.dtype != FLCE_F32;
+  L.d_small = P.N > 0 && (L.split || small_is_faster(P, P.n_tt * vc256, n64 * vc64, 1.0, 1.0));
   L.gw_small = small_is_faster(P, P.n_ht * vc256, h64 * vc64, 1.0, 1.0);
-  L.K_pad = L.d_small ? L.N64 : (int)P.N_pad;
+  L.K_pad = L.split ? 2 * L.N64 : (L.d_small ? L.N64 : (int)P.N_pad);
   // grad_hidden: split the vocabulary until the tiles fill the chip, at least 8 stages to a part
-  const int64_t stages = P.Vc * P.esize / 128, tiles = n64 * h64;
+  const int64_t stages = P.Vc * P.esize / 128, tiles = (L.split ? 2 : 1) * n64 * h64;
   int64_t parts = tiles > 0 ? wg_target / tiles : 1;
   if (parts > stages / kMinStagesPerPart) parts = stages / kMinStagesPerPart;
   const size_t per_part = size_t(P.N) * P.H * 4;
@@ -366,8 +367,8 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   const int64_t kt = (stages + parts - 1) / parts;
   L.gh_kt = (int)kt;
   L.gh_parts = (int)((stages + kt - 1) / kt);
-  L.gh_small = P.N > 0 && small_is_faster(P, P.n_ht * P.n_tt * P.gh_parts, tiles * L.gh_parts,
-                                          (double)P.gh_kt_per_part, (double)kt);
+  L.gh_small = P.N > 0 && (L.split || small_is_faster(P, P.n_ht * P.n_tt * P.gh_parts, tiles * L.gh_parts,
+                                                      (double)P.gh_kt_per_part, (double)kt));
   size_t o = P.b_bytes;
   L.b_coefE = o;
   o = align_up(o + size_t(P.N_pad) * 4, 256);

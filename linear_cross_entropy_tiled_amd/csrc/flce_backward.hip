@@ -693,14 +693,15 @@ __global__ __launch_bounds__(256) void bwd_gh_reduce(const float* part, int part
 // hidden^T [H][N_pad] (zero for t >= N): the token-contiguous copy of hidden
 // that the grad_weight contraction reads as its register operand.  With tgt, rows
 // without a target are zero too: their D is 0, and 0 times what they hold is to be 0.
+// With shift 1 every token has two columns (LpPlan::split).
 template <typename T>
 __global__ __launch_bounds__(256) void transpose_hidden_kernel(const T* x, int N, int H, int N_pad, T* xt,
-                                                               const int* tgt) {
+                                                               const int* tgt, int shift) {
   __shared__ float tile[64][65];
   const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int r = ty; r < 64; r += 4) {
-    const int t = t0 + r, h = h0 + tx;
+    const int t = (t0 + r) >> shift, h = h0 + tx;
     tile[r][tx] = (t < N && h < H && (!tgt || tgt[t] >= 0)) ? load_elem<T>(x, (int64_t)t * H + h) : 0.0f;
   }
   __syncthreads();
@@ -894,18 +895,19 @@ void launch_gb_reduce(int dtype, const float* part, int n_tt, int ld, int V, voi
 }
 
 template <typename T>
-static void launch_transpose_t(const void* hidden, int N, int H, int N_pad, void* hiddenT, const int* tgt,
+static void launch_transpose_t(const void* hidden, int N, int H, int N_pad, void* hiddenT, const int* tgt, int shift,
                                hipStream_t st) {
   dim3 grid((unsigned)(N_pad / 64), (unsigned)((H + 63) / 64));
   transpose_hidden_kernel<T><<<grid, 256, 0, st>>>(reinterpret_cast<const T*>(hidden), N, H, N_pad,
-                                                   reinterpret_cast<T*>(hiddenT), tgt);
+                                                   reinterpret_cast<T*>(hiddenT), tgt, shift);
 }
 
 void launch_transpose_hidden(int dtype, const void* hidden, int N, int H, int N_pad, void* hiddenT,
-                             hipStream_t st, const int* tgt) {
-  if (dtype == FLCE_BF16) launch_transpose_t<bf16>(hidden, N, H, N_pad, hiddenT, tgt, st);
-  else if (dtype == FLCE_F16) launch_transpose_t<f16>(hidden, N, H, N_pad, hiddenT, tgt, st);
-  else launch_transpose_t<float>(hidden, N, H, N_pad, hiddenT, tgt, st);
+                             hipStream_t st, const int* tgt, bool twice) {
+  const int shift = twice ? 1 : 0;
+  if (dtype == FLCE_BF16) launch_transpose_t<bf16>(hidden, N, H, N_pad, hiddenT, tgt, shift, st);
+  else if (dtype == FLCE_F16) launch_transpose_t<f16>(hidden, N, H, N_pad, hiddenT, tgt, shift, st);
+  else launch_transpose_t<float>(hidden, N, H, N_pad, hiddenT, tgt, shift, st);
 }
 
 void launch_gw(int dtype, const GwArgs& g, hipStream_t st) {

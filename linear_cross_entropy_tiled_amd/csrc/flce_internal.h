@@ -105,6 +105,7 @@ struct DlogitsArgs {
   int ld_gb;
   const float* dscale;   // [0]: factor D is stored with
   const float* coefE;    // ENTROPY only
+  int split = 0;         // small tiles: D as two rows per token (LpPlan::split)
 };
 
 // ---------------------------------------------------------------------------
@@ -152,11 +153,13 @@ struct GhArgs {
   int kt_per_part;
   float* part;      // parts x N x H fp32 partials (parts > 1)
   const float* dscale;   // [1]: 2^-s, undoes the factor D is stored with
+  int split = 0;         // small tiles: two rows of D per token (n_tt counts tiles of D's rows)
 };
 
-// hiddenT[h][t] = hidden[t][h] for t < N, 0 for N <= t < N_pad and, with tgt, where tgt[t] < 0.
+// hiddenT[h][t] = hidden[t][h] for t < N, 0 for N <= t < N_pad and, with tgt, where tgt[t] < 0;
+// with twice, column t is hidden row t / 2.
 void launch_transpose_hidden(int dtype, const void* hidden, int N, int H, int N_pad, void* hiddenT,
-                             hipStream_t st, const int* tgt = nullptr);
+                             hipStream_t st, const int* tgt = nullptr, bool twice = false);
 void launch_gw(int dtype, const GwArgs& g, hipStream_t st);
 void launch_gh(int dtype, const GhArgs& h, hipStream_t st);
 void launch_gh_reduce(int dtype, const GhArgs& h, hipStream_t st);

@@ -15,6 +15,13 @@ struct LpPlan {
   int N_pad;
   size_t f_bytes;
 
+  // Up to 64 tokens in 16 bits: the logit gradient is held as the sum of two 16-bit
+  // rows per token, its rounding and the rest.  One rounding of each entry, relative to
+  // the output's own, averages out over many tokens (the gradients' error against fp64
+  // is 1.4 times that of rounding the outputs alone); of few tokens' gradients one entry
+  // can be most (2.5 times).  Costs a second row in two contractions that are bound by
+  // reading or writing the weight there.
+  bool split;
   bool d_small, gw_small, gh_small;
   int n64, N64;           // 64-token tiles, padded tokens
   int K_pad;              // tokens the grad_weight contraction runs over

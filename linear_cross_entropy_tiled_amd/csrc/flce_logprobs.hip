@@ -577,7 +577,7 @@ hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGr
   lp_prep_kernel<<<1, 1024, 0, st>>>(a);
 
   char* hiddenT = ws + pl.b_xt;
-  if (pl.N > 0 && grad_weight) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, lp.K_pad, hiddenT, st, a.tgt);
+  if (pl.N > 0 && grad_weight) launch_transpose_hidden(pl.dtype, hidden, (int)pl.N, (int)pl.H, lp.K_pad, hiddenT, st, a.tgt, lp.split);
   float* gb_part = reinterpret_cast<float*>(ws + (lp.d_small ? lp.b_gbpart : pl.b_gbpart));
   const bool f32 = pl.dtype == FLCE_F32;
   for (int c = 0; c < pl.n_chunks; c++) {
@@ -608,6 +608,7 @@ hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGr
       d.gb_part = gb_part;
       d.ld_gb = (int)pl.V_pad;
       d.dscale = a.dscale;
+      d.split = lp.split;
       if (lp.d_small) launch_dlogits_small(pl, d, st);
       else launch_lp_dlogits(pl, d, st);
     }
@@ -643,7 +644,8 @@ hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGr
       h.cv0 = cv0;
       h.cvn = cvn;
       h.n_ht = lp.gh_small ? (int)((pl.H + 63) / 64) : (int)pl.n_ht;
-      h.n_tt = lp.gh_small ? lp.n64 : (int)pl.n_tt;
+      h.n_tt = lp.split ? 2 * lp.n64 : (lp.gh_small ? lp.n64 : (int)pl.n_tt);
+      h.split = lp.split;
       h.accb = f32 ? reinterpret_cast<float*>(grad_hidden) : reinterpret_cast<float*>(ws + pl.b_ghacc);
       h.out = grad_hidden;
       h.out_f32 = f32;

@@ -273,7 +273,17 @@ __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(Dlogits
         if (v >= a.V) d[r] = 0.0f;
         cs[mi][r] += d[r];
       }
-      put4<T>(D + (size_t)t * a.ldD + (v0 - a.cv0) + vl, d);
+      if (sizeof(T) == 2 && a.split) {
+        // two rows: the rounded value and the rest
+        T* row = D + (size_t)(2 * t) * a.ldD + (v0 - a.cv0) + vl;
+        float rest[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++) rest[r] = d[r] - (float)(T)d[r];
+        put4<T>(row, d);
+        put4<T>(row + a.ldD, rest);
+      } else {
+        put4<T>(D + (size_t)t * a.ldD + (v0 - a.cv0) + vl, d);
+      }
     }
   }
   if constexpr (HAS_BIAS) {
@@ -386,15 +396,19 @@ __global__ __launch_bounds__(small::kThreadsS) void gh_small_kernel(GhArgs a) {
   const float inv = a.dscale[1];
 #pragma unroll
   for (int ni = 0; ni < NI; ni++) {
-    const int t = t0 + (wn * NI + ni) * 16 + (lane & 15);
+    const int row = t0 + (wn * NI + ni) * 16 + (lane & 15), t = a.split ? row >> 1 : row;
 #pragma unroll
     for (int mi = 0; mi < MI; mi++) {
-      const int h = h0 + (wm * MI + mi) * 16 + 4 * (lane >> 4);
-      if (t >= a.N || h >= a.H) continue;
-      const size_t o = (size_t)t * a.H + h;
       float c[4], prev[4];
 #pragma unroll
       for (int r = 0; r < 4; r++) c[r] = acc[mi][ni][r] * inv;
+      if (a.split) {   // a token's two rows are neighbouring columns here
+#pragma unroll
+        for (int r = 0; r < 4; r++) c[r] += __shfl_xor(c[r], 1);
+      }
+      const int h = h0 + (wm * MI + mi) * 16 + 4 * (lane >> 4);
+      if (t >= a.N || h >= a.H || (a.split && (row & 1))) continue;
+      const size_t o = (size_t)t * a.H + h;
       if (a.parts > 1) {   // partial of this split; the reduction applies the mode
         put4<float>(a.part + (size_t)split * a.N * a.H + o, c);
         continue;

@@ -394,3 +394,35 @@ def test_accumulated_gradients(flce_lib, n, h, v, gw_dtype):
     gw, gb = run(True, gw_dtype, prior.clone(), prior_b.clone())
     assert torch.equal(gw, (exact + prior.float()).to(dt))
     assert torch.all((gb.float() - gb0.float() - prior_b.float()).abs() <= 2.0 ** -7 * (gb0.float().abs() + prior_b.float().abs()))
+
+
+@pytest.mark.parametrize("n,h,v", [(1, 264, 900), (2, 64, 5001), (17, 136, 1100), (59, 520, 3350), (64, 72, 255)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradients_of_few_tokens_are_rounded_once(flce_lib, n, h, v, dtype):
+    """Up to 64 tokens the logit gradient is held as a rounded value and the rest: 2^-17 (2^-23) of each entry.
+    What is left: the outputs' own rounding, half a step; the softmax's fp32 (p, log p and H off by
+    (4 + 2 |log p|) (z's bound + 16 x 2^-24 (1 + |z| + |log p|))) and the fp32 sums, as in
+    test_values_and_gradients."""
+    import torch
+    x, w, b, t = _tensors(n, h, v, dtype, seed=77, ignored=0.0)
+    leaves = [a.cuda().requires_grad_(True) for a in (x, w)]
+    lp, ent = flce_lib.token_logprobs(*leaves, t.cuda(), return_entropy=True, vocab_chunk=1024)
+    rng = np.random.default_rng(n)
+    g, e = rng.normal(size=n).astype(np.float32), 0.1 * rng.normal(size=n).astype(np.float32)
+    e = e.astype(np.float32)
+    got = torch.autograd.grad((lp, ent), leaves, (torch.from_numpy(g).cuda(), torch.from_numpy(e).cuda()))
+    X, W, T = _np(x), _np(w), t.numpy()
+    want = ao.token_logprobs_grads(X, W, None, T, g.astype(np.float64), e.astype(np.float64))
+    _, ent64, z, _ = ao.token_logprobs(X, W, None, T)
+    l = z - (z.max(1) + np.log(np.exp(z - z.max(1, keepdims=True)).sum(1)))[:, None]
+    p = np.exp(l)
+    a = np.abs(g)[:, None] * p + np.abs(e)[:, None] * p * (np.abs(l) + ent64[:, None])
+    a[np.arange(n), T] += np.abs(g)
+    ez = _bounds(X, W, None, dtype, {})[:, None]
+    half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    tiny = 2.0 ** -24 * a.max() if dtype == "f16" else 0.0      # the rest of an entry below fp16's normal range
+    d_err = a * (half ** 2 / 2 + (4 + 2 * np.abs(l)) * (ez + 16 * U32 * (1 + np.abs(z) + np.abs(l)))) + tiny
+    for name, gotten, ref, err, size in (("hidden", got[0], want[0], d_err @ np.abs(W), a @ np.abs(W)),
+                                         ("weight", got[1], want[1], d_err.T @ np.abs(X), a.T @ np.abs(X))):
+        out = 1.01 * half * np.abs(ref) + (2.0 ** -25 if dtype == "f16" else 0.0)
+        assert np.all(np.abs(_np(gotten) - ref) <= out + err + (64 + v / 16) * U32 * size), name
