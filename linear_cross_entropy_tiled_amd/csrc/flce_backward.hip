@@ -693,21 +693,39 @@ __global__ __launch_bounds__(256) void bwd_gh_reduce(const float* part, int part
 // hidden^T [H][N_pad] (zero for t >= N): the token-contiguous copy of hidden
 // that the grad_weight contraction reads as its register operand.  With tgt, rows
 // without a target are zero too: their D is 0, and 0 times what they hold is to be 0.
-// With shift 1 every token has two columns (LpPlan::split).
+// With shift 1 every token has two columns (LpPlan::split).  64 x 64 elements to a
+// workgroup, 16 bytes to a load and a store, all of a thread's loads in flight at once
+// (element by element, 250 x 4096 bf16 took 13 us, nearly all of it latency).
 template <typename T>
 __global__ __launch_bounds__(256) void transpose_hidden_kernel(const T* x, int N, int H, int N_pad, T* xt,
                                                                const int* tgt, int shift) {
-  __shared__ float tile[64][65];
-  const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  for (int r = ty; r < 64; r += 4) {
-    const int t = (t0 + r) >> shift, h = h0 + tx;
-    tile[r][tx] = (t < N && h < H && (!tgt || tgt[t] >= 0)) ? load_elem<T>(x, (int64_t)t * H + h) : 0.0f;
+  constexpr int kVec = 16 / sizeof(T), kChunks = 64 / kVec, kPer = 64 * kChunks / 256;
+  typedef T TV __attribute__((ext_vector_type(16 / sizeof(T))));
+  __shared__ T tile[64][64 + 4 / sizeof(T)];   // one bank past a whole row
+  const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 64, tid = threadIdx.x;
+  TV v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; i++) {
+    const int r = (tid + 256 * i) / kChunks, c = (tid + 256 * i) % kChunks;
+    const int t = (t0 + r) >> shift, h = h0 + c * kVec;   // H % 8 == 0: whole chunks
+#pragma unroll
+    for (int j = 0; j < kVec; j++) v[i][j] = (T)0.0f;
+    if (t < N && h < H && (!tgt || tgt[t] >= 0)) v[i] = *reinterpret_cast<const TV*>(x + (size_t)t * H + h);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; i++) {
+    const int r = (tid + 256 * i) / kChunks, c = (tid + 256 * i) % kChunks;
+#pragma unroll
+    for (int j = 0; j < kVec; j++) tile[r][c * kVec + j] = v[i][j];
   }
   __syncthreads();
-  for (int r = ty; r < 64; r += 4) {
-    const int h = h0 + r, t = t0 + tx;
-    if (h < H && t < N_pad) xt[(size_t)h * N_pad + t] = (T)tile[tx][r];
+#pragma unroll
+  for (int i = 0; i < kPer; i++) {
+    const int r = (tid + 256 * i) / kChunks, c = (tid + 256 * i) % kChunks;   // row h0 + r, columns t0 + c kVec ..
+    TV o;
+#pragma unroll
+    for (int j = 0; j < kVec; j++) o[j] = tile[c * kVec + j][r];
+    if (h0 + r < H) *reinterpret_cast<TV*>(xt + (size_t)(h0 + r) * N_pad + t0 + c * kVec) = o;
   }
 }
 

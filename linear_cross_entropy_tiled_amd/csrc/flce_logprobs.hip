@@ -268,14 +268,15 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   }
 }
 
-// Merges each row's vocabulary splits and writes its outputs: `group` lanes a row
-// (a power of two up to 64), each taking every group-th split, then a tree, so that
-// the order depends on the sizes alone.  Few rows have hundreds of splits, and a lane
-// on its own would wait for one load after the other (38 us for 4 rows of 256 splits).
+// Merges each row's vocabulary splits and writes its outputs.  A workgroup takes 16 rows
+// by `subs` threads each (a power of two from 4 to 64), neighbouring threads on
+// neighbouring rows; a thread merges every subs-th split, then lanes, then waves merge,
+// all in an order that depends on the sizes alone.  (Few rows have hundreds of splits:
+// one thread to a row took 38 us for 4 rows of 256.)
 struct LpRowArgs {
   const void* targets;
   int tgt_i32;
-  int N, V, S, N_pad, group;
+  int N, V, S, N_pad, subs;
   int64_t ignore_index;
   const float* part;
   float* logps;
@@ -285,28 +286,9 @@ struct LpRowArgs {
   int init_status;  // no tile kernel ran before (N = 0)
 };
 
-__global__ __launch_bounds__(256) void lp_rows_kernel(LpRowArgs a) {
-  const int i = ((int)blockIdx.x * 256 + (int)threadIdx.x) / a.group, sub = threadIdx.x & (a.group - 1);
-  if (a.init_status && blockIdx.x == 0 && threadIdx.x == 0) a.status[0] = FLCE_OK;
-  const int row = min(i, a.N - 1);   // whole groups past the last row stay in step
-  if (a.N == 0) return;
-  const size_t plane = (size_t)a.S * a.N_pad;
-  LpState r{kMasked, 0.0f, 0.0f, -INFINITY};
-  for (int s0 = sub; s0 < a.S; s0 += 4 * a.group) {
-    LpState q[4];
+__device__ __forceinline__ LpState lp_lane_merge(LpState r) {   // over lanes l, l ^ 16, l ^ 32, l ^ 48
 #pragma unroll
-    for (int j = 0; j < 4; j++) {   // four loads in flight; past the last split the last one, not merged
-      const float* p = a.part + (size_t)min(s0 + j * a.group, a.S - 1) * a.N_pad + row;
-      q[j].m = p[0];
-      q[j].l = p[plane];
-      q[j].T = p[2 * plane];
-      q[j].yt = p[3 * plane];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      if (s0 + j * a.group < a.S) lp_merge(r, q[j]);
-  }
-  for (int o = 1; o < a.group; o <<= 1) {
+  for (int o = 16; o <= 32; o <<= 1) {
     LpState q;
     q.m = __shfl_xor(r.m, o);
     q.l = __shfl_xor(r.l, o);
@@ -314,9 +296,44 @@ __global__ __launch_bounds__(256) void lp_rows_kernel(LpRowArgs a) {
     q.yt = __shfl_xor(r.yt, o);
     lp_merge(r, q);
   }
+  return r;
+}
+
+__global__ __launch_bounds__(1024) void lp_rows_kernel(LpRowArgs a) {
+  __shared__ LpState waves[16][16];
+  const int tid = threadIdx.x, sub = tid >> 4, i = (int)blockIdx.x * 16 + (tid & 15);
+  if (a.init_status && blockIdx.x == 0 && tid == 0) a.status[0] = FLCE_OK;
+  if (a.N == 0) return;
+  const int row = min(i, a.N - 1);   // threads past the last row stay in step
+  const size_t plane = (size_t)a.S * a.N_pad;
+  const int64_t t = load_target(a.targets, row, a.tgt_i32);
+  LpState r{kMasked, 0.0f, 0.0f, -INFINITY};
+  for (int s0 = sub; s0 < a.S; s0 += 4 * a.subs) {
+    LpState q[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {   // four splits' loads in flight; past the last one it again, not merged
+      const float* p = a.part + (size_t)min(s0 + j * a.subs, a.S - 1) * a.N_pad + row;
+      q[j].m = p[0];
+      q[j].l = p[plane];
+      q[j].T = p[2 * plane];
+      q[j].yt = p[3 * plane];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (s0 + j * a.subs < a.S) lp_merge(r, q[j]);
+  }
+  r = lp_lane_merge(r);
+  const int n_waves = a.subs >> 2;
+  if (n_waves > 1) {
+    if ((tid & 63) < 16) waves[tid >> 6][tid & 15] = r;
+    __syncthreads();
+    if (tid >= 64) return;
+    r = LpState{kMasked, 0.0f, 0.0f, -INFINITY};
+    for (int w = sub; w < n_waves; w += 4) lp_merge(r, waves[w][tid & 15]);
+    r = lp_lane_merge(r);
+  }
   if (sub != 0 || i >= a.N) return;
   const float l2 = fast_log2(r.l);
-  const int64_t t = load_target(a.targets, i, a.tgt_i32);
   const bool in_range = t >= 0 && t < a.V, valid = t != a.ignore_index && in_range;
   // (a row without any finite logit: l = 0, and every output is NaN or -inf)
   a.lse[i] = (r.m + l2) * kLn2;
@@ -449,8 +466,8 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
   r.V = (int)pl.V;
   r.S = lp.S_large + lp.S_small;
   r.N_pad = lp.N_pad;
-  r.group = 1;
-  while (r.group < 64 && r.group < r.S) r.group *= 2;
+  r.subs = 4;
+  while (r.subs < 64 && r.subs < r.S) r.subs *= 2;
   r.ignore_index = pl.ignore_index;
   r.part = part;
   r.logps = logps;
@@ -458,8 +475,8 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
   r.lse = lse;
   r.status = status;
   r.init_status = pl.N == 0;
-  const int64_t blocks = (pl.N * r.group + 255) / 256;
-  lp_rows_kernel<<<(unsigned)(blocks > 0 ? blocks : 1), 256, 0, st>>>(r);
+  const int64_t blocks = (pl.N + 15) / 16;
+  lp_rows_kernel<<<(unsigned)(blocks > 0 ? blocks : 1), 16 * r.subs, 0, st>>>(r);
   return hipGetLastError();
 }
 
