@@ -18,7 +18,7 @@ from typing import Optional
 from . import (DTYPES, REDUCTIONS, _dtype_name, _ptr, flce_policy_backward,
                flce_policy_forward, flce_policy_params, flce_policy_workspace_size, flce_preference_backward,
                flce_preference_forward, flce_preference_params, flce_preference_workspace_size, flce_token_view)
-from .logprobs import differentiable, on_device, raise_for, stream_handle
+from .logprobs import differentiable, first_order, on_device, raise_for, stream_handle, upstream
 
 PREFERENCE_TYPES = {"sigmoid": 0, "hinge": 1, "squared": 2}
 POLICY_REDUCTIONS = {**REDUCTIONS, "sequence_mean": 3}
@@ -105,43 +105,42 @@ def _preference_forward(p, logps, ref, mask, offsets):
     pairs = p.n_seqs // 2
     with on_device(dev):
         ws_bytes = _preference_workspace(p.n_seqs, p.length)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        # one allocation: the workspace, then the sequences' gradient factors for the backward
+        kept = torch.empty(ws_bytes // 4 + p.n_seqs, dtype=torch.float32, device=dev)
         loss = torch.empty((pairs,) if p.reduction == 0 else (), dtype=torch.float32, device=dev)
         rewards = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
-        seq_grad = torch.empty(p.n_seqs, dtype=torch.float32, device=dev)
         raise_for(flce_preference_forward(p, _view(logps), _view(ref), _view(mask), _ptr(offsets), _ptr(loss),
-                                           _ptr(rewards), _ptr(seq_grad), _ptr(workspace), ws_bytes,
-                                           stream_handle(dev)), "flce_preference_forward")
-    return loss, rewards, seq_grad
+                                          _ptr(rewards), kept.data_ptr() + ws_bytes, _ptr(kept), ws_bytes,
+                                          stream_handle(dev)), "flce_preference_forward")
+    return loss, rewards, kept
 
 
 @functools.lru_cache(maxsize=None)
 def _preference_function():
     import torch
-    from torch.autograd.function import once_differentiable
 
     class PreferenceLoss(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logps, ref, mask, offsets, p):
-            loss, rewards, seq_grad = _preference_forward(p, logps, ref, mask, offsets)
+            loss, rewards, kept = _preference_forward(p, logps, ref, mask, offsets)
             ctx.mark_non_differentiable(rewards)
             ctx.set_materialize_grads(False)
-            ctx.save_for_backward(seq_grad, mask, offsets)
+            ctx.save_for_backward(kept, mask, offsets)
             ctx.p, ctx.like = p, (logps.shape, logps.dtype, logps.device)
             return loss, rewards
 
-        @staticmethod
-        @once_differentiable
+        @first_order
         def backward(ctx, g, _):
             if g is None:
                 return (None,) * 5
-            seq_grad, mask, offsets = ctx.saved_tensors
+            kept, mask, offsets = ctx.saved_tensors
             shape, dtype, dev = ctx.like
-            g = g.to(torch.float32).contiguous()
+            g = upstream(g)
             grad = torch.empty(shape, dtype=dtype, device=dev)
             with on_device(dev):
-                raise_for(flce_preference_backward(ctx.p, _ptr(g), _ptr(seq_grad), _view(mask), _ptr(offsets),
-                                                    _ptr(grad), stream_handle(dev)), "flce_preference_backward")
+                raise_for(flce_preference_backward(ctx.p, _ptr(g), kept.data_ptr() + 4 * (kept.numel() - ctx.p.n_seqs),
+                                                   _view(mask), _ptr(offsets),
+                                                   _ptr(grad), stream_handle(dev)), "flce_preference_backward")
             return grad, None, None, None, None
 
     return PreferenceLoss
@@ -195,44 +194,46 @@ def _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets, need
     dev = logps.device
     with on_device(dev):
         ws_bytes = _policy_workspace(p.n_seqs, p.length)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        # one allocation: the workspace, then for the backward the tokens' gradients (16-byte
+        # aligned) and the weights
+        n_unit = (logps.numel() + 3) // 4 * 4 if needs_grad else 0
+        kept = torch.empty(ws_bytes // 4 + n_unit + 1 + p.n_seqs, dtype=torch.float32, device=dev)
+        at = kept.data_ptr()
         loss = torch.empty(logps.shape if p.reduction == 0 else (), dtype=torch.float32, device=dev)
-        unit = torch.empty(logps.shape, dtype=torch.float32, device=dev) if needs_grad else None
-        weights = torch.empty(1 + p.n_seqs, dtype=torch.float32, device=dev)
         per_seq = p.flags & FLCE_ADVANTAGE_PER_SEQUENCE
         adv = flce_token_view(advantages.data_ptr(), 0) if per_seq else _view(advantages)
         raise_for(flce_policy_forward(p, _view(logps), _view(old), _view(ref), _view(entropy), adv, _view(mask),
-                                       _ptr(offsets), _ptr(loss), _ptr(unit), _ptr(weights), _ptr(metrics),
-                                       _ptr(workspace), ws_bytes, stream_handle(dev)), "flce_policy_forward")
-    return loss, unit, weights
+                                       _ptr(offsets), _ptr(loss), at + ws_bytes if n_unit else None,
+                                      at + ws_bytes + 4 * n_unit, _ptr(metrics), at, ws_bytes, stream_handle(dev)),
+                  "flce_policy_forward")
+    return loss, kept, ws_bytes, n_unit
 
 
 @functools.lru_cache(maxsize=None)
 def _policy_function():
     import torch
-    from torch.autograd.function import once_differentiable
 
     class PolicyLoss(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logps, entropy, old, ref, advantages, mask, offsets, p, metrics):
-            loss, unit, weights = _policy_forward(p, logps, old, ref, entropy, advantages, mask, offsets,
-                                                  ctx.needs_input_grad[0], metrics)
-            ctx.save_for_backward(unit, weights, mask, offsets)
+            loss, kept, ctx.unit_at, ctx.n_unit = _policy_forward(p, logps, old, ref, entropy, advantages, mask,
+                                                                  offsets, ctx.needs_input_grad[0], metrics)
+            ctx.save_for_backward(kept, mask, offsets)
             ctx.p, ctx.like = p, (logps.shape, logps.dtype, logps.device)
             return loss
 
-        @staticmethod
-        @once_differentiable
+        @first_order
         def backward(ctx, g):
-            unit, weights, mask, offsets = ctx.saved_tensors
+            kept, mask, offsets = ctx.saved_tensors
+            unit = kept.data_ptr() + ctx.unit_at
             shape, dtype, dev = ctx.like
-            g = g.to(torch.float32).contiguous()
+            g = upstream(g)
             grads = [torch.empty(shape, dtype=dtype, device=dev) if need else None
                      for need in ctx.needs_input_grad[:2]]
             with on_device(dev):
-                raise_for(flce_policy_backward(ctx.p, _ptr(g), _ptr(unit), _ptr(weights), _view(mask),
-                                                _ptr(offsets), _ptr(grads[0]), _ptr(grads[1]), stream_handle(dev)),
-                           "flce_policy_backward")
+                raise_for(flce_policy_backward(ctx.p, _ptr(g), unit if ctx.n_unit else None,
+                                               unit + 4 * ctx.n_unit, _view(mask), _ptr(offsets), _ptr(grads[0]),
+                                               _ptr(grads[1]), stream_handle(dev)), "flce_policy_backward")
             return (*grads, None, None, None, None, None, None, None)
 
     return PolicyLoss
@@ -293,7 +294,7 @@ def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, o
     if differentiable(logps, entropy):
         loss = _policy_function().apply(logps, entropy, old_logps, ref_logps, advantages, mask, offsets, p, metrics)
     else:
-        loss, _, _ = _policy_forward(p, logps, old_logps, ref_logps, entropy, advantages, mask, offsets, False, metrics)
+        loss, *_ = _policy_forward(p, logps, old_logps, ref_logps, entropy, advantages, mask, offsets, False, metrics)
     if not return_metrics:
         return loss
     both = metrics.view(torch.float32)

@@ -35,6 +35,26 @@ def differentiable(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
+def first_order(backward):
+    """backward for a torch.autograd.Function without a second derivative: once_differentiable, whose
+    bookkeeping is skipped where autograd does not record the backward (small steps are bound by the
+    Python that runs in the backward's thread)."""
+    import torch
+    from torch.autograd.function import once_differentiable
+    recorded = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return recorded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    return staticmethod(run)
+
+
+def upstream(g):
+    """An upstream gradient as the kernels read it."""
+    import torch
+    return g if g is None or (g.dtype == torch.float32 and g.is_contiguous()) else g.to(torch.float32).contiguous()
+
+
 def raise_for(rc, where):
     if rc != FLCE_OK:
         raise FlceError(rc, where)
@@ -53,15 +73,9 @@ def _forward(p, hidden, weight, bias, targets):
     return logps, entropy, lse
 
 
-def _upstream(g):
-    import torch
-    return None if g is None else g.to(torch.float32).contiguous()
-
-
 @functools.lru_cache(maxsize=None)
 def _function():
     import torch
-    from torch.autograd.function import once_differentiable
 
     class TokenLogprobs(torch.autograd.Function):
         @staticmethod
@@ -72,13 +86,12 @@ def _function():
             ctx.p = p
             return logps, entropy
 
-        @staticmethod
-        @once_differentiable
+        @first_order
         def backward(ctx, g, h):
             if g is None and h is None:
                 return (None,) * 5
             hidden, weight, bias, targets, lse, entropy = ctx.saved_tensors
-            g, h = _upstream(g), _upstream(h)
+            g, h = upstream(g), upstream(h)
             dev = hidden.device
             with on_device(dev):
                 ws_bytes = flce_logprobs_workspace_size(ctx.p, FLCE_PASS_BACKWARD)
