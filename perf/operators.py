@@ -352,7 +352,7 @@ def _run_own(s):
                             entropy=s["entropies"], offsets=s["offsets"], mask=s["mask"], clip_low=CLIP_LOW,
                             clip_high=CLIP_HIGH, dual_clip=DUAL if s["dual"] else None,
                             kl_coef=KL if s["reference"] else 0.0, entropy_coef=ENTROPY if s["entropy"] else 0.0,
-                            reduction=s["reduction"])
+                            reduction=s["reduction"], advantages_per_sequence=s["per_sequence"])
     leaves = (s["logps"],) if s["entropies"] is None else (s["logps"], s["entropies"])
     grads = torch.autograd.grad(loss, leaves, s["grad"])
     out = dict(loss=loss.detach(), grad=grads[0])
