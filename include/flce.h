@@ -337,7 +337,7 @@ int flce_weighted_mse_chunk(void* user, int64_t row0, int64_t rows, int64_t voca
  * Log-probabilities of the targets and entropies, per token, with gradients:
  *   logp_i = z_{i,t_i} - LSE_i,   H_i = -sum_j p_ij log p_ij,   p_ij = exp(z_ij - LSE_i),
  * z as in flce_forward.  params->reduction must be FLCE_REDUCTION_NONE and z_loss
- * 0.  Rows whose target is ignored (or out of range, see flce_get_status) give 0
+ * 0; targets and the fp32 vectors need the alignment of their element only.  Rows whose target is ignored (or out of range, see flce_get_status) give 0
  * and take no gradient, whatever their hidden state holds.  A logit of -inf (a bias that masks vocabulary entries)
  * has probability 0, and one below -2^99 counts as -inf; a row whose every logit
  * does gives NaN.
@@ -361,6 +361,9 @@ int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* 
  *  grad_logps, grad_entropy: device fp32 (N); NULL = zeros.
  *  grad_hidden, grad_weight, grad_bias, flags: as flce_backward, except that each
  *  may be NULL where it is not wanted (a frozen head, say), which saves its work.
+ * The logit gradient that feeds the contractions is held in the input dtype (fp16:
+ * scaled, as in flce_backward); up to 64 tokens, where one rounded entry can be most
+ * of a gradient, as the rounded value and the rest.
  */
 int flce_logprobs_backward(const flce_params* p, const void* hidden, const void* weight, const void* bias,
                            const void* targets, const float* lse, const float* entropy, const float* grad_logps,

@@ -242,14 +242,15 @@ def _policy_function():
 def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, offsets=None, mask=None,
                 clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: Optional[float] = None,
                 kl_coef: float = 0.0, entropy_coef: float = 0.0, reduction: str = "mean",
-                return_metrics: bool = False):
+                return_metrics: bool = False, advantages_per_sequence: Optional[bool] = None):
     """Clipped policy loss with a KL term, differentiable in ``logps`` and ``entropy``.
 
     Per kept token, with r = exp(logps - old_logps) and A its advantage:
       s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A); for A < 0 and ``dual_clip`` c: max(s, c A)
       k = e^d - d - 1 with d = ref_logps - logps
       loss = -s + kl_coef k - entropy_coef entropy
-    ``advantages`` (fp32): the tokens' shape, or one value per sequence, (S,) or (S, 1).
+    ``advantages`` (fp32): the tokens' shape, or one value per sequence, (S,) or (S, 1).  A packed batch
+    with as many tokens as sequences leaves (S,) open: ``advantages_per_sequence`` says which.
     ``reduction``: "mean" over the kept tokens, "sequence_mean" (mean over sequences of each one's
     mean, sequences without a kept token left out), "sum", or "none" (the tokens' shape).  A mean of
     nothing is NaN, with zero gradients.
@@ -273,15 +274,18 @@ def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, o
     others = [("old_logps", old_logps), ("ref_logps", ref_logps), ("entropy", entropy)]
     constants = [("old_logps", old_logps), ("ref_logps", ref_logps), ("advantages", advantages)]
     n_seqs, length, flags = _check_tokens(logps, others, offsets, mask, constants, [("advantages", advantages)])
+    per_token = advantages.shape == logps.shape
     per_seq = tuple(advantages.shape) in ((n_seqs,), (n_seqs, 1))
-    if advantages.shape == logps.shape:
-        if per_seq and advantages.dim() == 1:
-            raise ValueError(f"advantages of shape {tuple(advantages.shape)} could be per token or per sequence: "
-                             f"pass ({n_seqs}, 1) for one per sequence, or pad the packed tokens")
-        per_seq = False
-    elif not per_seq:
-        raise ValueError(f"advantages must have logps' shape {tuple(logps.shape)} or ({n_seqs},), "
-                         f"got {tuple(advantages.shape)}")
+    if advantages_per_sequence is not None:
+        per_token, per_seq = per_token and not advantages_per_sequence, per_seq and advantages_per_sequence
+    if not (per_token or per_seq):
+        wanted = {None: f"logps' shape {tuple(logps.shape)} or ({n_seqs},)", True: f"shape ({n_seqs},)",
+                  False: f"logps' shape {tuple(logps.shape)}"}[advantages_per_sequence]
+        raise ValueError(f"advantages must have {wanted}, got {tuple(advantages.shape)}")
+    if per_token and per_seq and advantages.dim() == 1 and n_seqs > 1:
+        raise ValueError(f"advantages of shape {tuple(advantages.shape)} could be per token or per sequence: "
+                         "say advantages_per_sequence=True or False")
+    per_seq = not per_token
     if per_seq:
         if n_seqs > 1 and advantages.stride(0) != 1:
             raise ValueError("advantages must be contiguous")

@@ -166,6 +166,9 @@ __device__ __forceinline__ void step_tokens(const Seqs& q, const Chunk& c, int64
       for (int j = 0; j < 4; j++)
         if (t + tok<VEC>(j, lane) >= edge) seq[j] = walk.s;
     }
+    // (offsets that decrease, against the rules, may lead the search past the last sequence)
+#pragma unroll
+    for (int j = 0; j < 4; j++) keep[j] = keep[j] && seq[j] >= 0 && seq[j] < q.S;
   }
 }
 

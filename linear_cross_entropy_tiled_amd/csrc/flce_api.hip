@@ -526,6 +526,11 @@ int flce_scale_gradients(const flce_params* p, const float* g, void* grad_hidden
 // The int32 sums of up to 2^17 products of magnitude at most 127^2 stay below 2^31.
 static constexpr int64_t kMaxInt8Hidden = int64_t(1) << 17;
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+static bool targets_aligned(const Plan& pl, const void* t) {   // read one at a time, unlike the matrices
+  return (reinterpret_cast<uintptr_t>(t) & (pl.tgt_i32 ? 3 : 7)) == 0;
+}
+
 // The log-probability entry points take the loss's parameters, of which the
 // reduction and the z-loss have no meaning there.
 static int logprobs_plan(const flce_params* p, bool int8, Plan* pl, LpPlan* lp) {
@@ -563,7 +568,8 @@ int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* 
   pl.has_bias = bias != nullptr;
   if (!workspace || !weight) return FLCE_ERR_INVALID_ARG;
   if (pl.N > 0 && (!hidden || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
-  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) || !aligned16(targets))
+  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) ||
+      !targets_aligned(pl, targets) || !aligned4(logps) || !aligned4(entropy) || !aligned4(lse))
     return FLCE_ERR_UNSUPPORTED;
   if (workspace_bytes < lp.f_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   const hipError_t e = launch_logprobs(pl, lp, hidden, weight, bias, nullptr, nullptr, targets, logps, entropy, lse,
@@ -585,7 +591,8 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
   if (pl.N > 0 && grad_entropy && !entropy) return FLCE_ERR_INVALID_ARG;
   if (grad_bias && !bias) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(workspace) ||
-      !aligned16(targets) || !aligned16(grad_hidden) || !aligned16(grad_weight) || !aligned16(grad_bias))
+      !targets_aligned(pl, targets) || !aligned4(lse) || !aligned4(entropy) || !aligned4(grad_logps) ||
+      !aligned4(grad_entropy) || !aligned16(grad_hidden) || !aligned16(grad_weight) || !aligned16(grad_bias))
     return FLCE_ERR_UNSUPPORTED;
   if (workspace_bytes < lp.b_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   const LpGrad g{grad_logps, grad_entropy, entropy};
@@ -599,7 +606,7 @@ int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, voi
   if (!valid_dtype(dtype) || rows < 0 || cols <= 0) return FLCE_ERR_INVALID_ARG;
   if (rows > 0 && (!x || !q || !scale)) return FLCE_ERR_INVALID_ARG;
   if (cols % 16 != 0 || rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30) || !aligned16(x) || !aligned16(q) ||
-      (reinterpret_cast<uintptr_t>(scale) & 3) != 0)
+      !aligned4(scale))
     return FLCE_ERR_UNSUPPORTED;
   const hipError_t e = launch_quantize(dtype, x, rows, cols, static_cast<int8_t*>(q), scale,
                                        static_cast<hipStream_t>(stream));
@@ -627,7 +634,8 @@ int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hi
   if (!workspace || !weight || !weight_scale) return FLCE_ERR_INVALID_ARG;
   if (pl.N > 0 && (!hidden || !hidden_scale || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(weight_scale) ||
-      !aligned16(workspace) || !aligned16(targets) || (reinterpret_cast<uintptr_t>(hidden_scale) & 3) != 0)
+      !aligned16(workspace) || !targets_aligned(pl, targets) || !aligned4(hidden_scale) || !aligned4(logps) ||
+      !aligned4(entropy) || !aligned4(lse))
     return FLCE_ERR_UNSUPPORTED;
   if (workspace_bytes < lp.f_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   const hipError_t e = launch_logprobs(pl, lp, hidden, weight, bias, hidden_scale, weight_scale, targets, logps, entropy,

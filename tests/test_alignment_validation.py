@@ -76,6 +76,8 @@ def _policy(**change):
     (dict(reduction="token"), ValueError),
     # packed, as many tokens as sequences: per token or per sequence?
     (dict(logps=torch.zeros(S), old_logps=torch.zeros(S), offsets=torch.zeros(S + 1, dtype=torch.int32)), ValueError),
+    (dict(advantages_per_sequence=False), ValueError),
+    (dict(advantages=torch.zeros(S, L), advantages_per_sequence=True), ValueError),
 ])
 def test_policy_loss_rejects(change, exc):
     with pytest.raises(exc):

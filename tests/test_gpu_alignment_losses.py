@@ -349,3 +349,36 @@ def test_gradients_of_one_input_alone(flce_lib, reduction):
         x = lp.detach().clone().requires_grad_(True)
         d, = torch.autograd.grad(flce_lib.policy_loss(x, lp.detach(), adv), x, create_graph=True)
         torch.autograd.grad(d.sum(), x)
+
+
+def test_as_many_packed_tokens_as_sequences(flce_lib):
+    """(S,) advantages are per token or per sequence as the caller says: sequences of 0, 3, 1 and 0 tokens."""
+    import torch
+    lp = torch.tensor([-1.0, -2.0, -0.5, -3.0], device="cuda")
+    old, adv = lp - 0.1, torch.tensor([1.0, -2.0, 3.0, -4.0], device="cuda")
+    off = torch.tensor([0, 0, 3, 4, 4], device="cuda")
+    for flag, want in ((True, [-2.0, -2.0, -2.0, 3.0]), (False, [1.0, -2.0, 3.0, -4.0])):
+        loss = flce_lib.policy_loss(lp, old, adv, offsets=off, reduction="none", advantages_per_sequence=flag)
+        assert torch.allclose(loss, -torch.tensor(want, device="cuda") * torch.exp(lp - old), rtol=1e-6)
+    loss = flce_lib.policy_loss(lp, old, adv[:, None], offsets=off, reduction="none")
+    assert torch.equal(loss, flce_lib.policy_loss(lp, old, adv, offsets=off, reduction="none",
+                                                  advantages_per_sequence=True))
+    one = flce_lib.policy_loss(lp[:1], old[:1], adv[:1], offsets=torch.tensor([0, 1], device="cuda"))
+    assert torch.allclose(one, -torch.exp(lp[0] - old[0]), rtol=1e-6)
+
+
+@pytest.mark.parametrize("s", [6, 200])
+def test_offsets_against_the_rules_stay_inside_the_buffers(flce_lib, s):
+    """Decreasing, negative and too large offsets: some answer, and zero gradients outside [first, last)."""
+    import torch
+    t = 3000
+    g = torch.Generator().manual_seed(s)
+    lp = (-torch.rand(t, generator=g)).cuda().requires_grad_(True)
+    adv = torch.randn(s, 1, generator=g).cuda()
+    for k in range(4):
+        off = torch.randint(-2 * t, 3 * t, (s + 1,), generator=g)
+        off[0], off[-1] = 100 * k, t - 50 * k
+        loss = flce_lib.policy_loss(lp, lp.detach() - 0.1, adv, offsets=off.cuda(), reduction="sequence_mean")
+        pref = flce_lib.preference_loss(lp, offsets=off.cuda())
+        for grad in (torch.autograd.grad(loss, lp)[0], torch.autograd.grad(pref, lp)[0]):
+            assert not torch.any(grad[:100 * k]) and not torch.any(grad[t - 50 * k:])

@@ -248,6 +248,15 @@ def test_empty_batch_and_status(flce_lib):
         assert rc == 0 and flce_lib.get_status(ws) == code
 
 
+def test_targets_need_no_alignment(flce_lib):
+    import torch
+    x, w, b, t = (a.cuda() for a in _tensors(100, 64, 300, "bf16", seed=41))
+    longer = torch.cat([t[:1], t])
+    for dt in (torch.int64, torch.int32):
+        got = flce_lib.token_logprobs(x, w, longer.to(dt)[1:], b)
+        assert torch.equal(got, flce_lib.token_logprobs(x, w, t, b))
+
+
 def test_gradients_against_differences(flce_lib):
     """(f(x + d) - f(x - d)) / 2 |d| along random directions of hidden, weight and bias, fp32: the values'
     rounding 32 x 2^-24 x 300 / 2^-6 = 0.04 of a sum over 60 rows, the third-order term 2^-12 / 6 x 60."""

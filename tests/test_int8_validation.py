@@ -64,6 +64,6 @@ def test_abi_codes():
 
     for name in ("x", "s", "w", "ws", "t", "lp", "lse", "work"):
         assert call(**{name: None}) == bad, name
-    for name in ("x", "w", "ws", "b", "t", "work"):
+    for name in ("x", "w", "ws", "b", "work"):
         assert call(**{name: 24}) == odd, name
-    assert call(s=18) == odd and call(n=need - 1) == flce.FLCE_ERR_WORKSPACE_TOO_SMALL
+    assert call(s=18) == odd and call(t=20) == odd and call(lp=18) == odd and call(n=need - 1) == flce.FLCE_ERR_WORKSPACE_TOO_SMALL

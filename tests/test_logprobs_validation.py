@@ -51,7 +51,9 @@ def test_abi_codes():
     for name in ("x", "w", "t", "lse", "ent", "ws"):
         assert bwd(**{name: None}) == bad, name
     assert bwd(gb=16) == bad                     # a bias gradient without a bias
-    for name in ("x", "w", "b", "t", "ws"):
+    for name in ("x", "w", "b", "ws"):
         assert fwd(**{name: 24}) == odd and bwd(**{name: 24}) == odd, name
+    assert fwd(t=20) == odd and bwd(t=20) == odd         # int64 values
+    assert fwd(lp=18) == odd and fwd(lse=18) == odd and bwd(g=18) == odd and bwd(e=18) == odd
     assert fwd(n=need[0] - 1) == flce.FLCE_ERR_WORKSPACE_TOO_SMALL
     assert bwd(n=need[1] - 1) == flce.FLCE_ERR_WORKSPACE_TOO_SMALL
