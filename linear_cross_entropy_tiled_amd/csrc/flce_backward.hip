@@ -23,6 +23,7 @@
 // D with fp16's full precision.  For bf16 and fp32 the factor is 1.
 #include "flce_device.h"
 #include "flce_internal.h"
+#include "flce_lp_state.h"
 
 namespace flce {
 
@@ -273,7 +274,10 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
   // 4 r (1 - r) and p = exp2(r * (-2 cap log2e) + cap log2e - LSE log2e).
   // Per token: cAs = scale coefA (4x with the cap), cBs likewise, k0 = the
   // exponent's constant term (or -LSE log2e without the cap).
-  const float s2 = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale;   // scale folded into the exp argument
+  // kTanh: fp32 with an entropy's gradient, in tanh(v / cap) as the forward that belongs to it.
+  constexpr bool kTanh = ENTROPY && SOFTCAP && sizeof(T) == 4;
+  const float s2 = kTanh ? a.scale / a.cap
+                         : (SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale);   // scale folded into the exp argument
   const float k1 = -a.two_cap * kLog2e;
   const float cmul = (SOFTCAP ? 4.0f * a.scale : a.scale) * a.dscale[0];
   float cAs[kNI], cBs[kNI], cEs[kNI], k0[kNI];
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
     cBs[ni] = reinterpret_cast<const float*>(vec_lds + 1024)[tl] * cmul;
     if constexpr (ENTROPY) cEs[ni] = reinterpret_cast<const float*>(vec_lds + 4096)[tl] * cmul;
     const float lL = reinterpret_cast<const float*>(vec_lds + 2048)[tl];
-    k0[ni] = SOFTCAP ? fmaf(a.cap, kLog2e, -lL) : -lL;
+    k0[ni] = SOFTCAP && !kTanh ? fmaf(a.cap, kLog2e, -lL) : -lL;
     rel[ni] = reinterpret_cast<const int*>(vec_lds + 3072)[tl] - vw;
   }
   // whether any lane's target row lies in this wave's 128 rows, per column tile
@@ -312,7 +316,12 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
       for (int r = 0; r < 4; r++) {
         float v = HAS_BIAS ? fmaf(acc[mi][ni][r], s2, sb[r]) : acc[mi][ni][r] * s2;
         if constexpr (ENTROPY && SOFTCAP) v = fmaxf(v, kMasked);
-        if constexpr (SOFTCAP) {
+        if constexpr (kTanh) {
+          float slope;
+          const float x = fmaf(a.cap * kLog2e, tanh_of<true>(v, &slope), k0[ni]);
+          f[r] = 0.25f * slope;
+          d[r] = (fast_exp2(x) * fmaf(x, cEs[ni], cAs[ni])) * f[r];
+        } else if constexpr (SOFTCAP) {
           const float rr = fast_rcp(fast_exp2(v) + 1.0f);
           const float x = fmaf(rr, k1, k0[ni]);   // log2 p
           const float p = fast_exp2(x);

@@ -46,7 +46,7 @@ struct LpTileArgs {
   int tgt_i32;
   int N, H, V;
   int64_t ignore_index;
-  float scale, cap, two_log2e_over_cap;
+  float scale, cap;
   int v_first;                // first vocabulary row of the launch
   int n_vt, S;                // its vocabulary tiles (256 or 64 rows) and splits
   int S_all, s_first, N_pad;

@@ -22,6 +22,42 @@ __device__ __forceinline__ void lp_merge(LpState& a, const LpState& b) {
   a.yt = fmaxf(a.yt, b.yt);
 }
 
+// tanh(w), for the softcap z = cap tanh(v / cap).  Up to |w| = 0.8 (logits up to two
+// thirds of the cap) w + w^3 p(w^2), p of degree 6 fitted to a relative error of 2e-10:
+// 1 - 2 / (e^2w + 1) is off by 1e-7 of 1 there, and the logit by 1e-7 of the cap, however
+// small it is.  Its eight multiply-adds cost what the exponential and the reciprocal do.
+// WIDE, for a wave that holds a larger w somewhere: the formula for those and only those,
+// so that no value depends on its neighbours.
+constexpr float kTanhNear = 0.8f;
+template <bool WIDE> __device__ __forceinline__ float tanh_of(float w) {
+  const float t = w * w;
+  float p = fmaf(t, -0.0005726429517380893f, 0.002854352118447423f);
+  p = fmaf(t, p, -0.008510654792189598f);
+  p = fmaf(t, p, 0.02177303470671177f);
+  p = fmaf(t, p, -0.0539538599550724f);
+  p = fmaf(t, p, 0.133332297205925f);
+  p = fmaf(t, p, -0.3333333134651184f);
+  p = fmaf(w * t, p, w);
+  if constexpr (WIDE) {
+    const float far = fmaf(-2.0f, fast_rcp(fast_exp2(2.0f * kLog2e * w) + 1.0f), 1.0f);
+    p = fabsf(w) > kTanhNear ? far : p;
+  }
+  return p;
+}
+
+// The same with the slope, 1 - tanh^2.  Where tanh comes near 1 that would lose its digits,
+// and 4 r (1 - r) of r = 1 / (e^2w + 1) does not.
+template <bool WIDE> __device__ __forceinline__ float tanh_of(float w, float* slope) {
+  float th = tanh_of<false>(w);
+  *slope = fmaf(-th, th, 1.0f);
+  if (WIDE && fabsf(w) > kTanhNear) {
+    const float r = fast_rcp(fast_exp2(2.0f * kLog2e * w) + 1.0f);
+    th = fmaf(-2.0f, r, 1.0f);
+    *slope = 4.0f * fmaf(-r, r, r);
+  }
+  return th;
+}
+
 template <typename T> struct BiasOf { typedef T type; };
 template <> struct BiasOf<int8_t> { typedef float type; };
 

@@ -36,7 +36,7 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
   const int t0 = tt * BN;
   if (blockIdx.x == 0 && tid == 0) a.status[0] = FLCE_OK;
 
-  const float s_u = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale * kLog2e;
+  const float s_u = SOFTCAP ? a.scale / a.cap : a.scale * kLog2e;   // as in lp_tiles_kernel
   const float cap2 = a.cap * kLog2e;
   LpState st[NI];
   int tgt[NI];
@@ -101,14 +101,16 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
     for (int mi = 0; mi < MI; mi++)
 #pragma unroll
       for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kt = 0; kt < KT; kt++, left--) {
-      if (left >= kStages - 1) small::wait_stage<T, true, true, BN, kStages - 2>(lb.loads);
-      else wait_loads();
-      __syncthreads();   // the stage has landed for every wave, and every wave has read the one before
-      load_next();       // into the buffer of the one before
-      small::stage_mma<T, true, true, BN>(lds + buf * SB, wm, wn, lane, acc);
-      buf = buf == kStages - 1 ? 0 : buf + 1;
-    }
+    small::in_blocks<T, BN>(KT, acc, [&](int kt, int end, Acc (&to)[MI][NI]) {
+      for (; kt < end; kt++, left--) {
+        if (left >= kStages - 1) small::wait_stage<T, true, true, BN, kStages - 2>(lb.loads);
+        else wait_loads();
+        __syncthreads();   // the stage has landed for every wave, and every wave has read the one before
+        load_next();       // into the buffer of the one before
+        small::stage_mma<T, true, true, BN>(lds + buf * SB, wm, wn, lane, to);
+        buf = buf == kStages - 1 ? 0 : buf + 1;
+      }
+    });
 
     float sb[MI][4], ws[MI][4];
 #pragma unroll
@@ -121,6 +123,19 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
       }
       if constexpr (I8) lds_vec4<float>(scale_lds[side], row, ws[mi]);
     }
+    float size = 0.0f;
+#pragma unroll
+    for (int ni = 0; ni < NI; ni++)
+#pragma unroll
+      for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          float u = I8 ? (float)__builtin_bit_cast(int, (float)acc[mi][ni][r]) * ws[mi][r] : acc[mi][ni][r];
+          u = HAS_BIAS ? fmaf(u, s_a[ni], sb[mi][r]) : u * s_a[ni];
+          acc[mi][ni][r] = u;
+          size = fmaxf(size, fabsf(u));
+        }
+    const bool wide = SOFTCAP && __builtin_amdgcn_ballot_w64(size > kTanhNear) != 0;
 #pragma unroll
     for (int ni = 0; ni < NI; ni++) {
       float mu = kMasked;
@@ -128,9 +143,8 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
       for (int mi = 0; mi < MI; mi++)
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          float u = I8 ? (float)__builtin_bit_cast(int, (float)acc[mi][ni][r]) * ws[mi][r] : acc[mi][ni][r];
-          u = HAS_BIAS ? fmaf(u, s_a[ni], sb[mi][r]) : u * s_a[ni];
-          if constexpr (SOFTCAP) u = fmaf(-2.0f * cap2, fast_rcp(fast_exp2(u) + 1.0f), cap2);
+          float u = acc[mi][ni][r];
+          if constexpr (SOFTCAP) u = cap2 * (wide ? tanh_of<true>(u) : tanh_of<false>(u));
           const int v = v0 + (wm * MI + mi) * 16 + 4 * (lane >> 4) + r;
           if (v == tgt[ni]) st[ni].yt = u;
           if (v >= a.V) u = 2.0f * kMasked;   // below every running maximum: adds 0
@@ -236,9 +250,27 @@ __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(Dlogits
     for (int ni = 0; ni < NI; ni++) acc[mi][ni] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
   small::mainloop<T, true, true, 64>(da, db, (a.H * E + kBKB - 1) / kBKB, lds, acc);
 
-  const float s2 = SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale;
-  const float k1 = -a.two_cap * kLog2e;
-  const float cmul = (SOFTCAP ? 4.0f * a.scale : a.scale) * a.dscale[0];
+  // with the cap u = v / cap, z = cap tanh(u) and softcap' = 1 - tanh^2(u)
+  const float s2 = SOFTCAP ? a.scale / a.cap : a.scale;
+  const float cap2 = a.cap * kLog2e;
+  const float cmul = a.scale * a.dscale[0];
+  float size = 0.0f;
+#pragma unroll
+  for (int ni = 0; ni < NI; ni++)
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        float u = acc[mi][ni][r] * s2;
+        if (HAS_BIAS) {
+          const int v = min(v0 + (wm * MI + mi) * 16 + 4 * (lane >> 4) + r, a.V - 1);
+          u = fmaf(acc[mi][ni][r], s2, (float)reinterpret_cast<const T*>(a.bias)[v] * s2);
+        }
+        if (SOFTCAP) u = fmaxf(u, kMasked);   // (not NaN: see bwd_dlogits_kernel, ENTROPY)
+        acc[mi][ni][r] = u;
+        size = fmaxf(size, fabsf(u));
+      }
+  const bool wide = SOFTCAP && __builtin_amdgcn_ballot_w64(size > kTanhNear) != 0;
   T* D = reinterpret_cast<T*>(a.D);
   float cs[MI][4];
 #pragma unroll
@@ -249,7 +281,6 @@ __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(Dlogits
   for (int ni = 0; ni < NI; ni++) {
     const int t = t0 + (wn * NI + ni) * 16 + (lane & 15);   // the per-token arrays hold whole 256-token tiles
     const float cA = a.coefA[t] * cmul, cB = a.coefB[t] * cmul, cE = a.coefE[t] * cmul, lL = a.lseL[t];
-    const float k0 = SOFTCAP ? fmaf(a.cap, kLog2e, -lL) : -lL;
     const int tg = a.tgt[t];
 #pragma unroll
     for (int mi = 0; mi < MI; mi++) {
@@ -258,15 +289,14 @@ __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(Dlogits
 #pragma unroll
       for (int r = 0; r < 4; r++) {
         const int v = v0 + vl + r;
-        float u = acc[mi][ni][r] * s2;
-        if (HAS_BIAS) u = fmaf(acc[mi][ni][r], s2, (float)reinterpret_cast<const T*>(a.bias)[min(v, a.V - 1)] * s2);
+        const float u = acc[mi][ni][r];
         if constexpr (SOFTCAP) {
-          u = fmaxf(u, kMasked);
-          const float rr = fast_rcp(fast_exp2(u) + 1.0f), x = fmaf(rr, k1, k0), f = fmaf(-rr, rr, rr);
+          float f;
+          const float x = fmaf(cap2, wide ? tanh_of<true>(u, &f) : tanh_of<false>(u, &f), -lL);
           d[r] = (fast_exp2(x) * fmaf(x, cE, cA)) * f;
           if (v == tg) d[r] -= cB * f;
         } else {
-          const float x = fmaxf(fmaf(u, kLog2e, k0), kMasked);
+          const float x = fmaxf(fmaf(u, kLog2e, -lL), kMasked);
           d[r] = fast_exp2(x) * fmaf(x, cE, cA);
           if (v == tg) d[r] -= cB;
         }

@@ -192,6 +192,27 @@ def test_masked_vocabulary_and_masked_rows(flce_lib):
     assert torch.all(gb[torch.from_numpy(np.flatnonzero(out)).cuda()] == 0)
 
 
+@pytest.mark.parametrize("n", [9, 40, 3000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_capped_infinite_logits_are_the_cap(flce_lib, n, dtype):
+    """cap tanh(-inf) = -cap: with the softcap a bias of -inf leaves an entry in, at the lowest
+    logit, also where whole tiles hold nothing else."""
+    import torch
+    x, w, b, t = _tensors(n, 64, 5000, dtype, seed=n)
+    low = np.random.default_rng(3).random(5000) < 0.3
+    low[:2100] = True
+    out = torch.from_numpy(low)
+    bias = torch.where(out, torch.tensor(-float("inf"), dtype=b.dtype), b)
+    lp, ent = flce_lib.token_logprobs(x.cuda(), w.cuda(), t.cuda(), bias.cuda(), softcap=2.0, return_entropy=True)
+    want_lp, want_h, _, _ = ao.token_logprobs(_np(x), _np(w), _np(bias), t.numpy(), softcap=2.0)
+    # as in _check_values; the capped entries are exact, |z| <= 2 and z.max - z.min <= 4
+    ez = _bounds(_np(x), _np(w), _np(torch.where(out, torch.zeros_like(b), b)), dtype, dict(softcap=2.0))
+    own = 8 * U32 * (2 + np.log(5000) + 1)
+    valid = t.numpy() >= 0
+    assert np.all(np.abs(_np(lp) - want_lp)[valid] <= (2 * ez + own)[valid])
+    assert np.all(np.abs(_np(ent) - want_h)[valid] <= ((1 + 2 * (4 + np.log(5000))) * ez + 2 * own)[valid])
+
+
 @pytest.mark.parametrize("cap", [None, 4.0])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_ignored_rows_hold_anything(flce_lib, cap, dtype):
