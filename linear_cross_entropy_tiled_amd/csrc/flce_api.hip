@@ -338,7 +338,7 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
     // tokens at H = 4096, V = 128256 in 8 bits: 130 us, rounded down 154; 40 at H = 2048,
     // V = 50000 in bf16: 60 against 68).  Otherwise the matrix instructions bound it, and it
     // is rounded down: more workgroups than fit at once even out, while one with a tile more
-    // than the others is waited for (64 fp32 tokens, same head: 604 us, rounded up 642).
+    // than the others is waited for (64 fp32 tokens, same head: 617 us, rounded up 660).
     const int64_t v64 = (rest + 63) / 64;
     const bool streams = L.bn == 16 || (P.N <= 64 && (P.int8 || P.dtype != FLCE_F32));
     int64_t each = streams ? (v64 + wg_target - 1) / wg_target : v64 * ((P.N + 63) / 64) / wg_target;

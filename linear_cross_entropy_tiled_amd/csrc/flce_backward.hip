@@ -274,10 +274,13 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
   // 4 r (1 - r) and p = exp2(r * (-2 cap log2e) + cap log2e - LSE log2e).
   // Per token: cAs = scale coefA (4x with the cap), cBs likewise, k0 = the
   // exponent's constant term (or -LSE log2e without the cap).
-  // kTanh: fp32 with an entropy's gradient, in tanh(v / cap) as the forward that belongs to it.
-  constexpr bool kTanh = ENTROPY && SOFTCAP && sizeof(T) == 4;
+  // ENTROPY: from the products on as lp_tiles_kernel and lp_small_kernel, in base 2 (another
+  // rounding of the scale would be off by 6e-8 of the logit in every p), and with the cap in
+  // fp32 in tanh(v / cap).
+  constexpr bool kTanh = ENTROPY && SOFTCAP && sizeof(T) == 4, kBase2 = ENTROPY && !SOFTCAP;
   const float s2 = kTanh ? a.scale / a.cap
-                         : (SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale);   // scale folded into the exp argument
+                 : kBase2 ? a.scale * kLog2e
+                          : (SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale);   // scale folded into the exp argument
   const float k1 = -a.two_cap * kLog2e;
   const float cmul = (SOFTCAP ? 4.0f * a.scale : a.scale) * a.dscale[0];
   float cAs[kNI], cBs[kNI], cEs[kNI], k0[kNI];
@@ -329,7 +332,7 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
           if constexpr (ENTROPY) d[r] = (p * fmaf(x, cEs[ni], cAs[ni])) * f[r];
           else d[r] = (p * cAs[ni]) * f[r];
         } else {
-          const float x = fmaf(v, kLog2e, k0[ni]);
+          const float x = kBase2 ? v + k0[ni] : fmaf(v, kLog2e, k0[ni]);
           if constexpr (ENTROPY) {
             const float xf = fmaxf(x, kMasked);
             d[r] = fast_exp2(xf) * fmaf(xf, cEs[ni], cAs[ni]);

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   // H = 4096, V = 32768 with the cap: bf16 1558 us, with tanh_of 1582 to 1630; 8-bit 836,
   // 858 to 914.)
   constexpr bool kExact = E == 4;
-  const float s_u = SOFTCAP ? a.scale / a.cap * (kExact ? 1.0f : 2.0f * kLog2e) : a.scale * kLog2e;
+  const float s_u = !SOFTCAP ? a.scale * kLog2e : kExact ? a.scale / a.cap : a.scale * (2.0f * kLog2e / a.cap);
   const float cap2 = a.cap * kLog2e;
   auto capped = [&](float u, float minus) {
     if constexpr (kExact) return fmaf(cap2, tanh_of<true>(u), -minus);
@@ -492,7 +492,10 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
 // g of log p_t and h of H,
 //   d / d z_j = g [j = t] - p_j (g + h (H + log p_j))
 //             = coefA p_j + coefE p_j log2 p_j - coefB [j = t],
-// coefA = -(g + h H), coefE = -h ln 2, coefB = -g.
+// coefA = -(g + h H), coefE = -h ln 2, coefB = -g.  The kernels subtract the LSE in base 2,
+// L, as one fp32 number: its rounding (1e-6 at 16 to 32, which every p of the row would carry)
+// is taken back by the constants: with L = Lf + d and p = 2^-d p',
+//   coefA p + coefE p log2 p = p' (2^-d (coefA - d coefE) + 2^-d coefE log2 p').
 struct LpPrepArgs {
   const void* targets;
   int tgt_i32;
@@ -529,13 +532,18 @@ __global__ __launch_bounds__(1024) void lp_prep_kernel(LpPrepArgs a) {
       const bool in_range = t >= 0 && t < a.V;
       bad |= (t != a.ignore_index && !in_range) ? 1 : 0;
       if (t != a.ignore_index && in_range) {
-        ll = a.lse[i] * kLog2e;
+        const double exact = (double)a.lse[i] / (double)kLn2;   // as lp_rows_kernel took it times kLn2
+        ll = (float)exact;
+        const float d = fabsf(ll) < INFINITY ? (float)(exact - (double)ll) : 0.0f;
         const float g = a.grad_logps ? a.grad_logps[i] : 0.0f;
         const float h = a.grad_entropy ? a.grad_entropy[i] : 0.0f;
         cb = -g;
         ca = a.grad_entropy ? -fmaf(h, a.entropy[i], g) : -g;
-        if (isnan(ll)) ca = ll;
         ce = -h * kLn2;
+        const float back = exp2f(-d);
+        ca = back * fmaf(-d, ce, ca);
+        ce *= back;
+        if (isnan(ll)) ca = ll;
         tg = (int)t;
       }
     }

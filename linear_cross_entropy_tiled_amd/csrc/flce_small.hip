@@ -251,7 +251,8 @@ __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(Dlogits
   small::mainloop<T, true, true, 64>(da, db, (a.H * E + kBKB - 1) / kBKB, lds, acc);
 
   // with the cap u = v / cap, z = cap tanh(u) and softcap' = 1 - tanh^2(u)
-  const float s2 = SOFTCAP ? a.scale / a.cap : a.scale;
+  // without it u = y, as in the forward (bwd_dlogits_kernel has the reason)
+  const float s2 = SOFTCAP ? a.scale / a.cap : a.scale * kLog2e;
   const float cap2 = a.cap * kLog2e;
   const float cmul = a.scale * a.dscale[0];
   float size = 0.0f;
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(small::kThreadsS) void dlogits_small_kernel(Dlogits
           d[r] = (fast_exp2(x) * fmaf(x, cE, cA)) * f;
           if (v == tg) d[r] -= cB * f;
         } else {
-          const float x = fmaxf(fmaf(u, kLog2e, -lL), kMasked);
+          const float x = fmaxf(u - lL, kMasked);
           d[r] = fast_exp2(x) * fmaf(x, cE, cA);
           if (v == tg) d[r] -= cB;
         }
