@@ -340,9 +340,11 @@ __global__ __launch_bounds__(1024) void preference_pairs_kernel(PreferenceArgs a
     double loss, slope;   // slope = d loss / d h
     if (a.type == FLCE_PREFERENCE_SIGMOID) {
       const double eps = a.smoothing;
-      const double soft = fmax(-h, 0.0) + log1p(exp(-fabs(h)));   // -log sigmoid(h); -log sigmoid(-h) = soft + h
-      // (1 - eps) soft + eps (soft + h), without inf - inf at an infinite margin
-      loss = eps > 0.0 ? soft + eps * h : soft;
+      // -log sigmoid(h) = max(-h, 0) + near and -log sigmoid(-h) = max(h, 0) + near, each of one sign, and one
+      // of weight 0 left out: an infinite margin is no inf - inf and no 0 times inf
+      const double near = log1p(exp(-fabs(h)));
+      loss = eps < 1.0 ? (1.0 - eps) * (fmax(-h, 0.0) + near) : 0.0;
+      if (eps > 0.0) loss += eps * (fmax(h, 0.0) + near);
       slope = 1.0 / (1.0 + exp(-h)) - (1.0 - eps);
       if (eps == 0.0) slope = -1.0 / (1.0 + exp(h));
     } else if (a.type == FLCE_PREFERENCE_HINGE) {
