@@ -496,8 +496,10 @@ typedef struct {
   double clip_low;            /* >= 0                                                    */
   double clip_high;           /* >= 0                                                    */
   double dual_clip;           /* > 1, or 0 = off                                         */
-  double kl_coef;             /* finite; 0 without a reference                           */
-  double entropy_coef;        /* finite; 0 without entropies                             */
+  double kl_coef;             /* finite; 0 without a reference, or with one that serves
+                                 the metric alone: the term is then left out, whatever
+                                 the reference holds                                     */
+  double entropy_coef;        /* finite; 0 without entropies, which are then not read    */
 } flce_policy_params;
 
 typedef struct {

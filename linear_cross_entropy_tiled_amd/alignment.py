@@ -248,7 +248,7 @@ def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, o
     Per kept token, with r = exp(logps - old_logps) and A its advantage:
       s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A); for A < 0 and ``dual_clip`` c: max(s, c A)
       k = e^d - d - 1 with d = ref_logps - logps
-      loss = -s + kl_coef k - entropy_coef entropy
+      loss = -s + kl_coef k - entropy_coef entropy,  a term with coefficient 0 left out
     ``advantages`` (fp32): the tokens' shape, or one value per sequence, (S,) or (S, 1).  A packed batch
     with as many tokens as sequences leaves (S,) open: ``advantages_per_sequence`` says which.
     ``reduction``: "mean" over the kept tokens, "sequence_mean" (mean over sequences of each one's

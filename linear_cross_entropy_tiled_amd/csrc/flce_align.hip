@@ -446,7 +446,8 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(PolicyArgs a) {
   const T* lp = reinterpret_cast<const T*>(a.logps) + c.row * a.ld_logps;
   const T* old = reinterpret_cast<const T*>(a.old) + c.row * a.ld_old;
   const T* ref = a.ref ? reinterpret_cast<const T*>(a.ref) + c.row * a.ld_ref : nullptr;
-  const T* ent = a.entropy ? reinterpret_cast<const T*>(a.entropy) + c.row * a.ld_entropy : nullptr;
+  const bool with_ent = a.entropy && a.entropy_coef != 0.0f;   // (0 times what entropies hold may be NaN)
+  const T* ent = with_ent ? reinterpret_cast<const T*>(a.entropy) + c.row * a.ld_entropy : nullptr;
   const float* adv = a.adv_per_seq ? a.adv : a.adv + c.row * a.ld_adv;
   auto load = [&](int64_t t, StepIn<5>& in) {
     const int n = step_size(c, t);
@@ -490,8 +491,10 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(PolicyArgs a) {
       if (ref) {
         const float away = r[j] - x[j], em1 = expm1f(away);
         const float k = exp_excess(away, em1);
-        l = fmaf(a.kl_coef, k, l);
-        d = fmaf(-a.kl_coef, em1, d);
+        if (a.kl_coef != 0.0f) {   // (0 times an infinite k, of a reference for its metric alone, is NaN)
+          l = fmaf(a.kl_coef, k, l);
+          d = fmaf(-a.kl_coef, em1, d);
+        }
         if (keep[j]) kl += (double)k;
       }
       if (ent) l = fmaf(-a.entropy_coef, h[j], l);
