@@ -178,7 +178,7 @@ def preference_loss(logps, ref_logps=None, *, offsets=None, mask=None, beta: flo
     p = flce_preference_params(n_seqs, length, DTYPES[_dtype_name(logps)], REDUCTIONS[reduction],
                                PREFERENCE_TYPES[loss_type], flags, 1 if length_normalize else 0, 0, beta,
                                label_smoothing, margin)
-    if differentiable(logps):
+    if differentiable(logps, ref_logps):
         loss, rewards = _preference_function().apply(logps, ref_logps, mask, offsets, p)
     else:
         loss, rewards, _ = _preference_forward(p, logps, ref_logps, mask, offsets)
@@ -295,7 +295,7 @@ def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, o
     p = flce_policy_params(n_seqs, length, DTYPES[_dtype_name(logps)], POLICY_REDUCTIONS[reduction], flags, 0,
                            clip_low, clip_high, dual_clip or 0.0, kl_coef, entropy_coef)
     metrics = torch.empty(2, dtype=torch.int64, device=logps.device) if return_metrics else None
-    if differentiable(logps, entropy):
+    if differentiable(logps, entropy, old_logps, ref_logps, advantages):
         loss = _policy_function().apply(logps, entropy, old_logps, ref_logps, advantages, mask, offsets, p, metrics)
     else:
         loss, *_ = _policy_forward(p, logps, old_logps, ref_logps, entropy, advantages, mask, offsets, False, metrics)

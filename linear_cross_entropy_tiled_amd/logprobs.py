@@ -30,9 +30,21 @@ def stream_handle(device):
 
 
 def differentiable(*tensors) -> bool:
-    """Whether autograd records this call (without, the autograd op's own cost is saved)."""
+    """Whether the call goes through its autograd function: autograd records it (without, the function's own cost
+    is saved), or an input carries a forward-mode tangent, which the function refuses to drop."""
     import torch
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    return has_tangent(*tensors)
+
+
+def has_tangent(*tensors) -> bool:
+    """Whether one of them is a dual tensor of forward-mode autograd (no_grad does not take tangents away)."""
+    import torch
+    ad = torch.autograd.forward_ad
+    if getattr(ad, "_current_level", 0) < 0:       # no level is open: there are none (0.4 us a tensor saved)
+        return False
+    return any(t is not None and ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def first_order(backward):
@@ -142,7 +154,8 @@ def _quantize(x):
 def quantize_int8(x):
     """Rows of x (R, H) as 8-bit integers: (q int8 (R, H), scale fp32 (R,)), x ~ scale[:, None] * q, with
     scale = max|row| / 127.  For a weight (V, H) once, when a scorer is loaded.  H must be a multiple of 16.
-    All-zero rows give scale 0, rows with NaN or infinities scale NaN."""
+    All-zero rows give scale 0, rows with NaN or infinities scale NaN.  Neither output has a gradient: x is a
+    constant here, also where it requires one."""
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
     _dtype_name(x)
@@ -189,10 +202,10 @@ def _check_int8(hidden, weight, weight_scale, targets, bias, hidden_scale):
     for name, t in named:
         if t is not None and (t.device.type != "cuda" or t.device != hidden.device):
             raise ValueError(f"{name} must be on hidden's GPU ({hidden.device}), not {t.device}")
-    if torch.is_grad_enabled():
-        for name, t in named:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"8-bit scores have no gradient: detach {name}, or use token_logprobs")
+    recorded = torch.is_grad_enabled()
+    for name, t in named:
+        if t is not None and ((recorded and t.requires_grad) or has_tangent(t)):
+            raise ValueError(f"8-bit scores have no gradient: detach {name}, or use token_logprobs")
 
 
 def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
