@@ -337,10 +337,13 @@ int flce_weighted_mse_chunk(void* user, int64_t row0, int64_t rows, int64_t voca
  * Log-probabilities of the targets and entropies, per token, with gradients:
  *   logp_i = z_{i,t_i} - LSE_i,   H_i = -sum_j p_ij log p_ij,   p_ij = exp(z_ij - LSE_i),
  * z as in flce_forward.  params->reduction must be FLCE_REDUCTION_NONE and z_loss
- * 0; targets and the fp32 vectors need the alignment of their element only.  Rows whose target is ignored (or out of range, see flce_get_status) give 0
- * and take no gradient, whatever their hidden state holds.  A logit of -inf (a bias that masks vocabulary entries)
- * has probability 0, and one below -2^99 counts as -inf; a row whose every logit
- * does gives NaN.
+ * 0.  hidden, weight, bias, their gradients and the workspace are 16-byte aligned;
+ * targets and the fp32 vectors logps, entropy, lse and their gradients need the
+ * alignment of their element only.
+ * Rows whose target is ignored (or out of range, see flce_get_status) give 0 and
+ * take no gradient, whatever their hidden state holds.  A logit of -inf (a bias
+ * that masks vocabulary entries) has probability 0, and one below -2^99 counts as
+ * -inf; a row whose every logit does gives NaN.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace one call of `pass` needs (flce_pass).  Host only. */
@@ -393,8 +396,9 @@ int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, voi
 int flce_logprobs_int8_workspace_size(const flce_params* p, size_t* bytes);
 
 /* hidden (N, H) and weight (V, H): device int8 within [-127, 127]; hidden_scale
- * (N), weight_scale (V), bias (V, or NULL): device fp32; outputs and rows without
- * a target as flce_logprobs_forward. */
+ * (N), weight_scale (V), bias (V, or NULL): device fp32.  weight_scale and bias are
+ * 16-byte aligned as the matrices are, hidden_scale as its element; outputs and rows
+ * without a target as flce_logprobs_forward. */
 int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hidden_scale, const void* weight,
                        const float* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
                        float* lse, void* workspace, size_t workspace_bytes, void* stream);

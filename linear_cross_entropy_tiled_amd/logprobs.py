@@ -208,6 +208,12 @@ def _check_int8(hidden, weight, weight_scale, targets, bias, hidden_scale):
             raise ValueError(f"8-bit scores have no gradient: detach {name}, or use token_logprobs")
 
 
+def _aligned16(t):
+    """A vector as the kernels' entry point takes it: a slice of a vocabulary may begin anywhere (its rows of
+    the weight are 16-byte aligned in any case)."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
                         logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
                         return_entropy: bool = False):
@@ -222,6 +228,7 @@ def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hid
     dev = hidden.device
     with on_device(dev):
         ws_bytes = flce_logprobs_int8_workspace_size(p)
+        weight_scale, bias = _aligned16(weight_scale), _aligned16(bias)
         if hidden_scale is None:
             hidden, hidden_scale = _quantize(hidden)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
