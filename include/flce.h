@@ -391,8 +391,9 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
 int flce_quantize_int8(int dtype, const void* x, int64_t rows, int64_t cols, void* q, float* scale, void* stream);
 
 /* Bytes of device workspace flce_logprobs_int8 needs.  Host only.  params as for
- * flce_logprobs_forward, with hidden % 16 == 0 and at most 2^17; params->dtype
- * (any valid one) and the gradient fields are not used. */
+ * flce_logprobs_forward, with hidden % 16 == 0 and at most 2^17, N*H below 2^30 and
+ * N at most 2^22 - 256; params->dtype (any valid one) and the gradient fields are not
+ * used. */
 int flce_logprobs_int8_workspace_size(const flce_params* p, size_t* bytes);
 
 /* hidden (N, H) and weight (V, H): device int8 within [-127, 127]; hidden_scale

@@ -534,6 +534,14 @@ static bool targets_aligned(const Plan& pl, const void* t) {   // read one at a 
 // The log-probability entry points take the loss's parameters, of which the
 // reduction and the z-loss have no meaning there.
 static int logprobs_plan(const flce_params* p, bool int8, Plan* pl, LpPlan* lp) {
+  flce_params q;
+  if (p && int8) {   // no backward: neither its chunk nor the type it would have limits the sizes
+    if (!valid_dtype(p->dtype)) return FLCE_ERR_INVALID_ARG;
+    q = *p;
+    q.dtype = q.grad_weight_dtype = FLCE_BF16;
+    q.vocab_chunk = 256;
+    p = &q;
+  }
   const int rc = make_plan(p, pl);
   if (rc != FLCE_OK) return rc;
   if (pl->reduction != FLCE_REDUCTION_NONE || pl->z_loss != 0.0f) return FLCE_ERR_INVALID_ARG;
