@@ -276,13 +276,13 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
   // exponent's constant term (or -LSE log2e without the cap).
   // ENTROPY: from the products on as lp_tiles_kernel and lp_small_kernel, in base 2 (another
   // rounding of the scale would be off by 6e-8 of the logit in every p), and with the cap in
-  // fp32 in tanh(v / cap).
-  constexpr bool kTanh = ENTROPY && SOFTCAP && sizeof(T) == 4, kBase2 = ENTROPY && !SOFTCAP;
+  // tanh(v / cap) and its slope.
+  constexpr bool kTanh = ENTROPY && SOFTCAP, kBase2 = ENTROPY && !SOFTCAP;
   const float s2 = kTanh ? a.scale / a.cap
                  : kBase2 ? a.scale * kLog2e
                           : (SOFTCAP ? a.scale * a.two_log2e_over_cap : a.scale);   // scale folded into the exp argument
   const float k1 = -a.two_cap * kLog2e;
-  const float cmul = (SOFTCAP ? 4.0f * a.scale : a.scale) * a.dscale[0];
+  const float cmul = (SOFTCAP && !kTanh ? 4.0f * a.scale : a.scale) * a.dscale[0];
   float cAs[kNI], cBs[kNI], cEs[kNI], k0[kNI];
   int rel[kNI];
 #pragma unroll
@@ -314,30 +314,35 @@ __global__ __launch_bounds__(kThreads, 1) void bwd_dlogits_kernel(DlogitsArgs a)
     for (int r = 0; r < 4; r++) cs[mi][r] = 0.0f;
 #pragma unroll
     for (int ni = 0; ni < kNI; ni++) {
-      float f[4], d[4];   // f: softcap' / 4 with the cap, else unused
+      float f[4], d[4];   // f: softcap' with the cap (without ENTROPY a quarter of it), else unused
+      if constexpr (kTanh) {
+        float u[4], th[4];
 #pragma unroll
-      for (int r = 0; r < 4; r++) {
-        float v = HAS_BIAS ? fmaf(acc[mi][ni][r], s2, sb[r]) : acc[mi][ni][r] * s2;
-        if constexpr (ENTROPY && SOFTCAP) v = fmaxf(v, kMasked);
-        if constexpr (kTanh) {
-          float slope;
-          const float x = fmaf(a.cap * kLog2e, tanh_of<true>(v, &slope), k0[ni]);
-          f[r] = 0.25f * slope;
+        for (int r = 0; r < 4; r++)
+          u[r] = fmaxf(HAS_BIAS ? fmaf(acc[mi][ni][r], s2, sb[r]) : acc[mi][ni][r] * s2, kMasked);
+        tanh4(u, th, f);
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const float x = fmaf(a.cap * kLog2e, th[r], k0[ni]);
           d[r] = (fast_exp2(x) * fmaf(x, cEs[ni], cAs[ni])) * f[r];
-        } else if constexpr (SOFTCAP) {
-          const float rr = fast_rcp(fast_exp2(v) + 1.0f);
-          const float x = fmaf(rr, k1, k0[ni]);   // log2 p
-          const float p = fast_exp2(x);
-          f[r] = fmaf(-rr, rr, rr);
-          if constexpr (ENTROPY) d[r] = (p * fmaf(x, cEs[ni], cAs[ni])) * f[r];
-          else d[r] = (p * cAs[ni]) * f[r];
-        } else {
-          const float x = kBase2 ? v + k0[ni] : fmaf(v, kLog2e, k0[ni]);
-          if constexpr (ENTROPY) {
-            const float xf = fmaxf(x, kMasked);
-            d[r] = fast_exp2(xf) * fmaf(xf, cEs[ni], cAs[ni]);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const float v = HAS_BIAS ? fmaf(acc[mi][ni][r], s2, sb[r]) : acc[mi][ni][r] * s2;
+          if constexpr (SOFTCAP) {
+            const float rr = fast_rcp(fast_exp2(v) + 1.0f);
+            const float p = fast_exp2(fmaf(rr, k1, k0[ni]));
+            f[r] = fmaf(-rr, rr, rr);
+            d[r] = (p * cAs[ni]) * f[r];
           } else {
-            d[r] = fast_exp2(x) * cAs[ni];
+            const float x = kBase2 ? v + k0[ni] : fmaf(v, kLog2e, k0[ni]);
+            if constexpr (ENTROPY) {
+              const float xf = fmaxf(x, kMasked);
+              d[r] = fast_exp2(xf) * fmaf(xf, cEs[ni], cAs[ni]);
+            } else {
+              d[r] = fast_exp2(x) * cAs[ni];
+            }
           }
         }
       }

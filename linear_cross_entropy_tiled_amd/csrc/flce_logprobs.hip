@@ -96,17 +96,11 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   static __shared__ __attribute__((aligned(16))) char bias_lds[2][256 * BE], wscale_lds[2][I8 ? 1024 : 16];
 
   // the accumulator times s_u is u = y, or with the cap u = v / cap, y = cap log2(e) tanh(u).
-  // Of narrower types u = 2 v log2(e) / cap and y = cap log2(e) (1 - 2 / (2^u + 1)): three
-  // operations fewer, off by 1e-7 of the cap, far below the inputs' own rounding.  (N = 8192,
-  // H = 4096, V = 32768 with the cap: bf16 1558 us, with tanh_of 1582 to 1630; 8-bit 836,
-  // 858 to 914.)
-  constexpr bool kExact = E == 4;
-  const float s_u = !SOFTCAP ? a.scale * kLog2e : kExact ? a.scale / a.cap : a.scale * (2.0f * kLog2e / a.cap);
+  // (N = 8192, H = 4096, V = 32768, cap 30: bf16 1570 us with all logits below 24, 1618 with most
+  // above; 8-bit 887, 940.  1 - 2 / (e^2u + 1) for all, off by 1e-7 of the cap: 1548, 865.)
+  const float s_u = SOFTCAP ? a.scale / a.cap : a.scale * kLog2e;
   const float cap2 = a.cap * kLog2e;
-  auto capped = [&](float u, float minus) {
-    if constexpr (kExact) return fmaf(cap2, tanh_of<true>(u), -minus);
-    else return fmaf(fast_rcp(fast_exp2(u) + 1.0f), -2.0f * cap2, cap2 - minus);
-  };
+  auto capped = [&](float u) { return cap2 * tanh_of<true>(u); };
 
   Acc acc[kMI][kNI];
   for (int vt = vt_begin; vt < vt_end; ++vt) {
@@ -174,7 +168,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
       }
       // a block without a finite logit keeps kMasked, with the cap one without a row (there a
       // logit of -inf is -cap)
-      const float mx = SOFTCAP && lim > 0 ? capped(mu, 0.0f) : mu;
+      const float mx = SOFTCAP && lim > 0 ? capped(mu) : mu;
       const int rel = tile_tgt[wn * kWaveN + acc_col(ni, lane)] - vw;
       const bool hit = rel >= 0 && rel < kWaveM && ((rel >> 2) & 3) == (lane >> 4);
       if (__builtin_amdgcn_ballot_w64(hit)) {
@@ -185,7 +179,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
 #pragma unroll
           for (int r = 0; r < 4; r++)
             if (16 * mi + r == rel_l) ut = acc[mi][ni][r];
-        if (hit) st_yt[wave][ni][lane] = SOFTCAP ? capped(ut, 0.0f) : ut;
+        if (hit) st_yt[wave][ni][lane] = SOFTCAP ? capped(ut) : ut;
       }
       const float m_old = st_m[ni];
       const float m_new = fmaxf(m_old, mx);
@@ -194,10 +188,13 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
       float se0 = 0.f, se1 = 0.f, sx0 = 0.f, sx1 = 0.f;
 #pragma unroll
       for (int mi = 0; mi < kMI; mi++) {
+        float u[4], th[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++) u[r] = acc[mi][ni][r];
+        if constexpr (SOFTCAP) tanh4(u, th);
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          const float u = acc[mi][ni][r];
-          float x = SOFTCAP ? capped(u, m_new) : u - m_new;
+          float x = SOFTCAP ? fmaf(cap2, th[r], -m_new) : u[r] - m_new;
           if (ragged && 16 * mi + r >= lim) x = kMasked;
           const float e = fast_exp2(x);
           // a logit of -inf (there is none with the cap, nor of 8-bit products without a

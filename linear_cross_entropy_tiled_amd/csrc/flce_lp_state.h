@@ -23,9 +23,11 @@ __device__ __forceinline__ void lp_merge(LpState& a, const LpState& b) {
 }
 
 // tanh(w), for the softcap z = cap tanh(v / cap).  Up to |w| = 0.8 (logits up to two
-// thirds of the cap) w + w^3 p(w^2), p of degree 6 fitted to a relative error of 2e-10:
-// 1 - 2 / (e^2w + 1) is off by 1e-7 of 1 there, and the logit by 1e-7 of the cap, however
-// small it is.  Its eight multiply-adds cost what the exponential and the reciprocal do.
+// thirds of the cap) w + w^3 p(w^2), p of degree 6: with its coefficients rounded to fp32
+// 7.5e-9 off tanh, as evaluated in fp32 about 1e-7 of it.  1 - 2 / (e^2w + 1) is off by 1e-7
+// of 1 there, and the logit by 1e-7 of the cap, however small it is (at a cap of 1000 the
+// log-probabilities of 1000 x 32000 were 7e-6 off, 15 to 80 times elementary torch's error).
+// The eight multiply-adds cost what the exponential and the reciprocal do.
 // WIDE, for a wave that holds a larger w somewhere: the formula for those and only those,
 // so that no value depends on its neighbours.
 constexpr float kTanhNear = 0.8f;
@@ -56,6 +58,32 @@ template <bool WIDE> __device__ __forceinline__ float tanh_of(float w, float* sl
     *slope = 4.0f * fmaf(-r, r, r);
   }
   return th;
+}
+
+// Four at a time, the formula only where some lane of the wave needs it.
+__device__ __forceinline__ void tanh4(const float (&w)[4], float (&th)[4]) {
+  float size = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; r++) {
+    th[r] = tanh_of<false>(w[r]);
+    size = fmaxf(size, fabsf(w[r]));
+  }
+  if (__builtin_amdgcn_ballot_w64(size > kTanhNear)) {
+#pragma unroll
+    for (int r = 0; r < 4; r++) th[r] = tanh_of<true>(w[r]);
+  }
+}
+__device__ __forceinline__ void tanh4(const float (&w)[4], float (&th)[4], float (&slope)[4]) {
+  float size = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; r++) {
+    th[r] = tanh_of<false>(w[r], &slope[r]);
+    size = fmaxf(size, fabsf(w[r]));
+  }
+  if (__builtin_amdgcn_ballot_w64(size > kTanhNear)) {
+#pragma unroll
+    for (int r = 0; r < 4; r++) th[r] = tanh_of<true>(w[r], &slope[r]);
+  }
 }
 
 template <typename T> struct BiasOf { typedef T type; };
