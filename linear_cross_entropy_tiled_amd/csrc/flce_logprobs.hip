@@ -407,14 +407,19 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
   }
 }
 
+template <typename T>
+static void launch_quantize_t(const void* x, int64_t rows, int64_t cols, int8_t* q, float* scale, hipStream_t st) {
+  constexpr int64_t kMost = int64_t(1) << 22;   // a launch of 2^32 threads or more leaves workgroups out
+  for (int64_t r = 0; r < rows; r += kMost)
+    quantize_rows_kernel<T><<<(unsigned)(rows - r < kMost ? rows - r : kMost), 256, 0, st>>>(
+        static_cast<const T*>(x) + r * cols, cols, q + r * cols, scale + r);
+}
+
 hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
                            hipStream_t st) {
-  if (rows > 0) {
-    const unsigned g = (unsigned)rows;
-    if (dtype == FLCE_BF16) quantize_rows_kernel<bf16><<<g, 256, 0, st>>>(static_cast<const bf16*>(x), cols, q, scale);
-    else if (dtype == FLCE_F16) quantize_rows_kernel<f16><<<g, 256, 0, st>>>(static_cast<const f16*>(x), cols, q, scale);
-    else quantize_rows_kernel<float><<<g, 256, 0, st>>>(static_cast<const float*>(x), cols, q, scale);
-  }
+  if (dtype == FLCE_BF16) launch_quantize_t<bf16>(x, rows, cols, q, scale, st);
+  else if (dtype == FLCE_F16) launch_quantize_t<f16>(x, rows, cols, q, scale, st);
+  else launch_quantize_t<float>(x, rows, cols, q, scale, st);
   return hipGetLastError();
 }
 

@@ -69,3 +69,25 @@ def test_long_hidden_states_and_a_long_vocabulary(flce_lib, n):
     want = l.gather(1, t[:, None])[:, 0]
     assert ((lp.double() - want).abs() <= 2 * ez + own).all()
     assert ((ent.double() + (l.exp() * l).sum(1)).abs() <= spread * ez + 2 * own).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [(1 << 22) + 1, (1 << 24) + 3])
+def test_quantize_many_rows(flce_lib, rows):
+    """More rows than one launch has workgroups for."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, 16, generator=g, device="cuda", dtype=torch.bfloat16)
+    x[-1, 3], x[5] = float("nan"), 0.0
+    q, scale = flce_lib.quantize_int8(x)
+    for at in range(0, rows, 1 << 21):       # the definition, in fp32
+        v = x[at:at + (1 << 21)].float()
+        top = v.abs().amax(1)
+        s = top * torch.tensor(1.0 / 127.0, device="cuda")
+        live = top >= 1e-30                  # NaN is not
+        r = torch.where(live, 1.0 / s, 0.0)
+        want = torch.where(live[:, None], torch.round(v * r[:, None]), 0.0).to(torch.int8)
+        assert torch.equal(q[at:at + (1 << 21)], want)
+        got = scale[at:at + (1 << 21)]
+        assert torch.equal(torch.isnan(got), torch.isnan(top))
+        assert torch.equal(torch.nan_to_num(got), torch.where(live, s, 0.0))
