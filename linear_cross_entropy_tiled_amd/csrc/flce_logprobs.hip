@@ -495,9 +495,12 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
 //   d / d z_j = g [j = t] - p_j (g + h (H + log p_j))
 //             = coefA p_j + coefE p_j log2 p_j - coefB [j = t],
 // coefA = -(g + h H), coefE = -h ln 2, coefB = -g.  The kernels subtract the LSE in base 2,
-// L, as one fp32 number: its rounding (1e-6 at 16 to 32, which every p of the row would carry)
-// is taken back by the constants: with L = Lf + d and p = 2^-d p',
+// L, as one fp32 number.  The saved LSE is in nats; the rounding of its conversion to base 2
+// (1e-6 at 16 to 32, which every p of the row would carry) is taken back by the constants:
+// with L = Lf + d and p = 2^-d p',
 //   coefA p + coefE p log2 p = p' (2^-d (coefA - d coefE) + 2^-d coefE log2 p').
+// What stays in every p of a row are the forward's own roundings, of m + log2 l and of its
+// product with ln 2.
 struct LpPrepArgs {
   const void* targets;
   int tgt_i32;
@@ -534,7 +537,7 @@ __global__ __launch_bounds__(1024) void lp_prep_kernel(LpPrepArgs a) {
       const bool in_range = t >= 0 && t < a.V;
       bad |= (t != a.ignore_index && !in_range) ? 1 : 0;
       if (t != a.ignore_index && in_range) {
-        const double exact = (double)a.lse[i] / (double)kLn2;   // as lp_rows_kernel took it times kLn2
+        const double exact = (double)a.lse[i] / (double)kLn2;   // the constant that lp_rows_kernel multiplied by
         ll = (float)exact;
         const float d = fabsf(ll) < INFINITY ? (float)(exact - (double)ll) : 0.0f;
         const float g = a.grad_logps ? a.grad_logps[i] : 0.0f;

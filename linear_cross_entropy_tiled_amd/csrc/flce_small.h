@@ -4,9 +4,10 @@
 //
 // Operands, fragments and accumulator layout are those of the large loop (stages of
 // 128 bytes of K per row, K-major or M/N-major); n stage buffers keep n - 1 stages of
-// loads in flight under one barrier a stage, and several workgroups share a CU.  A 64 x 64 tile reads its fragments twice as often per matrix operation as the
-// large tile, which costs the 16-bit types about half their rate and fp32, whose
-// matrix instructions take 16 times as long per byte, nothing.
+// loads in flight under one barrier a stage, and several workgroups share a CU.  A 64 x 64
+// tile reads its fragments twice as often per matrix operation as the large tile, which
+// costs the 16-bit types about half their rate and fp32, whose matrix instructions take
+// 16 times as long per byte, nothing.
 #pragma once
 
 #include "flce_device.h"
@@ -17,9 +18,11 @@ namespace small {
 constexpr int kBMs = 64;
 constexpr int kThreadsS = 256;
 constexpr int kStageA = kBMs * kBKB;                             // 8 KiB
-// Stage buffers: three, so that three workgroups (BN 64, 48 KiB) or five (BN 16) share a
-// CU; two for fp32 at BN 64, whose stage takes 1024 cycles of matrix instructions, and
-// where a fourth workgroup is worth 5%.
+// Stage buffers: three at BN 64 (48 KiB), so that three workgroups share a CU; two for
+// fp32 there, whose stage takes 1024 cycles of matrix instructions, and where a fourth
+// workgroup is worth 5%.  Four at BN 16 (40 KiB, 42 with the sides), three workgroups as
+// well: 4 tokens at V = 128256 in 8 bits took 114 us, with three buffers 136, with five
+// within 2% of four.
 template <typename T> constexpr int stages(int bn) { return bn == 16 ? 4 : (sizeof(T) == 4 ? 2 : 3); }
 constexpr int stage_bytes(int bn) { return (kBMs + bn) * kBKB; }
 template <typename T> constexpr int lds_bytes(int bn) { return stages<T>(bn) * stage_bytes(bn); }

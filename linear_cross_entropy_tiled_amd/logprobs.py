@@ -125,7 +125,7 @@ def token_logprobs(hidden, weight, targets, bias=None, *, logit_scale: float = 1
     in fp32, without the (N, V) logits; with ``return_entropy`` also each row's entropy (nats).
 
     Both are differentiable in hidden, weight and bias (the backward recomputes the logit tiles).
-    Rows whose target is ``ignore_index`` give 0 and take no gradient.  ``vocab_chunk``: as in
+    Rows whose target is ``ignore_index``, or no row of weight, give 0 and take no gradient.  ``vocab_chunk``: as in
     ``backward``.  hidden, weight and bias share one dtype (fp32, bf16, fp16)."""
     dt = _validate(hidden, weight, targets, bias, reduction="none")
     p = make_params(hidden.shape[0], hidden.shape[1], weight.shape[0], dtype=dt, logit_scale=logit_scale,
