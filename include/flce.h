@@ -538,6 +538,44 @@ int flce_policy_backward(const flce_policy_params* p, const float* grad_loss, co
                          const float* weights, flce_token_view mask, const void* offsets, void* grad_logps,
                          void* grad_entropy, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer norm of rows (the norm that makes hidden, and takes grad_hidden), forward
+ * and backward:
+ *   mean = sum_j x_j / cols,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / cols + eps),
+ *   y_j = weight_j (x_j - mean) rstd + bias_j.
+ * Everything is formed in fp32 and rounded once.  Pointers need the alignment of
+ * their element only (the workspace 16 bytes); 16-byte aligned rows run faster.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int64_t rows;               /* >= 0, at most 2^31                                      */
+  int64_t cols;               /* >= 1, at most 2^20                                      */
+  int64_t ld_x;               /* elements between rows of x, >= cols; 0 = cols           */
+  int64_t ld_grad;            /* the same of grad_y (backward); 0 = cols                 */
+  int32_t dtype;              /* flce_dtype of x, y, grad_y and grad_x                   */
+  int32_t param_dtype;        /* flce_dtype of weight, bias and their gradients: dtype,
+                                 or fp32                                                 */
+  float eps;                  /* >= 0, finite                                            */
+  int32_t reserved;           /* must be 0                                               */
+} flce_norm_params;
+
+/* Bytes of device workspace flce_layer_norm_backward needs.  Host only. */
+int flce_layer_norm_workspace_size(const flce_norm_params* p, size_t* bytes);
+
+/*
+ *  weight, bias: device (cols), or NULL for ones and zeros.
+ *  y:            device (rows, cols), contiguous.
+ *  mean, rstd:   device fp32 (rows), for the backward, or both NULL.
+ */
+int flce_layer_norm_forward(const flce_norm_params* p, const void* x, const void* weight, const void* bias, void* y,
+                            float* mean, float* rstd, void* stream);
+
+/* grad_x (rows, cols, contiguous), grad_weight and grad_bias (cols): each may be NULL where it is not
+ * wanted, which saves its work; the workspace may be NULL without the last two.  Without rows grad_weight
+ * and grad_bias are 0.  The rows are summed in fixed ranges: results are bitwise reproducible. */
+int flce_layer_norm_backward(const flce_norm_params* p, const void* x, const void* weight, const float* mean,
+                             const float* rstd, const void* grad_y, void* grad_x, void* grad_weight, void* grad_bias,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Library version, major*10000 + minor*100 + patch. */
 int flce_version(void);
 

@@ -14,6 +14,8 @@ declared in ``include/flce.h``).  This module only marshals arguments:
 * ``token_logprobs`` (``logprobs.py``) is a torch op for per-token log-probabilities
   and entropies of the head (``flce_logprobs_*``), ``token_logprobs_int8`` their form
   for a frozen 8-bit head, whose weight ``quantize_int8`` makes;
+* ``layer_norm`` (``norm.py``) is a torch op for the norm in front of the head
+  (``flce_layer_norm_*``);
 * ``preference_loss`` / ``policy_loss`` (``alignment.py``) are torch ops over
   per-token log-probabilities (``flce_preference_*``, ``flce_policy_*``).
 
@@ -57,7 +59,8 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_get_st
             "flce_preference_backward", "flce_policy_workspace_size", "flce_policy_forward",
             "flce_policy_backward", "flce_logprobs_workspace_size", "flce_logprobs_forward",
             "flce_logprobs_backward", "flce_quantize_int8", "flce_logprobs_int8_workspace_size",
-            "flce_logprobs_int8")
+            "flce_logprobs_int8", "flce_layer_norm_workspace_size", "flce_layer_norm_forward",
+            "flce_layer_norm_backward")
 
 FLCE_KERNEL_FORWARD_TILES = 1
 FLCE_KERNEL_DLOGITS = 2
@@ -153,6 +156,19 @@ class flce_policy_params(ctypes.Structure):
     ]
 
 
+class flce_norm_params(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_grad", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 # int fn(void* user, int64 row0, int64 rows, int64 vocab, void* logits, int64 ld, int32 dtype,
 #        float* loss, void* stream)
 CHUNK_LOSS_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
@@ -245,6 +261,13 @@ def load(path: Optional[str] = None):
     lib.flce_policy_forward.restype = ctypes.c_int
     lib.flce_policy_backward.argtypes = [LP, vp, vp, vp, view, vp, vp, vp, vp]
     lib.flce_policy_backward.restype = ctypes.c_int
+    NP = ctypes.POINTER(flce_norm_params)
+    lib.flce_layer_norm_workspace_size.argtypes = [NP, ctypes.POINTER(sz)]
+    lib.flce_layer_norm_workspace_size.restype = ctypes.c_int
+    lib.flce_layer_norm_forward.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp]
+    lib.flce_layer_norm_forward.restype = ctypes.c_int
+    lib.flce_layer_norm_backward.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_layer_norm_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -437,6 +460,24 @@ def flce_policy_backward(params, grad_loss, unit_grad, weights, mask, offsets, g
                          stream) -> int:
     return load().flce_policy_backward(ctypes.byref(params), grad_loss, unit_grad, weights, mask, offsets, grad_logps,
                                        grad_entropy, stream)
+
+
+def flce_layer_norm_workspace_size(params: flce_norm_params) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_layer_norm_workspace_size(ctypes.byref(params), ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_layer_norm_workspace_size")
+    return out.value
+
+
+def flce_layer_norm_forward(params, x, weight, bias, y, mean, rstd, stream) -> int:
+    return load().flce_layer_norm_forward(ctypes.byref(params), x, weight, bias, y, mean, rstd, stream)
+
+
+def flce_layer_norm_backward(params, x, weight, mean, rstd, grad_y, grad_x, grad_weight, grad_bias, workspace,
+                             workspace_bytes, stream) -> int:
+    return load().flce_layer_norm_backward(ctypes.byref(params), x, weight, mean, rstd, grad_y, grad_x, grad_weight,
+                                           grad_bias, workspace, workspace_bytes, stream)
 
 
 def flce_get_status(workspace, stream) -> int:
@@ -900,3 +941,8 @@ def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_ro
 
 from .logprobs import quantize_int8, token_logprobs, token_logprobs_int8  # noqa: E402,F401
 from .alignment import policy_loss, preference_loss  # noqa: E402,F401
+
+
+# ----------------------------------------------------------------------------- the ends of a model
+
+from .norm import layer_norm  # noqa: E402,F401

@@ -1,0 +1,21 @@
+"""fp64 definitions of the operators at the ends of a model.  TEST INFRASTRUCTURE ONLY."""
+import numpy as np
+
+
+def layer_norm(x, weight, bias, eps):
+    """(y, xhat, rstd, mean), all fp64; weight and bias may be None."""
+    x = np.asarray(x, dtype=np.float64)
+    mean = x.mean(axis=1, keepdims=True)
+    c = x - mean
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=1, keepdims=True) + eps)
+    xhat = c * rstd
+    y = xhat if weight is None else xhat * weight
+    return (y if bias is None else y + bias), xhat, rstd, mean
+
+
+def layer_norm_grads(x, weight, eps, dy):
+    """(dx, dweight, dbias), fp64."""
+    _, xhat, rstd, _ = layer_norm(x, None, None, eps)
+    d = dy if weight is None else dy * weight
+    dx = rstd * (d - d.mean(axis=1, keepdims=True) - xhat * (d * xhat).mean(axis=1, keepdims=True))
+    return dx, (dy * xhat).sum(axis=0), dy.sum(axis=0)
