@@ -539,6 +539,39 @@ int flce_policy_backward(const flce_policy_params* p, const float* grad_loss, co
                          void* grad_entropy, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Token embedding (of a model whose head's weight is its embedding, or of its own):
+ *   out_i = scale weight_{id_i},     grad_weight_v = scale sum_{i: id_i = v} grad_out_i.
+ * A token whose id is ignore_index, or no row of weight, gives 0 and takes no
+ * gradient, whatever its row of grad_out holds.  Pointers need the alignment of
+ * their element only (the workspace 16 bytes); rows of whole, 16-byte aligned
+ * pieces run faster.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int64_t n_tokens;           /* >= 0, below 2^31                                        */
+  int64_t hidden;             /* >= 1, at most 2^20                                      */
+  int64_t vocab;              /* >= 1, below 2^31                                        */
+  int64_t ignore_index;
+  int32_t dtype;              /* flce_dtype of weight, out and grad_out                  */
+  int32_t grad_weight_dtype;  /* flce_dtype of grad_weight; summed in fp32 always        */
+  int32_t flags;              /* FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32 (ids)    */
+  float scale;                /* finite                                                  */
+} flce_embedding_params;
+
+/* Bytes of device workspace flce_embedding_backward needs.  Host only. */
+int flce_embedding_workspace_size(const flce_embedding_params* p, size_t* bytes);
+
+/* ids: device (n_tokens); weight: device (vocab, hidden); out: device (n_tokens, hidden). */
+int flce_embedding_forward(const flce_embedding_params* p, const void* ids, const void* weight, void* out,
+                           void* stream);
+
+/* grad_weight (vocab, hidden): every row is written, or with FLCE_ACCUMULATE_GRAD_WEIGHT the rows that occur
+ * are added to (in fp32, rounded once) and the others left as they are: the buffer may be the one that
+ * flce_backward's grad_weight of a tied head went to.  A row's tokens are summed in their order, in fixed
+ * pieces: results are bitwise reproducible. */
+int flce_embedding_backward(const flce_embedding_params* p, const void* ids, const void* grad_out, void* grad_weight,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Layer norm of rows (the norm that makes hidden, and takes grad_hidden), forward
  * and backward:
  *   mean = sum_j x_j / cols,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / cols + eps),

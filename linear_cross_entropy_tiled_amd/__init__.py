@@ -14,6 +14,9 @@ declared in ``include/flce.h``).  This module only marshals arguments:
 * ``token_logprobs`` (``logprobs.py``) is a torch op for per-token log-probabilities
   and entropies of the head (``flce_logprobs_*``), ``token_logprobs_int8`` their form
   for a frozen 8-bit head, whose weight ``quantize_int8`` makes;
+* ``embedding`` (``embedding.py``) is a torch op for the token embedding,
+  ``embedding_backward`` its gradient added into a tied head's buffer
+  (``flce_embedding_*``);
 * ``layer_norm`` (``norm.py``) is a torch op for the norm in front of the head
   (``flce_layer_norm_*``);
 * ``preference_loss`` / ``policy_loss`` (``alignment.py``) are torch ops over
@@ -60,7 +63,8 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_get_st
             "flce_policy_backward", "flce_logprobs_workspace_size", "flce_logprobs_forward",
             "flce_logprobs_backward", "flce_quantize_int8", "flce_logprobs_int8_workspace_size",
             "flce_logprobs_int8", "flce_layer_norm_workspace_size", "flce_layer_norm_forward",
-            "flce_layer_norm_backward")
+            "flce_layer_norm_backward", "flce_embedding_workspace_size", "flce_embedding_forward",
+            "flce_embedding_backward")
 
 FLCE_KERNEL_FORWARD_TILES = 1
 FLCE_KERNEL_DLOGITS = 2
@@ -169,6 +173,19 @@ class flce_norm_params(ctypes.Structure):
     ]
 
 
+class flce_embedding_params(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("ignore_index", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("grad_weight_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 # int fn(void* user, int64 row0, int64 rows, int64 vocab, void* logits, int64 ld, int32 dtype,
 #        float* loss, void* stream)
 CHUNK_LOSS_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
@@ -268,6 +285,13 @@ def load(path: Optional[str] = None):
     lib.flce_layer_norm_forward.restype = ctypes.c_int
     lib.flce_layer_norm_backward.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.flce_layer_norm_backward.restype = ctypes.c_int
+    EP = ctypes.POINTER(flce_embedding_params)
+    lib.flce_embedding_workspace_size.argtypes = [EP, ctypes.POINTER(sz)]
+    lib.flce_embedding_workspace_size.restype = ctypes.c_int
+    lib.flce_embedding_forward.argtypes = [EP, vp, vp, vp, vp]
+    lib.flce_embedding_forward.restype = ctypes.c_int
+    lib.flce_embedding_backward.argtypes = [EP, vp, vp, vp, vp, sz, vp]
+    lib.flce_embedding_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -478,6 +502,23 @@ def flce_layer_norm_backward(params, x, weight, mean, rstd, grad_y, grad_x, grad
                              workspace_bytes, stream) -> int:
     return load().flce_layer_norm_backward(ctypes.byref(params), x, weight, mean, rstd, grad_y, grad_x, grad_weight,
                                            grad_bias, workspace, workspace_bytes, stream)
+
+
+def flce_embedding_workspace_size(params: flce_embedding_params) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_embedding_workspace_size(ctypes.byref(params), ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_embedding_workspace_size")
+    return out.value
+
+
+def flce_embedding_forward(params, ids, weight, out, stream) -> int:
+    return load().flce_embedding_forward(ctypes.byref(params), ids, weight, out, stream)
+
+
+def flce_embedding_backward(params, ids, grad_out, grad_weight, workspace, workspace_bytes, stream) -> int:
+    return load().flce_embedding_backward(ctypes.byref(params), ids, grad_out, grad_weight, workspace,
+                                          workspace_bytes, stream)
 
 
 def flce_get_status(workspace, stream) -> int:
@@ -945,4 +986,5 @@ from .alignment import policy_loss, preference_loss  # noqa: E402,F401
 
 # ----------------------------------------------------------------------------- the ends of a model
 
+from .embedding import embedding, embedding_backward  # noqa: E402,F401
 from .norm import layer_norm  # noqa: E402,F401

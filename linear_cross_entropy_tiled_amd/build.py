@@ -26,7 +26,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libflce.so")
 SOURCES = ["flce_api.hip", "flce_forward.hip", "flce_backward.hip", "flce_chunked.hip", "flce_fused.hip",
            "flce_noalloc.hip", "flce_logprobs.hip", "flce_small.hip",
-           "flce_align.hip", "flce_align_api.hip", "flce_norm.hip", "flce_ends_api.hip"]
+           "flce_align.hip", "flce_align_api.hip", "flce_norm.hip", "flce_embed.hip",
+           "flce_ends_api.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,0 +1,386 @@
+// Token embedding, out_i = scale weight[id_i], and its gradient
+//   grad_weight_v = scale sum over the tokens i with id_i = v of grad_i.
+//
+// The gradient sorts the tokens by their id (stable, so that a row's tokens are summed in
+// their order and results do not depend on timing), then sums each run of equal ids in
+// fp32 and rounds it once.  Runs are summed by chunks of sorted tokens, not by rows: a
+// frequent token's run of thousands is spread over many workgroups.  The part of a run
+// that reaches over a chunk's edge is left in fp32 and a second kernel adds the parts.
+#include "flce_device.h"
+#include "flce_embed.h"
+
+namespace flce {
+
+struct EmbedArgs {
+  const void* ids;
+  int ids_i32;
+  int64_t n, v, ignore_index;
+  int h;
+  float scale;
+  const void* weight;
+  void* out;
+};
+
+// The id of token i as a row of the weight, or v for a token that is none.
+__device__ __forceinline__ uint32_t row_of(const EmbedArgs& a, int64_t i) {
+  const int64_t t = load_target(a.ids, i, a.ids_i32);
+  return (uint32_t)(t != a.ignore_index && t >= 0 && t < a.v ? t : a.v);
+}
+
+// ---------------------------------------------------------------------------
+// Forward: one wave a token, VEC elements (16 bytes, or 1 where rows are not aligned) a lane
+// ---------------------------------------------------------------------------
+template <typename T, int VEC> __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedArgs a) {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  const int lane = threadIdx.x & 63;
+  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < a.n; i += (int64_t)gridDim.x * 4) {
+    const uint32_t r = row_of(a, i);
+    const T* w = static_cast<const T*>(a.weight) + (int64_t)r * a.h;
+    T* out = static_cast<T*>(a.out) + i * a.h;
+    for (int c = lane * VEC; c < a.h; c += 64 * VEC) {
+      V x;
+#pragma unroll
+      for (int j = 0; j < VEC; j++) x[j] = (T)0.0f;
+      if (r < a.v) {
+        x = *reinterpret_cast<const V*>(w + c);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) x[j] = (T)((float)x[j] * a.scale);
+      }
+      *reinterpret_cast<V*>(out + c) = x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Stable radix sort of (id, token), 8 bits a pass: counts by workgroup, an exclusive
+// scan of them in the order (digit, workgroup), then every item to its place.
+// ---------------------------------------------------------------------------
+struct SortArgs {
+  EmbedArgs e;
+  int shift, first;            // bits already sorted; first pass: keys come from the ids
+  const uint32_t* keys;
+  const uint32_t* at;
+  uint32_t* keys_out;
+  uint32_t* at_out;
+  uint32_t* hist;              // [kSortBins][blocks]
+  int blocks;
+};
+
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i) {
+  return a.first ? row_of(a.e, i) : a.keys[i];
+}
+
+__global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a) {
+  __shared__ uint32_t bins[kSortBins];
+  const int tid = threadIdx.x;
+  if (tid < kSortBins) bins[tid] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * kSortItems;
+#pragma unroll
+  for (int k = 0; k < kSortItems / 1024; k++) {
+    const int64_t i = i0 + k * 1024 + tid;
+    if (i < a.e.n) atomicAdd(&bins[(sort_key(a, i) >> a.shift) & (kSortBins - 1)], 1u);   // counts: any order
+  }
+  __syncthreads();
+  if (tid < kSortBins) a.hist[(int64_t)tid * a.blocks + blockIdx.x] = bins[tid];
+}
+
+// Exclusive scan of n counts in place, one workgroup.
+__global__ __launch_bounds__(1024) void sort_scan_kernel(uint32_t* hist, int64_t n) {
+  __shared__ uint32_t waves[16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  uint32_t before = 0;
+  for (int64_t i0 = 0; i0 < n; i0 += 1024) {
+    const uint32_t own = i0 + tid < n ? hist[i0 + tid] : 0u;
+    uint32_t x = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t y = __shfl_up(x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 63) waves[tid >> 6] = x;
+    __syncthreads();
+    uint32_t base = before, total = 0;
+#pragma unroll
+    for (int w = 0; w < 16; w++) {
+      if (w < tid >> 6) base += waves[w];
+      total += waves[w];
+    }
+    if (i0 + tid < n) hist[i0 + tid] = base + x - own;
+    before += total;
+    __syncthreads();
+  }
+}
+
+__global__ __launch_bounds__(1024) void sort_place_kernel(SortArgs a) {
+  __shared__ uint32_t bins[16][kSortBins];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int k = tid; k < 16 * kSortBins; k += 1024) bins[k / kSortBins][k % kSortBins] = 0;
+  __syncthreads();
+  // a wave's items are neighbours; within a round of 64 the lanes with the same digit find
+  // each other by ballots, and the first of them counts for all
+  constexpr int kRounds = kSortItems / 1024;
+  const int64_t i0 = (int64_t)blockIdx.x * kSortItems + wave * (kSortItems / 16);
+  uint32_t key[kRounds], at[kRounds], rank[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; k++) {
+    const int64_t i = i0 + k * 64 + lane;
+    const bool here = i < a.e.n;
+    key[k] = here ? sort_key(a, i) : 0u;
+    at[k] = here && !a.first ? a.at[i] : (uint32_t)i;
+    const uint32_t digit = (key[k] >> a.shift) & (kSortBins - 1);
+    uint64_t same = __ballot(here);
+#pragma unroll
+    for (int b = 0; b < kSortBits; b++) {
+      const bool bit = (digit >> b) & 1;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    const uint64_t below = same & ((uint64_t(1) << lane) - 1);
+    rank[k] = here ? bins[wave][digit] + (uint32_t)__popcll(below) : 0u;
+    wave_lds_sync();
+    if (here && below == 0) bins[wave][digit] += (uint32_t)__popcll(same);
+    wave_lds_sync();
+  }
+  __syncthreads();
+  if (tid < kSortBins) {
+    uint32_t s = a.hist[(int64_t)tid * a.blocks + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < 16; w++) {
+      const uint32_t c = bins[w][tid];
+      bins[w][tid] = s;
+      s += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kRounds; k++) {
+    if (i0 + k * 64 + lane >= a.e.n) continue;
+    const uint32_t to = bins[wave][(key[k] >> a.shift) & (kSortBins - 1)] + rank[k];
+    a.keys_out[to] = key[k];
+    a.at_out[to] = at[k];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of runs
+// ---------------------------------------------------------------------------
+struct RunArgs {
+  const uint32_t* keys;        // sorted; tokens without a row last
+  const uint32_t* at;
+  int64_t n, v;
+  int h, chunk;
+  int64_t n_chunks;
+  float scale;
+  int accumulate;
+  const void* grad;
+  void* gw;
+  float* part;                 // [2][n_chunks][h]: what a chunk's first run adds to one begun before it, and its
+                               // last run's sum where that goes on
+};
+
+template <typename O, int VEC> __global__ __launch_bounds__(256) void embed_zero_kernel(O* gw, int64_t n) {
+  typedef O V __attribute__((ext_vector_type(VEC)));
+  const int64_t whole = n / VEC;
+  V z;
+#pragma unroll
+  for (int j = 0; j < VEC; j++) z[j] = (O)0.0f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < whole; i += (int64_t)gridDim.x * 256)
+    reinterpret_cast<V*>(gw)[i] = z;
+  if (blockIdx.x == 0 && threadIdx.x < n - whole * VEC) gw[whole * VEC + threadIdx.x] = (O)0.0f;
+}
+
+template <typename O, int VEC>
+__device__ __forceinline__ void put_row(const RunArgs& a, uint32_t row, int c, const float (&s)[VEC]) {
+  typedef O V __attribute__((ext_vector_type(VEC)));
+  V* to = reinterpret_cast<V*>(static_cast<O*>(a.gw) + (int64_t)row * a.h + c);
+  V o;
+  if (a.accumulate) {
+    o = *to;
+#pragma unroll
+    for (int j = 0; j < VEC; j++) o[j] = (O)fmaf(s[j], a.scale, (float)o[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; j++) o[j] = (O)(s[j] * a.scale);
+  }
+  *to = o;
+}
+
+// One chunk of sorted tokens by 256 VEC columns.
+template <typename T, typename O, int VEC> __global__ __launch_bounds__(256) void embed_runs_kernel(RunArgs a) {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  const int64_t chunk = blockIdx.x, i0 = chunk * a.chunk, i1 = min(i0 + a.chunk, a.n);
+  const int c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * VEC;
+  if (c >= a.h) return;
+  float s[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) s[j] = 0.0f;
+  uint32_t key = a.keys[i0];
+  bool inner = i0 == 0 || a.keys[i0 - 1] != key;   // the run began here
+  for (int64_t i = i0; i < i1; i++) {
+    if (key >= a.v) return;
+    const V g = *reinterpret_cast<const V*>(static_cast<const T*>(a.grad) + (int64_t)a.at[i] * a.h + c);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) s[j] += (float)g[j];
+    const uint32_t next = i + 1 < a.n ? a.keys[i + 1] : (uint32_t)a.v;
+    if (next == key && i + 1 < i1) continue;
+    if (inner && next != key) {
+      put_row<O, VEC>(a, key, c, s);
+    } else {
+      float* p = a.part + ((inner ? a.n_chunks : 0) + chunk) * a.h + c;
+#pragma unroll
+      for (int j = 0; j < VEC; j++) p[j] = s[j];
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; j++) s[j] = 0.0f;
+    key = next;
+    inner = true;
+  }
+}
+
+// Runs that begin in a chunk and end in another.
+template <typename O> __global__ __launch_bounds__(256) void embed_join_kernel(RunArgs a) {
+  const int64_t chunk = blockIdx.x, i0 = chunk * a.chunk, i1 = i0 + a.chunk;
+  if (i1 >= a.n) return;
+  const uint32_t key = a.keys[i1 - 1];
+  if (key >= a.v || a.keys[i1] != key) return;
+  if (i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key) return;   // begun before
+  const int c = (int)blockIdx.y * 256 + (int)threadIdx.x;
+  if (c >= a.h) return;
+  float s[1] = {a.part[(a.n_chunks + chunk) * a.h + c]};
+  for (int64_t k = chunk + 1; k < a.n_chunks; k++) {
+    s[0] += a.part[k * a.h + c];
+    if ((k + 1) * a.chunk >= a.n || a.keys[(k + 1) * a.chunk] != key) break;
+  }
+  put_row<O, 1>(a, key, c, s);
+}
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+void plan_embedding_backward(EmbedPlan* p) {
+  int bits = 1;
+  while ((p->v >> bits) != 0) bits++;      // of the key v
+  p->passes = (bits + kSortBits - 1) / kSortBits;
+  p->sort_blocks = (int)((p->n + kSortItems - 1) / kSortItems);
+  p->chunk = 32;
+  while (p->chunk < (1 << 20) && p->n / p->chunk > 4096) p->chunk *= 2;
+  p->n_chunks = (p->n + p->chunk - 1) / p->chunk;
+  size_t o = 0;
+  for (int k = 0; k < 2; k++) {
+    p->w_keys[k] = o;
+    o += up256(size_t(p->n) * 4);
+    p->w_at[k] = o;
+    o += up256(size_t(p->n) * 4);
+  }
+  p->w_hist = o;
+  o += up256(size_t(kSortBins) * p->sort_blocks * 4);
+  p->w_part = o;
+  o += up256(size_t(2) * p->n_chunks * p->h * 4);
+  p->w_bytes = o > 0 ? o : 256;
+}
+
+static size_t bytes_of(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
+static bool whole16(const void* p, int64_t h, int dtype) {   // rows of whole, aligned 16-byte pieces
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (h * bytes_of(dtype)) % 16 == 0;
+}
+
+static EmbedArgs embed_args(const EmbedPlan& p, const void* ids) {
+  EmbedArgs a{};
+  a.ids = ids;
+  a.ids_i32 = p.ids_i32 ? 1 : 0;
+  a.n = p.n;
+  a.v = p.v;
+  a.ignore_index = p.ignore_index;
+  a.h = p.h;
+  a.scale = p.scale;
+  return a;
+}
+
+template <typename T> static void embed_forward_t(const EmbedPlan& p, const EmbedArgs& a, hipStream_t st) {
+  const int64_t need = (p.n + 3) / 4;
+  const unsigned wgs = (unsigned)(need < 65536 ? need : 65536);
+  if (whole16(a.weight, p.h, p.dtype) && whole16(a.out, p.h, p.dtype))
+    embed_fwd_kernel<T, 16 / sizeof(T)><<<wgs, 256, 0, st>>>(a);
+  else
+    embed_fwd_kernel<T, 1><<<wgs, 256, 0, st>>>(a);
+}
+
+hipError_t launch_embedding_forward(const EmbedPlan& p, const void* ids, const void* weight, void* out, hipStream_t st) {
+  if (p.n == 0) return hipSuccess;
+  EmbedArgs a = embed_args(p, ids);
+  a.weight = weight;
+  a.out = out;
+  if (p.dtype == FLCE_BF16) embed_forward_t<bf16>(p, a, st);
+  else if (p.dtype == FLCE_F16) embed_forward_t<f16>(p, a, st);
+  else embed_forward_t<float>(p, a, st);
+  return hipGetLastError();
+}
+
+template <typename T, typename O> static void embed_runs_t(const EmbedPlan& p, const RunArgs& a, hipStream_t st) {
+  constexpr int kVec = 16 / sizeof(T);
+  const bool vec = whole16(a.grad, p.h, p.dtype) && p.h % kVec == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.gw) & (kVec * sizeof(O) - 1)) == 0;
+  const int per = 256 * (vec ? kVec : 1);
+  const dim3 grid((unsigned)p.n_chunks, (unsigned)((p.h + per - 1) / per));
+  if (vec) embed_runs_kernel<T, O, kVec><<<grid, 256, 0, st>>>(a);
+  else embed_runs_kernel<T, O, 1><<<grid, 256, 0, st>>>(a);
+  embed_join_kernel<O><<<dim3((unsigned)p.n_chunks, (unsigned)((p.h + 255) / 256)), 256, 0, st>>>(a);
+}
+
+template <typename O> static void embed_zero_t(const EmbedPlan& p, void* gw, hipStream_t st) {
+  if ((reinterpret_cast<uintptr_t>(gw) & 15) == 0)
+    embed_zero_kernel<O, 16 / sizeof(O)><<<4096, 256, 0, st>>>(static_cast<O*>(gw), p.v * p.h);
+  else
+    embed_zero_kernel<O, 1><<<4096, 256, 0, st>>>(static_cast<O*>(gw), p.v * p.h);
+}
+
+template <typename T> static void embed_runs_o(const EmbedPlan& p, const RunArgs& a, hipStream_t st) {
+  if (p.grad_dtype == FLCE_BF16) embed_runs_t<T, bf16>(p, a, st);
+  else if (p.grad_dtype == FLCE_F16) embed_runs_t<T, f16>(p, a, st);
+  else embed_runs_t<T, float>(p, a, st);
+}
+
+hipError_t launch_embedding_backward(const EmbedPlan& p, const void* ids, const void* grad, void* grad_weight, char* ws,
+                                     hipStream_t st) {
+  if (!p.accumulate) {
+    if (p.grad_dtype == FLCE_BF16) embed_zero_t<bf16>(p, grad_weight, st);
+    else if (p.grad_dtype == FLCE_F16) embed_zero_t<f16>(p, grad_weight, st);
+    else embed_zero_t<float>(p, grad_weight, st);
+  }
+  if (p.n == 0) return hipGetLastError();
+  SortArgs s{};
+  s.e = embed_args(p, ids);
+  s.hist = reinterpret_cast<uint32_t*>(ws + p.w_hist);
+  s.blocks = p.sort_blocks;
+  int to = 0;
+  for (int k = 0; k < p.passes; k++, to ^= 1) {
+    s.shift = k * kSortBits;
+    s.first = k == 0;
+    s.keys = reinterpret_cast<const uint32_t*>(ws + p.w_keys[to ^ 1]);
+    s.at = reinterpret_cast<const uint32_t*>(ws + p.w_at[to ^ 1]);
+    s.keys_out = reinterpret_cast<uint32_t*>(ws + p.w_keys[to]);
+    s.at_out = reinterpret_cast<uint32_t*>(ws + p.w_at[to]);
+    sort_count_kernel<<<p.sort_blocks, 1024, 0, st>>>(s);
+    sort_scan_kernel<<<1, 1024, 0, st>>>(s.hist, (int64_t)kSortBins * p.sort_blocks);
+    sort_place_kernel<<<p.sort_blocks, 1024, 0, st>>>(s);
+  }
+  RunArgs a{};
+  a.keys = s.keys_out;
+  a.at = s.at_out;
+  a.n = p.n;
+  a.v = p.v;
+  a.h = p.h;
+  a.chunk = p.chunk;
+  a.n_chunks = p.n_chunks;
+  a.scale = p.scale;
+  a.accumulate = p.accumulate ? 1 : 0;
+  a.grad = grad;
+  a.gw = grad_weight;
+  a.part = reinterpret_cast<float*>(ws + p.w_part);
+  if (p.dtype == FLCE_BF16) embed_runs_o<bf16>(p, a, st);
+  else if (p.dtype == FLCE_F16) embed_runs_o<f16>(p, a, st);
+  else embed_runs_o<float>(p, a, st);
+  return hipGetLastError();
+}
+
+}  // namespace flce

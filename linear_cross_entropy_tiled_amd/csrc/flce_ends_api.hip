@@ -1,7 +1,8 @@
-// C ABI of the operators at the ends of a model: layer norm.  Validation runs on
-// the host before any HIP call.
+// C ABI of the operators at the ends of a model: token embedding and layer norm.
+// Validation runs on the host before any HIP call.
 #include <math.h>
 
+#include "flce_embed.h"
 #include "flce_norm.h"
 
 namespace flce {
@@ -34,11 +35,72 @@ static int norm_args(const flce_norm_params* p, NormArgs* a) {
   return FLCE_OK;
 }
 
+// Token numbers and rows are held in 32 bits by the gradient's sort.
+static constexpr int64_t kMaxEmbedRows = (int64_t(1) << 31) - 1;
+
+static int embedding_plan(const flce_embedding_params* p, EmbedPlan* pl) {
+  if (!p || p->n_tokens < 0 || p->hidden < 1 || p->vocab < 1) return FLCE_ERR_INVALID_ARG;
+  if (!ends_dtype_ok(p->dtype) || !ends_dtype_ok(p->grad_weight_dtype)) return FLCE_ERR_INVALID_ARG;
+  if ((p->flags & ~(FLCE_ACCUMULATE_GRAD_WEIGHT | FLCE_TARGETS_INT32)) != 0 || !isfinite(p->scale))
+    return FLCE_ERR_INVALID_ARG;
+  if (p->n_tokens > kMaxEmbedRows || p->vocab > kMaxEmbedRows || p->hidden > (int64_t(1) << 20))
+    return FLCE_ERR_UNSUPPORTED;
+  if (p->n_tokens > kMaxElements / p->hidden || p->vocab > kMaxElements / p->hidden) return FLCE_ERR_UNSUPPORTED;
+  *pl = EmbedPlan{};
+  pl->n = p->n_tokens;
+  pl->v = p->vocab;
+  pl->h = (int)p->hidden;
+  pl->dtype = p->dtype;
+  pl->grad_dtype = p->grad_weight_dtype;
+  pl->ids_i32 = (p->flags & FLCE_TARGETS_INT32) != 0;
+  pl->accumulate = (p->flags & FLCE_ACCUMULATE_GRAD_WEIGHT) != 0;
+  pl->scale = p->scale;
+  pl->ignore_index = p->ignore_index;
+  plan_embedding_backward(pl);
+  return FLCE_OK;
+}
+
 }  // namespace flce
 
 using namespace flce;
 
 extern "C" {
+
+int flce_embedding_workspace_size(const flce_embedding_params* p, size_t* bytes) {
+  if (!bytes) return FLCE_ERR_INVALID_ARG;
+  EmbedPlan pl;
+  const int rc = embedding_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  *bytes = pl.w_bytes;
+  return FLCE_OK;
+}
+
+int flce_embedding_forward(const flce_embedding_params* p, const void* ids, const void* weight, void* out,
+                           void* stream) {
+  EmbedPlan pl;
+  const int rc = embedding_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  if (pl.n > 0 && (!ids || !weight || !out)) return FLCE_ERR_INVALID_ARG;
+  const size_t e = size_of(pl.dtype);
+  if (!aligned_to(ids, pl.ids_i32 ? 4 : 8) || !aligned_to(weight, e) || !aligned_to(out, e)) return FLCE_ERR_UNSUPPORTED;
+  return launch_embedding_forward(pl, ids, weight, out, static_cast<hipStream_t>(stream)) == hipSuccess ? FLCE_OK
+                                                                                                      : FLCE_ERR_HIP;
+}
+
+int flce_embedding_backward(const flce_embedding_params* p, const void* ids, const void* grad_out, void* grad_weight,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  EmbedPlan pl;
+  const int rc = embedding_plan(p, &pl);
+  if (rc != FLCE_OK) return rc;
+  if (!grad_weight || !workspace || (pl.n > 0 && (!ids || !grad_out))) return FLCE_ERR_INVALID_ARG;
+  if (!aligned_to(ids, pl.ids_i32 ? 4 : 8) || !aligned_to(grad_out, size_of(pl.dtype)) ||
+      !aligned_to(grad_weight, size_of(pl.grad_dtype)) || !aligned_to(workspace, 16))
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < pl.w_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = launch_embedding_backward(pl, ids, grad_out, grad_weight, static_cast<char*>(workspace),
+                                                 static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
 
 int flce_layer_norm_workspace_size(const flce_norm_params* p, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;

@@ -19,3 +19,22 @@ def layer_norm_grads(x, weight, eps, dy):
     d = dy if weight is None else dy * weight
     dx = rstd * (d - d.mean(axis=1, keepdims=True) - xhat * (d * xhat).mean(axis=1, keepdims=True))
     return dx, (dy * xhat).sum(axis=0), dy.sum(axis=0)
+
+
+def embedding(ids, weight, scale, ignore_index=-100):
+    ids = np.asarray(ids, dtype=np.int64)
+    known = (ids != ignore_index) & (ids >= 0) & (ids < len(weight))
+    out = np.zeros((len(ids), weight.shape[1]))
+    out[known] = scale * weight[ids[known]]
+    return out
+
+
+def embedding_grad(ids, vocab, grad, scale, ignore_index=-100):
+    """(gradient (V, H), its absolute terms, tokens of each row)."""
+    ids = np.asarray(ids, dtype=np.int64)
+    known = (ids != ignore_index) & (ids >= 0) & (ids < vocab)
+    out, terms, count = np.zeros((vocab, grad.shape[1])), np.zeros((vocab, grad.shape[1])), np.zeros(vocab)
+    np.add.at(out, ids[known], scale * grad[known])
+    np.add.at(terms, ids[known], abs(scale) * np.abs(grad[known]))
+    np.add.at(count, ids[known], 1)
+    return out, terms, count
