@@ -405,6 +405,39 @@ int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hi
                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The same from 4-bit microscaled operands (MXFP4, of the OCP Microscaling Formats
+ * specification): half the weight bytes of 8 bits and twice their matrix rate.  32
+ * neighbouring values of a row share a scale 2^(s - 127), one byte s (255 = NaN); a
+ * value is a 4-bit code, a sign bit above the number of one of
+ * 0, 1/2, 1, 3/2, 2, 3, 4, 6, two to a byte, the earlier value in the low half.
+ * z_ij as above, of the values that both operands stand for; products are summed in
+ * fp32.  No backward.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * x (rows x cols, contiguous, dtype) to codes q (rows x cols / 2 bytes) and scales
+ * (rows x cols / 32 bytes).  Of a block's largest magnitude m, s - 127 is
+ * floor(log2 m) - 2, at least -127; x 2^(127 - s) is rounded to the nearest code,
+ * ties to the even one, and to 6 beyond it.  A block that holds NaN or an infinity
+ * gives s = 255 and codes 0.  cols % 32 == 0; x and q 16-byte aligned.
+ */
+int flce_quantize_mxfp4(int dtype, const void* x, int64_t rows, int64_t cols, void* q, void* scale, void* stream);
+
+/* The values that q and scale stand for, rounded to dtype. */
+int flce_dequantize_mxfp4(int dtype, const void* q, const void* scale, int64_t rows, int64_t cols, void* x,
+                          void* stream);
+
+/* Bytes of device workspace flce_logprobs_mxfp4 needs.  Host only.  params as for
+ * flce_logprobs_int8, with hidden % 32 == 0 and at most 2^18, and N*H below 2^31. */
+int flce_logprobs_mxfp4_workspace_size(const flce_params* p, size_t* bytes);
+
+/* hidden (N, H / 2) and weight (V, H / 2): codes, 16-byte aligned as bias (fp32, or NULL) is; their scales
+ * (N, H / 32) and (V, H / 32): 4-byte aligned.  Outputs and rows without a target as flce_logprobs_forward. */
+int flce_logprobs_mxfp4(const flce_params* p, const void* hidden, const void* hidden_scale, const void* weight,
+                        const void* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Preference and policy losses over per-token log-probabilities (as
  * flce_logprobs_forward gives them), forward and backward.
  *

@@ -13,7 +13,8 @@ declared in ``include/flce.h``).  This module only marshals arguments:
   weighted squared error (``flce_weighted_mse_chunk``);
 * ``token_logprobs`` (``logprobs.py``) is a torch op for per-token log-probabilities
   and entropies of the head (``flce_logprobs_*``), ``token_logprobs_int8`` their form
-  for a frozen 8-bit head, whose weight ``quantize_int8`` makes;
+  for a frozen 8-bit head, whose weight ``quantize_int8`` makes, and
+  ``token_logprobs_mxfp4`` for a 4-bit one (``quantize_mxfp4``, ``dequantize_mxfp4``);
 * ``embedding`` (``embedding.py``) is a torch op for the token embedding,
   ``embedding_backward`` its gradient added into a tied head's buffer
   (``flce_embedding_*``);
@@ -64,7 +65,8 @@ EXPORTED = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_get_st
             "flce_logprobs_backward", "flce_quantize_int8", "flce_logprobs_int8_workspace_size",
             "flce_logprobs_int8", "flce_layer_norm_workspace_size", "flce_layer_norm_forward",
             "flce_layer_norm_backward", "flce_embedding_workspace_size", "flce_embedding_forward",
-            "flce_embedding_backward")
+            "flce_embedding_backward", "flce_quantize_mxfp4", "flce_dequantize_mxfp4",
+            "flce_logprobs_mxfp4_workspace_size", "flce_logprobs_mxfp4")
 
 FLCE_KERNEL_FORWARD_TILES = 1
 FLCE_KERNEL_DLOGITS = 2
@@ -265,6 +267,14 @@ def load(path: Optional[str] = None):
     lib.flce_logprobs_int8_workspace_size.restype = ctypes.c_int
     lib.flce_logprobs_int8.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.flce_logprobs_int8.restype = ctypes.c_int
+    lib.flce_quantize_mxfp4.argtypes = [ctypes.c_int, vp, i64, i64, vp, vp, vp]
+    lib.flce_quantize_mxfp4.restype = ctypes.c_int
+    lib.flce_dequantize_mxfp4.argtypes = [ctypes.c_int, vp, vp, i64, i64, vp, vp]
+    lib.flce_dequantize_mxfp4.restype = ctypes.c_int
+    lib.flce_logprobs_mxfp4_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+    lib.flce_logprobs_mxfp4_workspace_size.restype = ctypes.c_int
+    lib.flce_logprobs_mxfp4.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_logprobs_mxfp4.restype = ctypes.c_int
     view, RP, LP = flce_token_view, ctypes.POINTER(flce_preference_params), ctypes.POINTER(flce_policy_params)
     lib.flce_preference_workspace_size.argtypes = [RP, ctypes.POINTER(sz)]
     lib.flce_preference_workspace_size.restype = ctypes.c_int
@@ -445,6 +455,28 @@ def flce_logprobs_int8(params, hidden, hidden_scale, weight, weight_scale, bias,
                        workspace_bytes, stream) -> int:
     return load().flce_logprobs_int8(ctypes.byref(params), hidden, hidden_scale, weight, weight_scale, bias, targets,
                                      logps, entropy, lse, workspace, workspace_bytes, stream)
+
+
+def flce_quantize_mxfp4(dtype, x, rows, cols, q, scale, stream) -> int:
+    return load().flce_quantize_mxfp4(dtype, x, rows, cols, q, scale, stream)
+
+
+def flce_dequantize_mxfp4(dtype, q, scale, rows, cols, x, stream) -> int:
+    return load().flce_dequantize_mxfp4(dtype, q, scale, rows, cols, x, stream)
+
+
+def flce_logprobs_mxfp4_workspace_size(params: flce_params) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().flce_logprobs_mxfp4_workspace_size(ctypes.byref(params), ctypes.byref(out))
+    if rc != FLCE_OK:
+        raise FlceError(rc, "flce_logprobs_mxfp4_workspace_size")
+    return out.value
+
+
+def flce_logprobs_mxfp4(params, hidden, hidden_scale, weight, weight_scale, bias, targets, logps, entropy, lse, workspace,
+                        workspace_bytes, stream) -> int:
+    return load().flce_logprobs_mxfp4(ctypes.byref(params), hidden, hidden_scale, weight, weight_scale, bias, targets,
+                                      logps, entropy, lse, workspace, workspace_bytes, stream)
 
 
 def flce_preference_workspace_size(params: flce_preference_params) -> int:
@@ -980,7 +1012,8 @@ def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_ro
 
 # ----------------------------------------------------------------------------- alignment training
 
-from .logprobs import quantize_int8, token_logprobs, token_logprobs_int8  # noqa: E402,F401
+from .logprobs import (dequantize_mxfp4, quantize_int8, quantize_mxfp4, token_logprobs,  # noqa: E402,F401
+                       token_logprobs_int8, token_logprobs_mxfp4)
 from .alignment import policy_loss, preference_loss  # noqa: E402,F401
 
 

@@ -6,6 +6,7 @@
 
 #include "flce_internal.h"
 #include "flce_logprobs.h"
+#include "flce_mx.h"
 
 namespace flce {
 
@@ -328,7 +329,7 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   const int64_t n64 = (P.N + 63) / 64, h64 = (P.H + 63) / 64;
   const int64_t wg_target = 3 * kTargetWorkgroups;   // small workgroups that share the chip
   L.bn = P.N <= 16 ? 16 : 64;
-  L.vt_large = P.N <= 16 ? 0 : (int)large_vocab_tiles(P, P.V);
+  L.vt_large = P.N <= 16 || P.mx ? 0 : (int)large_vocab_tiles(P, P.V);
   if (L.vt_large > 0) L.S_large = forward_splits(P.n_tt, L.vt_large);
   const int64_t rest = P.V - int64_t(L.vt_large) * 256;
   if (rest > 0) {
@@ -349,6 +350,15 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   }
   L.N_pad = L.vt_large > 0 ? (int)P.N_pad : (int)((P.N + L.bn - 1) / L.bn * L.bn);
   L.f_bytes = align_up(kStatusBytes + size_t(4) * (L.S_large + L.S_small) * L.N_pad * 4, 256);
+  if (P.mx) {
+    const int blocks = (int)(P.H / 16);
+    L.ld_mx = (blocks + 3) / 4 * 4;
+    if (L.ld_mx != blocks) {
+      L.f_hmx = L.f_bytes;
+      L.f_wmx = align_up(L.f_hmx + size_t(P.N) * L.ld_mx, 256);
+      L.f_bytes = align_up(L.f_wmx + size_t(P.V) * L.ld_mx, 256);
+    }
+  }
 
   L.n64 = (int)n64;
   L.N64 = (int)(n64 * 64);
@@ -525,6 +535,8 @@ int flce_scale_gradients(const flce_params* p, const float* g, void* grad_hidden
 
 // The int32 sums of up to 2^17 products of magnitude at most 127^2 stay below 2^31.
 static constexpr int64_t kMaxInt8Hidden = int64_t(1) << 17;
+static constexpr int64_t kMaxMxHidden = int64_t(1) << 18;
+static constexpr int64_t kMxBlock = 32;
 
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 static bool targets_aligned(const Plan& pl, const void* t) {   // read one at a time, unlike the matrices
@@ -533,13 +545,21 @@ static bool targets_aligned(const Plan& pl, const void* t) {   // read one at a 
 
 // The log-probability entry points take the loss's parameters, of which the
 // reduction and the z-loss have no meaning there.
-static int logprobs_plan(const flce_params* p, bool int8, Plan* pl, LpPlan* lp) {
+enum class Scores { kTrained, kInt8, kMx };
+
+static int logprobs_plan(const flce_params* p, Scores kind, Plan* pl, LpPlan* lp) {
   flce_params q;
-  if (p && int8) {   // no backward: neither its chunk nor the type it would have limits the sizes
+  const bool int8 = kind == Scores::kInt8, mx = kind == Scores::kMx;
+  if (p && kind != Scores::kTrained) {   // no backward: neither its chunk nor the type it would have limits the sizes
     if (!valid_dtype(p->dtype)) return FLCE_ERR_INVALID_ARG;
     q = *p;
     q.dtype = q.grad_weight_dtype = FLCE_BF16;
     q.vocab_chunk = 256;
+    if (mx) {   // planned by the row's bytes
+      if (q.hidden <= 0) return FLCE_ERR_INVALID_ARG;
+      if (q.hidden % kMxBlock != 0) return FLCE_ERR_UNSUPPORTED;
+      q.hidden /= 2;
+    }
     p = &q;
   }
   const int rc = make_plan(p, pl);
@@ -550,6 +570,11 @@ static int logprobs_plan(const flce_params* p, bool int8, Plan* pl, LpPlan* lp) 
     pl->int8 = true;
     pl->esize = 1;
   }
+  if (mx) {
+    if (pl->H > kMaxMxHidden / 2) return FLCE_ERR_UNSUPPORTED;
+    pl->int8 = pl->mx = true;
+    pl->esize = 1;
+  }
   plan_logprobs(*pl, lp);
   return FLCE_OK;
 }
@@ -558,7 +583,7 @@ int flce_logprobs_workspace_size(const flce_params* p, int pass, size_t* bytes) 
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   Plan pl;
   LpPlan lp;
-  const int rc = logprobs_plan(p, false, &pl, &lp);
+  const int rc = logprobs_plan(p, Scores::kTrained, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   if (pass == FLCE_PASS_FORWARD) *bytes = lp.f_bytes;
   else if (pass == FLCE_PASS_BACKWARD) *bytes = lp.b_bytes;
@@ -571,7 +596,7 @@ int flce_logprobs_forward(const flce_params* p, const void* hidden, const void* 
                           size_t workspace_bytes, void* stream) {
   Plan pl;
   LpPlan lp;
-  const int rc = logprobs_plan(p, false, &pl, &lp);
+  const int rc = logprobs_plan(p, Scores::kTrained, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!workspace || !weight) return FLCE_ERR_INVALID_ARG;
@@ -591,7 +616,7 @@ int flce_logprobs_backward(const flce_params* p, const void* hidden, const void*
                            void* workspace, size_t workspace_bytes, void* stream) {
   Plan pl;
   LpPlan lp;
-  const int rc = logprobs_plan(p, false, &pl, &lp);
+  const int rc = logprobs_plan(p, Scores::kTrained, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!weight || !workspace) return FLCE_ERR_INVALID_ARG;
@@ -625,7 +650,7 @@ int flce_logprobs_int8_workspace_size(const flce_params* p, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   Plan pl;
   LpPlan lp;
-  const int rc = logprobs_plan(p, true, &pl, &lp);
+  const int rc = logprobs_plan(p, Scores::kInt8, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   *bytes = lp.f_bytes;
   return FLCE_OK;
@@ -636,12 +661,63 @@ int flce_logprobs_int8(const flce_params* p, const void* hidden, const float* hi
                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   Plan pl;
   LpPlan lp;
-  const int rc = logprobs_plan(p, true, &pl, &lp);
+  const int rc = logprobs_plan(p, Scores::kInt8, &pl, &lp);
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!workspace || !weight || !weight_scale) return FLCE_ERR_INVALID_ARG;
   if (pl.N > 0 && (!hidden || !hidden_scale || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned16(weight_scale) ||
+      !aligned16(workspace) || !targets_aligned(pl, targets) || !aligned4(hidden_scale) || !aligned4(logps) ||
+      !aligned4(entropy) || !aligned4(lse))
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < lp.f_bytes) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = launch_logprobs(pl, lp, hidden, weight, bias, hidden_scale, weight_scale, targets, logps, entropy,
+                                       lse, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+int flce_quantize_mxfp4(int dtype, const void* x, int64_t rows, int64_t cols, void* q, void* scale, void* stream) {
+  if (!valid_dtype(dtype) || rows < 0 || cols <= 0) return FLCE_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !q || !scale)) return FLCE_ERR_INVALID_ARG;
+  if (cols % kMxBlock != 0 || rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30) || !aligned16(x) || !aligned16(q))
+    return FLCE_ERR_UNSUPPORTED;
+  const hipError_t e = launch_quantize_mx(dtype, x, rows * (cols / kMxBlock), static_cast<uint8_t*>(q),
+                                          static_cast<uint8_t*>(scale), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+int flce_dequantize_mxfp4(int dtype, const void* q, const void* scale, int64_t rows, int64_t cols, void* x,
+                          void* stream) {
+  if (!valid_dtype(dtype) || rows < 0 || cols <= 0) return FLCE_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !q || !scale)) return FLCE_ERR_INVALID_ARG;
+  if (cols % kMxBlock != 0 || rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30) || !aligned16(x) || !aligned16(q))
+    return FLCE_ERR_UNSUPPORTED;
+  const hipError_t e = launch_dequantize_mx(dtype, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale),
+                                            rows * (cols / kMxBlock), x, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+int flce_logprobs_mxfp4_workspace_size(const flce_params* p, size_t* bytes) {
+  if (!bytes) return FLCE_ERR_INVALID_ARG;
+  Plan pl;
+  LpPlan lp;
+  const int rc = logprobs_plan(p, Scores::kMx, &pl, &lp);
+  if (rc != FLCE_OK) return rc;
+  *bytes = lp.f_bytes;
+  return FLCE_OK;
+}
+
+int flce_logprobs_mxfp4(const flce_params* p, const void* hidden, const void* hidden_scale, const void* weight,
+                        const void* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  Plan pl;
+  LpPlan lp;
+  const int rc = logprobs_plan(p, Scores::kMx, &pl, &lp);
+  if (rc != FLCE_OK) return rc;
+  pl.has_bias = bias != nullptr;
+  if (!workspace || !weight || !weight_scale) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && (!hidden || !hidden_scale || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned4(weight_scale) ||
       !aligned16(workspace) || !targets_aligned(pl, targets) || !aligned4(hidden_scale) || !aligned4(logps) ||
       !aligned4(entropy) || !aligned4(lse))
     return FLCE_ERR_UNSUPPORTED;

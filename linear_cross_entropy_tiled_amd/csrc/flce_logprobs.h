@@ -13,6 +13,9 @@ struct LpPlan {
   int bn;
   int vt_large, S_large, S_small;
   int N_pad;
+  // MXFP4 scale rows of a length that is no multiple of 4 are copied to rows of ld_mx
+  int ld_mx;
+  size_t f_hmx, f_wmx;
   size_t f_bytes;
 
   // Up to 64 tokens in 16 bits: the logit gradient is held as the sum of two 16-bit
@@ -42,9 +45,12 @@ struct LpTileArgs {
   const void* bias;           // the operands' type; fp32 for int8
   const float* hidden_scale;  // int8
   const float* weight_scale;  // int8
+  const uint8_t* hidden_mx;   // MXFP4: scale bytes, rows of ld_hmx (a multiple of 4)
+  const uint8_t* weight_mx;
+  uint32_t ld_hmx, ld_wmx;
   const void* targets;
   int tgt_i32;
-  int N, H, V;
+  int N, H, V;                // H: elements of a row, of MXFP4 its bytes
   int64_t ignore_index;
   float scale, cap;
   int v_first;                // first vocabulary row of the launch
@@ -55,9 +61,9 @@ struct LpTileArgs {
 };
 
 void plan_logprobs(const Plan& pl, LpPlan* lp);
-// pl.int8: 8-bit operands with their scales, bias in fp32.
+// pl.int8, pl.mx: 8- and 4-bit operands with their scales (fp32 and bytes), bias in fp32.
 hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden, const void* weight, const void* bias,
-                           const float* hidden_scale, const float* weight_scale, const void* targets, float* logps,
+                           const void* hidden_scale, const void* weight_scale, const void* targets, float* logps,
                            float* entropy, float* lse, char* ws, hipStream_t st);
 hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGrad& g, const void* hidden,
                                     const void* weight, const void* bias, const void* targets, const float* lse,

@@ -424,7 +424,7 @@ hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols,
 }
 
 hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden, const void* weight, const void* bias,
-                           const float* hidden_scale, const float* weight_scale, const void* targets, float* logps,
+                           const void* hidden_scale, const void* weight_scale, const void* targets, float* logps,
                            float* entropy, float* lse, char* ws, hipStream_t st) {
   float* part = reinterpret_cast<float*>(ws + kStatusBytes);
   int* status = reinterpret_cast<int*>(ws);
@@ -433,8 +433,22 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
     a.hidden = static_cast<const char*>(hidden);
     a.weight = static_cast<const char*>(weight);
     a.bias = bias;
-    a.hidden_scale = hidden_scale;
-    a.weight_scale = weight_scale;
+    a.hidden_scale = static_cast<const float*>(hidden_scale);
+    a.weight_scale = static_cast<const float*>(weight_scale);
+    if (pl.mx) {
+      const int blocks = (int)(pl.H / 16);
+      a.hidden_mx = static_cast<const uint8_t*>(hidden_scale);
+      a.weight_mx = static_cast<const uint8_t*>(weight_scale);
+      a.ld_hmx = a.ld_wmx = (uint32_t)lp.ld_mx;
+      if (lp.ld_mx != blocks) {
+        uint8_t* hs = reinterpret_cast<uint8_t*>(ws + lp.f_hmx);
+        uint8_t* wsc = reinterpret_cast<uint8_t*>(ws + lp.f_wmx);
+        launch_pad_scales(a.hidden_mx, pl.N, blocks, lp.ld_mx, hs, st);
+        launch_pad_scales(a.weight_mx, pl.V, blocks, lp.ld_mx, wsc, st);
+        a.hidden_mx = hs;
+        a.weight_mx = wsc;
+      }
+    }
     a.targets = targets;
     a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
     a.N = (int)pl.N;

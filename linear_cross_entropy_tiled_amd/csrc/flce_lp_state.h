@@ -2,6 +2,7 @@
 #pragma once
 
 #include "flce_device.h"
+#include "flce_mx.h"
 
 namespace flce {
 
@@ -88,5 +89,6 @@ __device__ __forceinline__ void tanh4(const float (&w)[4], float (&th)[4], float
 
 template <typename T> struct BiasOf { typedef T type; };
 template <> struct BiasOf<int8_t> { typedef float type; };
+template <> struct BiasOf<mx4> { typedef float type; };
 
 }  // namespace flce

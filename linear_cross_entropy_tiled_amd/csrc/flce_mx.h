@@ -1,0 +1,28 @@
+// 4-bit microscaled operands (MXFP4): the type's tag, matrix instruction and launchers (internal).
+//
+// 32 neighbouring values of a row share one power of two, held as a byte s (2^(s - 127),
+// 255 = NaN); each value is a 4-bit code, sign and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6 (two
+// to a byte, the earlier one in the low half).  A lane's 16 bytes of K are exactly one such
+// block: v_mfma_scale_f32_16x16x128_f8f6f4 takes them as the 8- and 16-bit instructions take
+// theirs, and the block's scale byte in a register of its own.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace flce {
+
+struct mx4 {   // one byte: two values
+  uint8_t two;
+};
+
+template <typename T> inline constexpr bool is_mx = false;
+template <> inline constexpr bool is_mx<mx4> = true;
+
+hipError_t launch_quantize_mx(int dtype, const void* x, int64_t blocks, uint8_t* q, uint8_t* scale, hipStream_t st);
+hipError_t launch_dequantize_mx(int dtype, const uint8_t* q, const uint8_t* scale, int64_t blocks, void* x,
+                                hipStream_t st);
+// Scale rows of `cols` bytes to rows of `ld` bytes, a multiple of 4.
+hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int ld, uint8_t* out, hipStream_t st);
+
+}  // namespace flce

@@ -1,0 +1,112 @@
+// Quantisation to MXFP4 (flce_mx.h has the format) and back.
+//
+// Of a block's largest magnitude m the scale is 2^(floor(log2 m) - 2), the power that
+// brings m into [4, 8), at least 2^-127; a value is rounded to the nearest code, ties to
+// the even code, and to 6 beyond it.  Everything but that rounding is exact in fp32, so
+// every implementation of the definition gives the same codes.  A block with NaN or an
+// infinity has scale 255 (NaN) and codes 0.
+#include "../../include/flce.h"
+#include "flce_device.h"
+#include "flce_mx.h"
+
+namespace flce {
+
+// The code of |y|, y below 8.
+__device__ __forceinline__ uint32_t e2m1(float y) {
+  return (uint32_t)(y > 0.25f) + (uint32_t)(y >= 0.75f) + (uint32_t)(y > 1.25f) + (uint32_t)(y >= 1.75f) +
+         (uint32_t)(y > 2.5f) + (uint32_t)(y >= 3.5f) + (uint32_t)(y > 5.0f);
+}
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  constexpr uint32_t kHalves = 0xC8643210u;   // twice the eight magnitudes, four bits each
+  const float v = 0.5f * (float)((kHalves >> (4 * (c & 7))) & 15u);
+  return c & 8 ? -v : v;
+}
+
+// Four neighbouring lanes hold a block, eight values each.
+template <typename T> __global__ __launch_bounds__(256) void quantize_mx_kernel(const T* x, int64_t n8, uint32_t* q,
+                                                                                uint8_t* scale) {
+  typedef T V __attribute__((ext_vector_type(8)));
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;   // whole blocks of four lanes: n8 is a multiple of 4
+  const V v = reinterpret_cast<const V*>(x)[i];
+  float a[8], top = 0.0f;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    a[j] = (float)v[j];
+    top = fmaxf(top, fabsf(a[j]));
+    bad = bad || !(fabsf(a[j]) < INFINITY);
+  }
+  if (bad) top = INFINITY;
+  top = fmaxf(top, __shfl_xor(top, 1));
+  top = fmaxf(top, __shfl_xor(top, 2));
+  // the exponent field less 2; 0 (and the 2^-127 that it stands for) from there down
+  const int field = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
+  const bool none = field == 255;
+  const int code = field > 2 ? field - 2 : 0;
+  const float inv = __builtin_bit_cast(float, (uint32_t)(254 - code) << 23);
+  uint32_t out = 0;
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    out |= (e2m1(fabsf(a[j]) * inv) | (__builtin_bit_cast(uint32_t, a[j]) >> 31 << 3)) << (4 * j);
+  q[i] = none ? 0u : out;
+  if ((i & 3) == 0) scale[i >> 2] = (uint8_t)(none ? 255 : code);
+}
+
+template <typename T> __global__ __launch_bounds__(256) void dequantize_mx_kernel(const uint32_t* q, const uint8_t* scale,
+                                                                                  int64_t n8, T* x) {
+  typedef T V __attribute__((ext_vector_type(8)));
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const uint32_t c = q[i];
+  const int s = scale[i >> 2];
+  V v;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const float y = ldexpf(e2m1_value(c >> (4 * j)), s - 127);
+    v[j] = (T)(s == 255 ? __builtin_nanf("") : y);
+  }
+  reinterpret_cast<V*>(x)[i] = v;
+}
+
+constexpr int64_t kMostGroups = int64_t(1) << 22;   // of 256 threads: a launch of 2^32 threads or more leaves some out
+
+template <typename T> static void quantize_t(const void* x, int64_t n8, uint8_t* q, uint8_t* scale, hipStream_t st) {
+  for (int64_t i = 0; i < n8; i += kMostGroups * 256) {
+    const int64_t n = n8 - i < kMostGroups * 256 ? n8 - i : kMostGroups * 256;
+    quantize_mx_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
+        static_cast<const T*>(x) + i * 8, n, reinterpret_cast<uint32_t*>(q) + i, scale + i / 4);
+  }
+}
+template <typename T> static void dequantize_t(const uint8_t* q, const uint8_t* scale, int64_t n8, void* x, hipStream_t st) {
+  for (int64_t i = 0; i < n8; i += kMostGroups * 256) {
+    const int64_t n = n8 - i < kMostGroups * 256 ? n8 - i : kMostGroups * 256;
+    dequantize_mx_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(reinterpret_cast<const uint32_t*>(q) + i,
+                                                                         scale + i / 4, n, static_cast<T*>(x) + i * 8);
+  }
+}
+
+hipError_t launch_quantize_mx(int dtype, const void* x, int64_t blocks, uint8_t* q, uint8_t* scale, hipStream_t st) {
+  if (dtype == FLCE_BF16) quantize_t<bf16>(x, 4 * blocks, q, scale, st);
+  else if (dtype == FLCE_F16) quantize_t<f16>(x, 4 * blocks, q, scale, st);
+  else quantize_t<float>(x, 4 * blocks, q, scale, st);
+  return hipGetLastError();
+}
+hipError_t launch_dequantize_mx(int dtype, const uint8_t* q, const uint8_t* scale, int64_t blocks, void* x,
+                                hipStream_t st) {
+  if (dtype == FLCE_BF16) dequantize_t<bf16>(q, scale, 4 * blocks, x, st);
+  else if (dtype == FLCE_F16) dequantize_t<f16>(q, scale, 4 * blocks, x, st);
+  else dequantize_t<float>(q, scale, 4 * blocks, x, st);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void pad_scales_kernel(const uint8_t* scale, int64_t rows, int cols, int ld, uint8_t* out) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < ld; c += 256) out[r * ld + c] = c < cols ? scale[r * cols + c] : 0;
+}
+hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int ld, uint8_t* out, hipStream_t st) {
+  if (rows > 0) pad_scales_kernel<<<(unsigned)(rows < 65536 ? rows : 65536), 256, 0, st>>>(scale, rows, cols, ld, out);
+  return hipGetLastError();
+}
+
+}  // namespace flce

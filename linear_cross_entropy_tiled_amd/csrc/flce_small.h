@@ -11,6 +11,7 @@
 #pragma once
 
 #include "flce_device.h"
+#include "flce_mx_device.h"
 
 namespace flce {
 namespace small {
@@ -154,11 +155,38 @@ __device__ __forceinline__ void stage_mma(const char* st, int wm, int wn, int la
   }
 }
 
+// The same of MXFP4 operands; sc: the stage's scales.
+template <int BN>
+__device__ __forceinline__ void stage_mma_mx(const char* st, const char* sc, int wm, int wn, int lane,
+                                             Acc (&acc)[Shape<BN>::MI][Shape<BN>::NI]) {
+  typedef Shape<BN> S;
+  const uint8_t* row = reinterpret_cast<const uint8_t*>(sc) + 8 * (lane & 15) + (lane >> 4);
+#pragma unroll
+  for (int s = 0; s < kSubsteps; s++) {
+    i32x4 a[S::MI], b[S::NI];
+    int sa[S::MI], sb[S::NI];
+#pragma unroll
+    for (int mi = 0; mi < S::MI; mi++) {
+      a[mi] = Frag<mx4, true>::read(st, (wm * S::MI + mi) * 16, s, lane);
+      sa[mi] = row[(wm * S::MI + mi) * 128 + 4 * s];
+    }
+#pragma unroll
+    for (int ni = 0; ni < S::NI; ni++) {
+      b[ni] = Frag<mx4, true>::read(st + kStageA, (wn * S::NI + ni) * 16, s, lane);
+      sb[ni] = row[512 + (wn * S::NI + ni) * 128 + 4 * s];
+    }
+#pragma unroll
+    for (int mi = 0; mi < S::MI; mi++)
+#pragma unroll
+      for (int ni = 0; ni < S::NI; ni++) mma_mx<0, 0>(acc[mi][ni], a[mi], b[ni], sa[mi], sb[ni]);
+  }
+}
+
 // Waits until at most the loads of `later` stages are outstanding (a wave that has issued
 // others since waits for a little more).
 template <typename T, bool A_KMAJOR, bool B_KMAJOR, int BN, int LATER>
 __device__ __forceinline__ void wait_stage(bool b_loads) {
-  constexpr int A = Loader<T, A_KMAJOR, kBMs>::PER, B = Loader<T, B_KMAJOR, BN>::PER;
+  constexpr int A = Loader<T, A_KMAJOR, kBMs>::PER + (is_mx<T> ? 1 : 0), B = Loader<T, B_KMAJOR, BN>::PER;
   if (b_loads) wait_vmcnt<LATER * (A + B)>();
   else wait_vmcnt<LATER * A>();
 }

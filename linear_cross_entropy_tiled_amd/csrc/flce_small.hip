@@ -21,9 +21,10 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
   typedef Shape<BN> Sh;
   constexpr int E = sizeof(T), MI = Sh::MI, NI = Sh::NI;
   constexpr int kStages = small::stages<T>(BN), SB = small::stage_bytes(BN);
-  constexpr bool I8 = E == 1;
+  constexpr bool MX = is_mx<T>, I8 = E == 1 && !MX;
   typedef typename BiasOf<T>::type B;
   static __shared__ __attribute__((aligned(1024))) char lds[small::lds_bytes<T>(BN)];
+  static __shared__ __attribute__((aligned(256))) char mx_lds[MX ? kStages * small::kScaleStage : 16];
   // a tile's bias and scales arrive with its first stage, up to kStages - 1 stages and so
   // as many tiles ahead of the tile in work
   static __shared__ __attribute__((aligned(256))) char bias_lds[kStages][256], scale_lds[kStages][256];
@@ -68,7 +69,11 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
   small::Loader<T, true, BN> lb;
   la.init(da, tid);
   lb.init(db, tid);
-  const uint32_t lds0 = lds_addr_of(lds);
+  const uint32_t lds0 = lds_addr_of(lds), mx0 = lds_addr_of(mx_lds);
+  small::ScaleLoader<BN> ls;
+  if constexpr (MX)
+    ls.init(a.weight_mx + (size_t)v_begin * a.ld_wmx, (uint32_t)(v_end - v_begin) * a.ld_wmx, a.ld_wmx,
+            a.hidden_mx + (size_t)t0 * a.ld_hmx, (uint32_t)min(a.N - t0, BN) * a.ld_hmx, a.ld_hmx, tid);
 
   int l_tile = 0, l_kt = 0, l_buf = 0, l_side = 0;   // the next stage to load
   auto load_next = [&]() {
@@ -83,6 +88,7 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
     const uint32_t to = lds0 + l_buf * SB;
     la.load(l_kt, to, (uint32_t)l_tile * 64u * ld);
     lb.load(l_kt, to + small::kStageA);
+    if constexpr (MX) ls.load(l_kt, mx0 + l_buf * small::kScaleStage, (uint32_t)l_tile * 64u * a.ld_wmx);
     l_buf = l_buf == kStages - 1 ? 0 : l_buf + 1;
     if (++l_kt == KT) {
       l_kt = 0;
@@ -107,7 +113,10 @@ __global__ __launch_bounds__(small::kThreadsS) void lp_small_kernel(LpTileArgs a
         else wait_loads();
         __syncthreads();   // the stage has landed for every wave, and every wave has read the one before
         load_next();       // into the buffer of the one before
-        small::stage_mma<T, true, true, BN>(lds + buf * SB, wm, wn, lane, to);
+        if constexpr (MX)
+          small::stage_mma_mx<BN>(lds + buf * SB, mx_lds + buf * small::kScaleStage, wm, wn, lane, to);
+        else
+          small::stage_mma<T, true, true, BN>(lds + buf * SB, wm, wn, lane, to);
         buf = buf == kStages - 1 ? 0 : buf + 1;
       }
     });
@@ -473,7 +482,8 @@ template <typename T> static void lp_small_bn(const Plan& pl, int bn, const LpTi
   else lp_small_t<T, 64>(pl, a, n_tt, st);
 }
 void launch_lp_small(const Plan& pl, int bn, const LpTileArgs& a, int n_tt, hipStream_t st) {
-  if (pl.int8) lp_small_bn<int8_t>(pl, bn, a, n_tt, st);
+  if (pl.mx) lp_small_bn<mx4>(pl, bn, a, n_tt, st);
+  else if (pl.int8) lp_small_bn<int8_t>(pl, bn, a, n_tt, st);
   else if (pl.dtype == FLCE_BF16) lp_small_bn<bf16>(pl, bn, a, n_tt, st);
   else if (pl.dtype == FLCE_F16) lp_small_bn<f16>(pl, bn, a, n_tt, st);
   else lp_small_bn<float>(pl, bn, a, n_tt, st);

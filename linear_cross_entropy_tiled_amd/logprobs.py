@@ -7,8 +7,10 @@ import functools
 from typing import Optional
 
 from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError, _dtype_name, _ptr, _stream_handle,
-               _targets_int32, _validate, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_int8,
-               flce_logprobs_int8_workspace_size, flce_logprobs_workspace_size, flce_quantize_int8, make_params)
+               _targets_int32, _validate, flce_dequantize_mxfp4, flce_logprobs_backward, flce_logprobs_forward,
+               flce_logprobs_int8, flce_logprobs_int8_workspace_size, flce_logprobs_mxfp4,
+               flce_logprobs_mxfp4_workspace_size, flce_logprobs_workspace_size, flce_quantize_int8,
+               flce_quantize_mxfp4, make_params)
 
 
 _SAME_DEVICE = contextlib.nullcontext()
@@ -236,4 +238,125 @@ def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hid
         raise_for(flce_logprobs_int8(p, _ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale), _ptr(bias),
                                      _ptr(targets), _ptr(logps), _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes,
                                      stream_handle(dev)), "flce_logprobs_int8")
+    return (logps, entropy) if return_entropy else logps
+
+
+# ----------------------------------------------------------------------------- 4-bit scoring
+
+def _quantize_mx(x):
+    import torch
+    dev = x.device
+    with on_device(dev):
+        q = torch.empty((x.shape[0], x.shape[1] // 2), dtype=torch.uint8, device=dev)
+        scale = torch.empty((x.shape[0], x.shape[1] // 32), dtype=torch.uint8, device=dev)
+        raise_for(flce_quantize_mxfp4(DTYPES[_dtype_name(x)], _ptr(x), x.shape[0], x.shape[1], _ptr(q), _ptr(scale),
+                                      stream_handle(dev)), "flce_quantize_mxfp4")
+    return q, scale
+
+
+def quantize_mxfp4(x):
+    """Rows of x (R, H) in MXFP4: (codes uint8 (R, H / 2), two to a byte, the earlier one in the low half; scales uint8
+    (R, H / 32), byte s for 2^(s - 127)).  For a weight (V, H) once, when a scorer is loaded.  H must be a multiple of
+    32, the values that share a scale.  A block with NaN or an infinity gives scale 255, which stands for NaN.
+    Neither output has a gradient: x is a constant here, also where it requires one."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    _dtype_name(x)
+    if x.shape[1] == 0 or x.shape[1] % 32:
+        raise ValueError(f"rows must be a multiple of 32 long, got {x.shape[1]}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if x.device.type != "cuda":
+        raise ValueError(f"x must be on a GPU, not {x.device}")
+    return _quantize_mx(_aligned16(x.detach()))
+
+
+def _check_mx(name, q, scale):
+    import torch
+    if q.dim() != 2 or scale.dim() != 2:
+        raise ValueError(f"{name} and {name}_scale must be 2-D, got {tuple(q.shape)} and {tuple(scale.shape)}")
+    for what, t in ((name, q), (f"{name}_scale", scale)):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{what} must be uint8 (quantize_mxfp4), not {t.dtype}")
+    if q.shape[1] == 0 or q.shape[1] % 16:
+        raise ValueError(f"rows of {name} must be a multiple of 16 bytes (32 values) long, got {q.shape[1]}")
+    if tuple(scale.shape) != (q.shape[0], q.shape[1] // 16):
+        raise ValueError(f"{name}_scale must have shape {(q.shape[0], q.shape[1] // 16)}, got {tuple(scale.shape)}")
+
+
+def dequantize_mxfp4(q, scale, dtype=None):
+    """The values (R, H) that ``quantize_mxfp4``'s codes and scales stand for, in ``dtype`` (float32, the default,
+    bfloat16 or float16; rounded where it does not hold them)."""
+    import torch
+    _check_mx("q", q, scale)
+    dtype = torch.float32 if dtype is None else dtype
+    if dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise TypeError(f"unsupported dtype {dtype}")
+    for name, t in (("q", q), ("scale", scale)):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t in (("q", q), ("scale", scale)):
+        if t.device.type != "cuda" or t.device != q.device:
+            raise ValueError(f"{name} must be on q's GPU ({q.device}), not {t.device}")
+    dev, q = q.device, _aligned16(q)
+    with on_device(dev):
+        x = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=dtype, device=dev)
+        raise_for(flce_dequantize_mxfp4(DTYPES[_dtype_name(x)], _ptr(q), _ptr(scale), x.shape[0], x.shape[1], _ptr(x),
+                                        stream_handle(dev)), "flce_dequantize_mxfp4")
+    return x
+
+
+def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
+                         logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
+                         return_entropy: bool = False):
+    """``token_logprobs`` of a frozen head held in MXFP4: weight uint8 (V, H / 2) and weight_scale uint8 (V, H / 32),
+    from ``quantize_mxfp4``.  hidden (N, H) is fp32, bf16 or fp16 and is quantized here, or is uint8 codes (N, H / 2)
+    with their ``hidden_scale`` (N, H / 32).  Products are exact and summed in fp32.  bias (V,) is fp32.  Vocabulary
+    slices are taken (``weight[first:]``, ``weight_scale[first:]``).  No gradients."""
+    import torch
+    _check_mx("weight", weight, weight_scale)
+    v, h = weight.shape[0], 2 * weight.shape[1]
+    if hidden_scale is not None:
+        _check_mx("hidden", hidden, hidden_scale)
+    else:
+        if hidden.dim() != 2:
+            raise ValueError(f"hidden must be 2-D, got {tuple(hidden.shape)}")
+        _dtype_name(hidden)
+    n, cols = hidden.shape[0], hidden.shape[1] * (1 if hidden_scale is None else 2)
+    if cols != h:
+        raise ValueError(f"weight has {h} columns, hidden has {cols}")
+    _targets_int32(targets)
+    if targets.dim() != 1 or targets.shape[0] != n:
+        raise ValueError(f"targets must have shape ({n},), got {tuple(targets.shape)}")
+    if bias is not None:
+        if bias.dtype != torch.float32:
+            raise TypeError(f"bias must be float32, not {bias.dtype}")
+        if bias.dim() != 1 or bias.shape[0] != v:
+            raise ValueError(f"bias must have shape ({v},), got {tuple(bias.shape)}")
+    named = [("hidden", hidden), ("weight", weight), ("targets", targets), ("weight_scale", weight_scale),
+             ("bias", bias), ("hidden_scale", hidden_scale)]
+    for name, t in named:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t in named:
+        if t is not None and (t.device.type != "cuda" or t.device != hidden.device):
+            raise ValueError(f"{name} must be on hidden's GPU ({hidden.device}), not {t.device}")
+    recorded = torch.is_grad_enabled()
+    for name, t in named:
+        if t is not None and ((recorded and t.requires_grad) or has_tangent(t)):
+            raise ValueError(f"4-bit scores have no gradient: detach {name}, or use token_logprobs")
+    p = make_params(n, h, v, logit_scale=logit_scale, softcap=softcap, ignore_index=ignore_index, reduction="none",
+                    targets_int32=_targets_int32(targets))
+    dev = hidden.device
+    with on_device(dev):
+        ws_bytes = flce_logprobs_mxfp4_workspace_size(p)
+        hidden, weight, weight_scale, bias, hidden_scale = map(_aligned16,
+                                                               (hidden, weight, weight_scale, bias, hidden_scale))
+        if hidden_scale is None:
+            hidden, hidden_scale = _quantize_mx(hidden)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        logps, entropy, lse = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(3))
+        raise_for(flce_logprobs_mxfp4(p, _ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale), _ptr(bias),
+                                      _ptr(targets), _ptr(logps), _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes,
+                                      stream_handle(dev)), "flce_logprobs_mxfp4")
     return (logps, entropy) if return_entropy else logps
