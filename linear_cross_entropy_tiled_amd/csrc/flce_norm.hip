@@ -7,6 +7,11 @@
 //   dweight = sum over rows of dy xhat,  dbias = sum over rows of dy.
 // Everything is formed in fp32 and rounded once to the output's type.  The variance is the
 // mean of the squared distances from the mean, not a difference of two large numbers.
+//
+// Rows of up to 16384 values stay in registers between the passes over them: 8 or 16
+// columns a thread, 64, 256 or 1024 threads a row, and a workgroup takes row after row with
+// the weight (backward: and the column sums) in registers too, loading the next row while
+// it works on one.  Every value is read once and written once.
 #include "flce_device.h"
 #include "flce_norm.h"
 
@@ -27,7 +32,10 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
   return v;
 }
 
-// One workgroup a row, any length; the passes after the first read the row from cache.
+// ---------------------------------------------------------------------------
+// Rows of any length (beyond 16384): one workgroup a row; the passes after the first
+// read the row from cache.
+// ---------------------------------------------------------------------------
 template <typename T, typename P> __global__ __launch_bounds__(256) void norm_fwd_any_kernel(NormArgs a) {
   __shared__ float lds[4];
   const float inv = 1.0f / (float)a.cols;
@@ -115,36 +123,275 @@ template <typename P> __global__ __launch_bounds__(1024) void norm_parts_kernel(
   static_cast<P*>(out)[c] = (P)s;
 }
 
-int norm_parts(int64_t rows, int64_t) {
-  const int64_t n = (rows + 31) / 32;   // 8 rows to a thread at least
-  return (int)(n < 1 ? 1 : (n > 256 ? 256 : n));
+// ---------------------------------------------------------------------------
+// Rows in registers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float param_at(const void* p, int dtype, int i, float none) {
+  if (!p) return none;
+  if (dtype == FLCE_F32) return static_cast<const float*>(p)[i];
+  return dtype == FLCE_BF16 ? (float)static_cast<const bf16*>(p)[i] : (float)static_cast<const f16*>(p)[i];
 }
 
-template <typename T, typename P> static void norm_forward_t(const NormArgs& a, hipStream_t st) {
-  if (a.rows == 0) return;
-  const unsigned wgs = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
-  norm_fwd_any_kernel<T, P><<<wgs, 256, 0, st>>>(a);
-}
+// A thread's columns of a row: CPT of them in pieces of VEC, TPR threads a row.
+template <typename T, int VEC, int CPT, int TPR> struct RowPart {
+  static constexpr int NV = CPT / VEC;
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  V v[NV];
+  __device__ __forceinline__ static int col(int k, int t) { return (k * TPR + t) * VEC; }
+  __device__ __forceinline__ void load(const T* row, int t, int cols) {
+#pragma unroll
+    for (int k = 0; k < NV; k++) {
+      if (col(k, t) < cols) {
+        v[k] = *reinterpret_cast<const V*>(row + col(k, t));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) v[k][j] = (T)0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int t, int cols) const {
+#pragma unroll
+    for (int k = 0; k < NV; k++)
+      if (col(k, t) < cols) *reinterpret_cast<V*>(row + col(k, t)) = v[k];
+  }
+  __device__ __forceinline__ float get(int c) const { return (float)v[c / VEC][c % VEC]; }
+  __device__ __forceinline__ void set(int c, float x) { v[c / VEC][c % VEC] = (T)x; }
+};
 
-template <typename T, typename P> static void norm_backward_t(const NormArgs& a, hipStream_t st) {
-  const unsigned wgs = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
-  if (a.rows > 0 && a.dx) norm_dx_any_kernel<T, P><<<wgs, 256, 0, st>>>(a);
-  if (a.dw || a.db) {
-    const unsigned n = (unsigned)((a.cols + 63) / 64);
-    norm_columns_any_kernel<T><<<dim3(n, (unsigned)a.parts), 256, 0, st>>>(a);
-    norm_parts_kernel<P><<<dim3(n, 2), 1024, 0, st>>>(a);
+// Sums of two values over the TPR threads of a row, on each of them.  lds: [2][ROWS][TPR / 64][2]; the caller
+// alternates `slot`, so that one barrier a call is enough.
+template <int TPR, int ROWS>
+__device__ __forceinline__ void row_sums(float& a, float& b, float* lds, int slot, int rg, int t) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    a += __shfl_xor(a, o);
+    b += __shfl_xor(b, o);
+  }
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    float* at = lds + (slot * ROWS + rg) * W * 2;
+    if ((t & 63) == 0) {
+      at[2 * (t >> 6)] = a;
+      at[2 * (t >> 6) + 1] = b;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+      a += at[2 * w];
+      b += at[2 * w + 1];
+    }
   }
 }
 
+template <typename T, int VEC, int CPT, int TPR, int ROWS>
+__global__ __launch_bounds__(TPR * ROWS) void norm_fwd_kernel(NormArgs a) {
+  typedef RowPart<T, VEC, CPT, TPR> Part;
+  __shared__ float lds[TPR > 64 ? 4 * ROWS * (TPR / 64) : 1];
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  const float inv = 1.0f / (float)a.cols;
+  float w[CPT], b[CPT];
+#pragma unroll
+  for (int c = 0; c < CPT; c++) {
+    const int at = Part::col(c / VEC, t) + c % VEC;
+    w[c] = at < a.cols ? param_at(a.weight, a.param_dtype, at, 1.0f) : 0.0f;
+    b[c] = at < a.cols ? param_at(a.bias, a.param_dtype, at, 0.0f) : 0.0f;
+  }
+  const int64_t groups = (a.rows + ROWS - 1) / ROWS;
+  Part next;
+  next.load(static_cast<const T*>(a.x) + min((int64_t)blockIdx.x * ROWS + rg, a.rows - 1) * a.ld_x, t, a.cols);
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int64_t r = g * ROWS + rg;
+    Part x = next;
+    if (g + gridDim.x < groups)
+      next.load(static_cast<const T*>(a.x) + min(r + (int64_t)gridDim.x * ROWS, a.rows - 1) * a.ld_x, t, a.cols);
+    float s = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CPT; c++) s += x.get(c);
+    row_sums<TPR, ROWS>(s, q, lds, 0, rg, t);
+    const float mean = s * inv;
+    float d[CPT];
+    s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CPT; c++) {
+      d[c] = Part::col(c / VEC, t) < a.cols ? x.get(c) - mean : 0.0f;
+      s = fmaf(d[c], d[c], s);
+    }
+    row_sums<TPR, ROWS>(s, q, lds, 1, rg, t);
+    const float rstd = 1.0f / sqrtf(fmaf(s, inv, a.eps));
+#pragma unroll
+    for (int c = 0; c < CPT; c++) x.set(c, fmaf(d[c] * rstd, w[c], b[c]));
+    if (r < a.rows) {
+      x.store(static_cast<T*>(a.y) + r * a.cols, t, a.cols);
+      if (a.mean && t == 0) {
+        a.mean[r] = mean;
+        a.rstd[r] = rstd;
+      }
+    }
+  }
+}
+
+// Workgroup g takes the row groups g, g + gridDim.x, ...; its column sums are part g.
+template <typename T, int VEC, int CPT, int TPR, int ROWS>
+__global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormArgs a) {
+  typedef RowPart<T, VEC, CPT, TPR> Part;
+  __shared__ float lds[TPR > 64 ? 4 * ROWS * (TPR / 64) : 1];
+  __shared__ float cs[ROWS > 1 ? TPR * CPT : 1];
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  const float inv = 1.0f / (float)a.cols;
+  float w[CPT], sw[CPT], sb[CPT];
+#pragma unroll
+  for (int c = 0; c < CPT; c++) {
+    const int at = Part::col(c / VEC, t) + c % VEC;
+    w[c] = at < a.cols ? param_at(a.weight, a.param_dtype, at, 1.0f) : 0.0f;
+    sw[c] = sb[c] = 0.0f;
+  }
+  const int64_t groups = (a.rows + ROWS - 1) / ROWS;
+  Part xn, gn;
+  float mean_n = 0.0f, rstd_n = 0.0f;
+  auto load = [&](int64_t r) {
+    r = min(r, a.rows - 1);
+    xn.load(static_cast<const T*>(a.x) + r * a.ld_x, t, a.cols);
+    gn.load(static_cast<const T*>(a.dy) + r * a.ld_dy, t, a.cols);
+    mean_n = a.mean[r];
+    rstd_n = a.rstd[r];
+  };
+  if (a.rows > 0) load((int64_t)blockIdx.x * ROWS + rg);
+  int slot = 0;
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x, slot ^= 1) {
+    const int64_t r = g * ROWS + rg;
+    const bool here = r < a.rows;
+    Part x = xn, dy = gn;
+    const float mean = mean_n, rstd = rstd_n;
+    if (g + gridDim.x < groups) load(r + (int64_t)gridDim.x * ROWS);
+    float s1 = 0.0f, s2 = 0.0f;
+    float xh[CPT];
+#pragma unroll
+    for (int c = 0; c < CPT; c++) {
+      const bool in = Part::col(c / VEC, t) < a.cols;
+      const float gy = dy.get(c);
+      xh[c] = in ? (x.get(c) - mean) * rstd : 0.0f;
+      const float d = gy * w[c];
+      s1 += d;
+      s2 = fmaf(d, xh[c], s2);
+      sw[c] += here ? gy * xh[c] : 0.0f;
+      sb[c] += here ? gy : 0.0f;
+    }
+    if (a.dx) {
+      row_sums<TPR, ROWS>(s1, s2, lds, slot, rg, t);
+      s1 *= inv;
+      s2 *= inv;
+#pragma unroll
+      for (int c = 0; c < CPT; c++) x.set(c, rstd * (dy.get(c) * w[c] - fmaf(xh[c], s2, s1)));
+      if (here) x.store(static_cast<T*>(a.dx) + r * a.cols, t, a.cols);
+    }
+  }
+  if (!a.dw && !a.db) return;
+  // the row groups' sums, one after the other
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+  for (int which = 0; which < 2; which++) {
+    float* v = which == 0 ? sw : sb;
+    if constexpr (ROWS > 1) {
+      for (int k = ROWS - 1; k > 0; k--) {
+        __syncthreads();
+        if (rg == k) {
+#pragma unroll
+          for (int c = 0; c < CPT; c++) cs[c * TPR + t] = v[c];
+        }
+        __syncthreads();
+        if (rg == k - 1) {
+#pragma unroll
+          for (int c = 0; c < CPT; c++) v[c] += cs[c * TPR + t];
+        }
+      }
+    }
+    if (rg == 0) {
+#pragma unroll
+      for (int c = 0; c < CPT; c++) {
+        const int at = Part::col(c / VEC, t) + c % VEC;
+        if (at < a.cols) part[(int64_t)which * a.cols + at] = v[c];
+      }
+    }
+  }
+}
+
+constexpr int64_t kRegisterCols = 16384;
+static int threads_per_row(int64_t cols) { return cols <= 1024 ? 64 : (cols <= 4096 ? 256 : 1024); }
+static int rows_at_once(int tpr) { return tpr == 1024 ? 1 : 512 / tpr; }
+
+int norm_parts(int64_t rows, int64_t cols) {
+  if (cols > kRegisterCols) {
+    const int64_t n = (rows + 31) / 32;   // 8 rows to a thread at least
+    return (int)(n < 1 ? 1 : (n > 256 ? 256 : n));
+  }
+  const int tpr = threads_per_row(cols), most = tpr == 1024 ? 256 : 512;
+  const int64_t n = (rows + rows_at_once(tpr) - 1) / rows_at_once(tpr);
+  return (int)(n < 1 ? 1 : (n > most ? most : n));
+}
+
+static size_t element_bytes(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
+static bool rows16(const void* p, int64_t ld, int dtype) {   // rows that begin on 16 bytes
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * element_bytes(dtype)) % 16 == 0;
+}
+
+template <typename T, int VEC, int CPT, int TPR>
+static void norm_rows_t(const NormArgs& a, bool back, hipStream_t st) {
+  if (back) {
+    constexpr int ROWS = TPR == 1024 ? 1 : 512 / TPR;
+    norm_bwd_kernel<T, VEC, CPT, TPR, ROWS><<<a.parts, TPR * ROWS, 0, st>>>(a);
+    return;
+  }
+  constexpr int ROWS = TPR == 1024 ? 1 : 256 / TPR;
+  const int64_t groups = (a.rows + ROWS - 1) / ROWS;
+  norm_fwd_kernel<T, VEC, CPT, TPR, ROWS><<<(unsigned)(groups < 2048 ? groups : 2048), TPR * ROWS, 0, st>>>(a);
+}
+
+template <typename T, int VEC, int CPT> static void norm_rows(const NormArgs& a, bool back, hipStream_t st) {
+  switch (threads_per_row(a.cols)) {
+    case 64: norm_rows_t<T, VEC, CPT, 64>(a, back, st); break;
+    case 256: norm_rows_t<T, VEC, CPT, 256>(a, back, st); break;
+    default: norm_rows_t<T, VEC, CPT, 1024>(a, back, st);
+  }
+}
+
+template <typename T, typename P> static void norm_any(const NormArgs& a, bool back, hipStream_t st) {
+  const unsigned wgs = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
+  if (!back) {
+    norm_fwd_any_kernel<T, P><<<wgs, 256, 0, st>>>(a);
+    return;
+  }
+  if (a.rows > 0 && a.dx) norm_dx_any_kernel<T, P><<<wgs, 256, 0, st>>>(a);
+  if (a.dw || a.db)
+    norm_columns_any_kernel<T><<<dim3((unsigned)((a.cols + 63) / 64), (unsigned)a.parts), 256, 0, st>>>(a);
+}
+
 template <typename T> static void norm_t(const NormArgs& a, bool back, hipStream_t st) {
-  if (a.param_dtype == FLCE_F32) back ? norm_backward_t<T, float>(a, st) : norm_forward_t<T, float>(a, st);
-  else back ? norm_backward_t<T, T>(a, st) : norm_forward_t<T, T>(a, st);
+  if (a.cols > kRegisterCols) {
+    if (a.param_dtype == FLCE_F32) norm_any<T, float>(a, back, st);
+    else norm_any<T, T>(a, back, st);
+    return;
+  }
+  constexpr int kVec = 16 / sizeof(T);
+  const bool vec = rows16(a.x, a.ld_x, a.dtype) && rows16(back ? a.dx : a.y, a.cols, a.dtype) &&
+                   (!back || rows16(a.dy, a.ld_dy, a.dtype));
+  const int tpr = threads_per_row(a.cols);
+  if (!vec) norm_rows<T, 1, 16>(a, back, st);
+  else if (a.cols <= 8 * tpr) norm_rows<T, kVec, 8>(a, back, st);
+  else norm_rows<T, kVec, 16>(a, back, st);
 }
 
 static hipError_t launch_norm(const NormArgs& a, bool back, hipStream_t st) {
+  if (!back && a.rows == 0) return hipSuccess;
   if (a.dtype == FLCE_BF16) norm_t<bf16>(a, back, st);
   else if (a.dtype == FLCE_F16) norm_t<f16>(a, back, st);
   else norm_t<float>(a, back, st);
+  if (back && (a.dw || a.db)) {
+    const dim3 grid((unsigned)((a.cols + 63) / 64), 2);
+    if (a.param_dtype == FLCE_F32) norm_parts_kernel<float><<<grid, 1024, 0, st>>>(a);
+    else if (a.param_dtype == FLCE_BF16) norm_parts_kernel<bf16><<<grid, 1024, 0, st>>>(a);
+    else norm_parts_kernel<f16><<<grid, 1024, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t st) { return launch_norm(a, false, st); }
