@@ -9,7 +9,7 @@
 // mean of the squared distances from the mean, not a difference of two large numbers.
 //
 // Rows of up to 16384 values stay in registers between the passes over them: 8 or 16
-// columns a thread, 64, 256 or 1024 threads a row, and a workgroup takes row after row with
+// columns a thread, 64 to 1024 threads a row, and a workgroup takes row after row with
 // the weight (backward: and the column sums) in registers too, loading the next row while
 // it works on one.  Every value is read once and written once.
 #include "flce_device.h"
@@ -112,8 +112,16 @@ template <typename P> __global__ __launch_bounds__(1024) void norm_parts_kernel(
   if (!out) return;
   const int tid = threadIdx.x, sub = tid >> 6, c = (int)blockIdx.x * 64 + (tid & 63);
   float s = 0.0f;
-  if (c < a.cols)
-    for (int p = sub; p < a.parts; p += 16) s += a.part[((int64_t)p * 2 + blockIdx.y) * a.cols + c];
+  if (c < a.cols) {
+    for (int p = sub; p < a.parts; p += 8 * 16) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++)   // eight in flight; past the last one it again, not added
+        v[k] = a.part[((int64_t)min(p + 16 * k, a.parts - 1) * 2 + blockIdx.y) * a.cols + c];
+#pragma unroll
+      for (int k = 0; k < 8; k++) s += p + 16 * k < a.parts ? v[k] : 0.0f;
+    }
+  }
   lds[sub][tid & 63] = s;
   __syncthreads();
   if (sub != 0 || c >= a.cols) return;
@@ -126,10 +134,24 @@ template <typename P> __global__ __launch_bounds__(1024) void norm_parts_kernel(
 // ---------------------------------------------------------------------------
 // Rows in registers
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float param_at(const void* p, int dtype, int i, float none) {
-  if (!p) return none;
-  if (dtype == FLCE_F32) return static_cast<const float*>(p)[i];
-  return dtype == FLCE_BF16 ? (float)static_cast<const bf16*>(p)[i] : (float)static_cast<const f16*>(p)[i];
+// VEC neighbouring values of a parameter vector of T or fp32, in pieces of up to 16 bytes (to which it is aligned).
+template <typename P, int VEC> __device__ __forceinline__ void param_piece(const P* p, float* out) {
+  constexpr int kMost = 16 / sizeof(P), kPiece = VEC < kMost ? VEC : kMost;
+  typedef P V __attribute__((ext_vector_type(kPiece)));
+#pragma unroll
+  for (int k = 0; k < VEC; k += kPiece) {
+    const V v = *reinterpret_cast<const V*>(p + k);
+#pragma unroll
+    for (int j = 0; j < kPiece; j++) out[k + j] = (float)v[j];
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void param_at(const void* p, int dtype, int i, bool in, float none, float* out) {
+#pragma unroll
+  for (int j = 0; j < VEC; j++) out[j] = in ? none : 0.0f;
+  if (!p || !in) return;
+  if (dtype == FLCE_F32) param_piece<float, VEC>(static_cast<const float*>(p) + i, out);
+  else param_piece<T, VEC>(static_cast<const T*>(p) + i, out);
 }
 
 // A thread's columns of a row: CPT of them in pieces of VEC, TPR threads a row.
@@ -192,10 +214,10 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_fwd_kernel(NormArgs a) {
   const float inv = 1.0f / (float)a.cols;
   float w[CPT], b[CPT];
 #pragma unroll
-  for (int c = 0; c < CPT; c++) {
-    const int at = Part::col(c / VEC, t) + c % VEC;
-    w[c] = at < a.cols ? param_at(a.weight, a.param_dtype, at, 1.0f) : 0.0f;
-    b[c] = at < a.cols ? param_at(a.bias, a.param_dtype, at, 0.0f) : 0.0f;
+  for (int k = 0; k < Part::NV; k++) {
+    const int at = Part::col(k, t);
+    param_at<T, VEC>(a.weight, a.param_dtype, at, at < a.cols, 1.0f, w + k * VEC);
+    param_at<T, VEC>(a.bias, a.param_dtype, at, at < a.cols, 0.0f, b + k * VEC);
   }
   const int64_t groups = (a.rows + ROWS - 1) / ROWS;
   Part next;
@@ -241,11 +263,12 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormArgs a) {
   const float inv = 1.0f / (float)a.cols;
   float w[CPT], sw[CPT], sb[CPT];
 #pragma unroll
-  for (int c = 0; c < CPT; c++) {
-    const int at = Part::col(c / VEC, t) + c % VEC;
-    w[c] = at < a.cols ? param_at(a.weight, a.param_dtype, at, 1.0f) : 0.0f;
-    sw[c] = sb[c] = 0.0f;
+  for (int k = 0; k < Part::NV; k++) {
+    const int at = Part::col(k, t);
+    param_at<T, VEC>(a.weight, a.param_dtype, at, at < a.cols, 1.0f, w + k * VEC);
   }
+#pragma unroll
+  for (int c = 0; c < CPT; c++) sw[c] = sb[c] = 0.0f;
   const int64_t groups = (a.rows + ROWS - 1) / ROWS;
   Part xn, gn;
   float mean_n = 0.0f, rstd_n = 0.0f;
@@ -265,24 +288,22 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormArgs a) {
     const float mean = mean_n, rstd = rstd_n;
     if (g + gridDim.x < groups) load(r + (int64_t)gridDim.x * ROWS);
     float s1 = 0.0f, s2 = 0.0f;
-    float xh[CPT];
 #pragma unroll
     for (int c = 0; c < CPT; c++) {
-      const bool in = Part::col(c / VEC, t) < a.cols;
-      const float gy = dy.get(c);
-      xh[c] = in ? (x.get(c) - mean) * rstd : 0.0f;
-      const float d = gy * w[c];
+      const float gy = here ? dy.get(c) : 0.0f, xh = here ? (x.get(c) - mean) * rstd : 0.0f;
+      const float d = gy * w[c];   // 0 past the row's end, where dy and w are
       s1 += d;
-      s2 = fmaf(d, xh[c], s2);
-      sw[c] += here ? gy * xh[c] : 0.0f;
-      sb[c] += here ? gy : 0.0f;
+      s2 = fmaf(d, xh, s2);
+      sw[c] = fmaf(gy, xh, sw[c]);
+      sb[c] += gy;
     }
     if (a.dx) {
       row_sums<TPR, ROWS>(s1, s2, lds, slot, rg, t);
       s1 *= inv;
       s2 *= inv;
 #pragma unroll
-      for (int c = 0; c < CPT; c++) x.set(c, rstd * (dy.get(c) * w[c] - fmaf(xh[c], s2, s1)));
+      for (int c = 0; c < CPT; c++)
+        x.set(c, rstd * (dy.get(c) * w[c] - fmaf((x.get(c) - mean) * rstd, s2, s1)));
       if (here) x.store(static_cast<T*>(a.dx) + r * a.cols, t, a.cols);
     }
   }
@@ -317,8 +338,12 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormArgs a) {
 }
 
 constexpr int64_t kRegisterCols = 16384;
-static int threads_per_row(int64_t cols) { return cols <= 1024 ? 64 : (cols <= 4096 ? 256 : 1024); }
-static int rows_at_once(int tpr) { return tpr == 1024 ? 1 : 512 / tpr; }
+static int threads_per_row(int64_t cols) {   // 8 columns each, 16 beyond 8192
+  int n = 64;
+  while (n < 1024 && 8 * n < cols) n *= 2;
+  return n;
+}
+static constexpr int rows_at_once(int tpr) { return tpr >= 512 ? 1 : 512 / tpr; }   // backward
 
 int norm_parts(int64_t rows, int64_t cols) {
   if (cols > kRegisterCols) {
@@ -338,20 +363,24 @@ static bool rows16(const void* p, int64_t ld, int dtype) {   // rows that begin 
 template <typename T, int VEC, int CPT, int TPR>
 static void norm_rows_t(const NormArgs& a, bool back, hipStream_t st) {
   if (back) {
-    constexpr int ROWS = TPR == 1024 ? 1 : 512 / TPR;
+    constexpr int ROWS = rows_at_once(TPR);
     norm_bwd_kernel<T, VEC, CPT, TPR, ROWS><<<a.parts, TPR * ROWS, 0, st>>>(a);
     return;
   }
-  constexpr int ROWS = TPR == 1024 ? 1 : 256 / TPR;
+  constexpr int ROWS = TPR >= 256 ? 1 : 256 / TPR;
   const int64_t groups = (a.rows + ROWS - 1) / ROWS;
   norm_fwd_kernel<T, VEC, CPT, TPR, ROWS><<<(unsigned)(groups < 2048 ? groups : 2048), TPR * ROWS, 0, st>>>(a);
 }
 
-template <typename T, int VEC, int CPT> static void norm_rows(const NormArgs& a, bool back, hipStream_t st) {
+template <typename T, int VEC> static void norm_rows(const NormArgs& a, bool back, hipStream_t st) {
   switch (threads_per_row(a.cols)) {
-    case 64: norm_rows_t<T, VEC, CPT, 64>(a, back, st); break;
-    case 256: norm_rows_t<T, VEC, CPT, 256>(a, back, st); break;
-    default: norm_rows_t<T, VEC, CPT, 1024>(a, back, st);
+    case 64: norm_rows_t<T, VEC, 8, 64>(a, back, st); break;
+    case 128: norm_rows_t<T, VEC, 8, 128>(a, back, st); break;
+    case 256: norm_rows_t<T, VEC, 8, 256>(a, back, st); break;
+    case 512: norm_rows_t<T, VEC, 8, 512>(a, back, st); break;
+    default:
+      if (a.cols <= 8192) norm_rows_t<T, VEC, 8, 1024>(a, back, st);
+      else norm_rows_t<T, VEC, 16, 1024>(a, back, st);
   }
 }
 
@@ -374,11 +403,10 @@ template <typename T> static void norm_t(const NormArgs& a, bool back, hipStream
   }
   constexpr int kVec = 16 / sizeof(T);
   const bool vec = rows16(a.x, a.ld_x, a.dtype) && rows16(back ? a.dx : a.y, a.cols, a.dtype) &&
-                   (!back || rows16(a.dy, a.ld_dy, a.dtype));
-  const int tpr = threads_per_row(a.cols);
-  if (!vec) norm_rows<T, 1, 16>(a, back, st);
-  else if (a.cols <= 8 * tpr) norm_rows<T, kVec, 8>(a, back, st);
-  else norm_rows<T, kVec, 16>(a, back, st);
+                   (!back || rows16(a.dy, a.ld_dy, a.dtype)) && rows16(a.weight, 0, a.dtype) &&
+                   rows16(a.bias, 0, a.dtype);
+  if (vec) norm_rows<T, kVec>(a, back, st);
+  else norm_rows<T, 1>(a, back, st);
 }
 
 static hipError_t launch_norm(const NormArgs& a, bool back, hipStream_t st) {
