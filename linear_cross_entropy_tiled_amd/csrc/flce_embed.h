@@ -9,8 +9,9 @@
 
 namespace flce {
 
-constexpr int kSortItems = 8192;     // ids a workgroup sorts: 16 waves, 8 each of their 64 lanes
-constexpr int kSortBits = 8;         // of a pass
+constexpr int kSortItems = 8192;     // ids of a workgroup of a pass: 16 waves, 8 each of their 64 lanes
+constexpr int kSortAlone = 16384;    // ids that one workgroup sorts by itself
+constexpr int kSortBits = 9;         // of a pass: two for a vocabulary below 2^18
 constexpr int kSortBins = 1 << kSortBits;
 
 struct EmbedPlan {

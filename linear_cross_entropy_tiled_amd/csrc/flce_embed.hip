@@ -52,12 +52,44 @@ template <typename T, int VEC> __global__ __launch_bounds__(256) void embed_fwd_
 }
 
 // ---------------------------------------------------------------------------
-// Stable radix sort of (id, token), 8 bits a pass: counts by workgroup, an exclusive
-// scan of them in the order (digit, workgroup), then every item to its place.
+// Zeros for the rows that do not occur.  They are most of the gradient's bytes, and need
+// nothing of the sort: they are written by further workgroups of the sort's own launches,
+// a share by each, while its few workgroups wait on memory and on each other.  (Rows that
+// occur are written twice, at most as many as there are tokens.)
+// ---------------------------------------------------------------------------
+struct ZeroArgs {
+  char* to;                // NULL: nothing to write
+  int64_t from, until;     // this launch's bytes, in whole pieces of kZeroPiece but for the end
+  int first;               // the launch's first workgroup that writes
+};
+constexpr int64_t kZeroPiece = 64 * 1024;
+
+// One workgroup of 1024.
+__device__ __forceinline__ void write_zeros(const ZeroArgs& z, int block) {
+  for (int64_t at = z.from + block * kZeroPiece; at < z.until; at += ((int64_t)gridDim.x - z.first) * kZeroPiece) {
+    const int64_t end = min(at + kZeroPiece, z.until);
+#pragma unroll
+    for (int k = 0; k < kZeroPiece / 16384; k++) {
+      const int64_t i = at + k * 16384 + threadIdx.x * 16;
+      if (i + 16 <= end) *reinterpret_cast<i32x4*>(z.to + i) = i32x4{0, 0, 0, 0};
+      else
+        for (int64_t j = i; j < end; j++) z.to[j] = 0;
+    }
+  }
+}
+// A gradient that is not 16-byte aligned.
+__global__ __launch_bounds__(256) void embed_zero_kernel(uint16_t* gw, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) gw[i] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Stable radix sort of (id, token), kSortBits a pass.
 // ---------------------------------------------------------------------------
 struct SortArgs {
   EmbedArgs e;
+  ZeroArgs z;
   int shift, first;            // bits already sorted; first pass: keys come from the ids
+  int passes;                  // sort_alone_kernel
   const uint32_t* keys;
   const uint32_t* at;
   uint32_t* keys_out;
@@ -70,8 +102,135 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i) {
   return a.first ? row_of(a.e, i) : a.keys[i];
 }
 
+// Ranks `rounds` items a lane by digit within their wave: a wave's items are neighbours (item k of a lane is number
+// 64 k + lane); in a round the lanes with the same digit find each other by ballots, and the first of them counts
+// for all.  bins: the wave's counts, zeroed before, its items by digit after.
+template <int ROUNDS>
+__device__ __forceinline__ void wave_ranks(const uint32_t (&key)[ROUNDS], int shift, int n_here, uint32_t* bins, int lane,
+                                           uint32_t (&rank)[ROUNDS]) {
+#pragma unroll
+  for (int k = 0; k < ROUNDS; k++) {
+    const bool here = k * 64 + lane < n_here;
+    const uint32_t digit = (key[k] >> shift) & (kSortBins - 1);
+    uint64_t same = __ballot(here);
+#pragma unroll
+    for (int b = 0; b < kSortBits; b++) {
+      const bool bit = (digit >> b) & 1;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    const uint64_t below = same & ((uint64_t(1) << lane) - 1);
+    rank[k] = here ? bins[digit] + (uint32_t)__popcll(below) : 0u;
+    wave_lds_sync();
+    if (here && below == 0) bins[digit] += (uint32_t)__popcll(same);
+    wave_lds_sync();
+  }
+}
+
+// Up to kSortAlone tokens: all passes by one workgroup, in LDS (8192 tokens: 69 us as three launches a pass of 8 bits,
+// 10 us here).
+__global__ __launch_bounds__(1024) void sort_alone_kernel(SortArgs a) {
+  constexpr int kRounds = kSortAlone / 1024, kPerWave = kSortAlone / 16;
+  __shared__ uint32_t keys[kSortAlone];
+  __shared__ uint16_t ats[kSortAlone];
+  __shared__ uint32_t bins[16][kSortBins];
+  __shared__ uint32_t totals[8];
+  if ((int)blockIdx.x >= a.z.first) {
+    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = (int)a.e.n;
+  // the items, spread evenly over the waves
+  const int rounds = (n + 1023) / 1024, i0 = wave * rounds * 64, n_here = min(max(n - i0, 0), rounds * 64);
+  uint32_t key[kRounds], at[kRounds], rank[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; k++) {
+    const int i = i0 + k * 64 + lane;
+    key[k] = k * 64 + lane < n_here ? row_of(a.e, i) : 0u;
+    at[k] = (uint32_t)i;
+  }
+  for (int pass = 0; pass < a.passes; pass++) {
+    const int shift = pass * kSortBits;
+    for (int k = tid; k < 16 * kSortBins; k += 1024) bins[k / kSortBins][k % kSortBins] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRounds; k++) {   // (as wave_ranks, up to the rounds there are)
+      if (k >= rounds) break;
+      const bool here = k * 64 + lane < n_here;
+      const uint32_t digit = (key[k] >> shift) & (kSortBins - 1);
+      uint64_t same = __ballot(here);
+#pragma unroll
+      for (int b = 0; b < kSortBits; b++) {
+        const bool bit = (digit >> b) & 1;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+      }
+      const uint64_t below = same & ((uint64_t(1) << lane) - 1);
+      rank[k] = here ? bins[wave][digit] + (uint32_t)__popcll(below) : 0u;
+      wave_lds_sync();
+      if (here && below == 0) bins[wave][digit] += (uint32_t)__popcll(same);
+      wave_lds_sync();
+    }
+    __syncthreads();
+    // exclusive scan in the order (digit, wave): a thread's digit over the waves, then the digits
+    uint32_t sum = 0, x = 0;
+    if (tid < kSortBins) {
+#pragma unroll
+      for (int w = 0; w < 16; w++) {
+        const uint32_t c = bins[w][tid];
+        bins[w][tid] = sum;
+        sum += c;
+      }
+      x = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = __shfl_up(x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 63) totals[wave] = x;
+    }
+    __syncthreads();
+    if (tid < kSortBins) {
+      uint32_t base = x - sum;
+      for (int w = 0; w < wave; w++) base += totals[w];
+#pragma unroll
+      for (int w = 0; w < 16; w++) bins[w][tid] += base;
+    }
+    __syncthreads();
+    const bool last = pass == a.passes - 1;
+#pragma unroll
+    for (int k = 0; k < kRounds; k++) {
+      if (k * 64 + lane >= n_here) continue;
+      const uint32_t to = bins[wave][(key[k] >> shift) & (kSortBins - 1)] + rank[k];
+      if (last) {
+        a.keys_out[to] = key[k];
+        a.at_out[to] = at[k];
+      } else {
+        keys[to] = key[k];
+        ats[to] = (uint16_t)at[k];
+      }
+    }
+    if (last) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRounds; k++) {
+      if (k * 64 + lane >= n_here) continue;
+      key[k] = keys[i0 + k * 64 + lane];
+      at[k] = ats[i0 + k * 64 + lane];
+    }
+    __syncthreads();
+  }
+}
+static_assert(kSortBins == 8 * 64, "the scan's digits are eight waves'");
+
+// More tokens, three launches a pass: counts by workgroup, an exclusive scan of them in
+// the order (digit, workgroup), then every item to its place.
 __global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a) {
   __shared__ uint32_t bins[kSortBins];
+  if ((int)blockIdx.x >= a.z.first) {
+    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    return;
+  }
   const int tid = threadIdx.x;
   if (tid < kSortBins) bins[tid] = 0;
   __syncthreads();
@@ -85,13 +244,18 @@ __global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a) {
   if (tid < kSortBins) a.hist[(int64_t)tid * a.blocks + blockIdx.x] = bins[tid];
 }
 
-// Exclusive scan of n counts in place, one workgroup.
-__global__ __launch_bounds__(1024) void sort_scan_kernel(uint32_t* hist, int64_t n) {
+// In place, one workgroup.
+__global__ __launch_bounds__(1024) void sort_scan_kernel(SortArgs a) {
   __shared__ uint32_t waves[16];
+  if ((int)blockIdx.x >= a.z.first) {
+    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    return;
+  }
+  const int64_t n = (int64_t)kSortBins * a.blocks;
   const int tid = threadIdx.x, lane = tid & 63;
   uint32_t before = 0;
   for (int64_t i0 = 0; i0 < n; i0 += 1024) {
-    const uint32_t own = i0 + tid < n ? hist[i0 + tid] : 0u;
+    const uint32_t own = i0 + tid < n ? a.hist[i0 + tid] : 0u;
     uint32_t x = own;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -106,42 +270,33 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(uint32_t* hist, int64_t
       if (w < tid >> 6) base += waves[w];
       total += waves[w];
     }
-    if (i0 + tid < n) hist[i0 + tid] = base + x - own;
+    if (i0 + tid < n) a.hist[i0 + tid] = base + x - own;
     before += total;
     __syncthreads();
   }
 }
 
 __global__ __launch_bounds__(1024) void sort_place_kernel(SortArgs a) {
+  constexpr int kRounds = kSortItems / 1024;
   __shared__ uint32_t bins[16][kSortBins];
+  if ((int)blockIdx.x >= a.z.first) {
+    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int k = tid; k < 16 * kSortBins; k += 1024) bins[k / kSortBins][k % kSortBins] = 0;
-  __syncthreads();
-  // a wave's items are neighbours; within a round of 64 the lanes with the same digit find
-  // each other by ballots, and the first of them counts for all
-  constexpr int kRounds = kSortItems / 1024;
   const int64_t i0 = (int64_t)blockIdx.x * kSortItems + wave * (kSortItems / 16);
+  const int n_here = (int)min(max(a.e.n - i0, (int64_t)0), (int64_t)kSortItems / 16);
   uint32_t key[kRounds], at[kRounds], rank[kRounds];
 #pragma unroll
   for (int k = 0; k < kRounds; k++) {
     const int64_t i = i0 + k * 64 + lane;
-    const bool here = i < a.e.n;
+    const bool here = k * 64 + lane < n_here;
     key[k] = here ? sort_key(a, i) : 0u;
     at[k] = here && !a.first ? a.at[i] : (uint32_t)i;
-    const uint32_t digit = (key[k] >> a.shift) & (kSortBins - 1);
-    uint64_t same = __ballot(here);
-#pragma unroll
-    for (int b = 0; b < kSortBits; b++) {
-      const bool bit = (digit >> b) & 1;
-      const uint64_t m = __ballot(bit);
-      same &= bit ? m : ~m;
-    }
-    const uint64_t below = same & ((uint64_t(1) << lane) - 1);
-    rank[k] = here ? bins[wave][digit] + (uint32_t)__popcll(below) : 0u;
-    wave_lds_sync();
-    if (here && below == 0) bins[wave][digit] += (uint32_t)__popcll(same);
-    wave_lds_sync();
   }
+  __syncthreads();
+  wave_ranks<kRounds>(key, a.shift, n_here, bins[wave], lane, rank);
   __syncthreads();
   if (tid < kSortBins) {
     uint32_t s = a.hist[(int64_t)tid * a.blocks + blockIdx.x];
@@ -155,7 +310,7 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(SortArgs a) {
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kRounds; k++) {
-    if (i0 + k * 64 + lane >= a.e.n) continue;
+    if (k * 64 + lane >= n_here) continue;
     const uint32_t to = bins[wave][(key[k] >> a.shift) & (kSortBins - 1)] + rank[k];
     a.keys_out[to] = key[k];
     a.at_out[to] = at[k];
@@ -179,17 +334,6 @@ struct RunArgs {
                                // last run's sum where that goes on
 };
 
-template <typename O, int VEC> __global__ __launch_bounds__(256) void embed_zero_kernel(O* gw, int64_t n) {
-  typedef O V __attribute__((ext_vector_type(VEC)));
-  const int64_t whole = n / VEC;
-  V z;
-#pragma unroll
-  for (int j = 0; j < VEC; j++) z[j] = (O)0.0f;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < whole; i += (int64_t)gridDim.x * 256)
-    reinterpret_cast<V*>(gw)[i] = z;
-  if (blockIdx.x == 0 && threadIdx.x < n - whole * VEC) gw[whole * VEC + threadIdx.x] = (O)0.0f;
-}
-
 template <typename O, int VEC>
 __device__ __forceinline__ void put_row(const RunArgs& a, uint32_t row, int c, const float (&s)[VEC]) {
   typedef O V __attribute__((ext_vector_type(VEC)));
@@ -206,51 +350,74 @@ __device__ __forceinline__ void put_row(const RunArgs& a, uint32_t row, int c, c
   *to = o;
 }
 
-// One chunk of sorted tokens by 256 VEC columns.
+// One chunk of sorted tokens by 256 VEC columns; the rows of kAhead tokens are in flight at a time.
+constexpr int kAhead = 8;
 template <typename T, typename O, int VEC> __global__ __launch_bounds__(256) void embed_runs_kernel(RunArgs a) {
   typedef T V __attribute__((ext_vector_type(VEC)));
   const int64_t chunk = blockIdx.x, i0 = chunk * a.chunk, i1 = min(i0 + a.chunk, a.n);
   const int c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * VEC;
-  if (c >= a.h) return;
+  uint32_t key = a.keys[i0];
+  if (c >= a.h || key >= a.v) return;
   float s[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; j++) s[j] = 0.0f;
-  uint32_t key = a.keys[i0];
   bool inner = i0 == 0 || a.keys[i0 - 1] != key;   // the run began here
-  for (int64_t i = i0; i < i1; i++) {
-    if (key >= a.v) return;
-    const V g = *reinterpret_cast<const V*>(static_cast<const T*>(a.grad) + (int64_t)a.at[i] * a.h + c);
+  for (int64_t i = i0; i < i1; i += kAhead) {
+    V g[kAhead];
+    uint32_t next[kAhead];
 #pragma unroll
-    for (int j = 0; j < VEC; j++) s[j] += (float)g[j];
-    const uint32_t next = i + 1 < a.n ? a.keys[i + 1] : (uint32_t)a.v;
-    if (next == key && i + 1 < i1) continue;
-    if (inner && next != key) {
-      put_row<O, VEC>(a, key, c, s);
-    } else {
-      float* p = a.part + ((inner ? a.n_chunks : 0) + chunk) * a.h + c;
-#pragma unroll
-      for (int j = 0; j < VEC; j++) p[j] = s[j];
+    for (int k = 0; k < kAhead; k++) {
+      const int64_t at = min(i + k, i1 - 1);   // past the chunk's end its last token again, not added
+      next[k] = at + 1 < a.n ? a.keys[at + 1] : (uint32_t)a.v;
+      g[k] = *reinterpret_cast<const V*>(static_cast<const T*>(a.grad) + (int64_t)a.at[at] * a.h + c);
     }
 #pragma unroll
-    for (int j = 0; j < VEC; j++) s[j] = 0.0f;
-    key = next;
-    inner = true;
+    for (int k = 0; k < kAhead; k++) {
+      if (i + k >= i1 || key >= a.v) return;
+#pragma unroll
+      for (int j = 0; j < VEC; j++) s[j] += (float)g[k][j];
+      if (next[k] == key && i + k + 1 < i1) continue;
+      if (inner && next[k] != key) {
+        put_row<O, VEC>(a, key, c, s);
+      } else {
+        float* p = a.part + ((inner ? a.n_chunks : 0) + chunk) * a.h + c;
+#pragma unroll
+        for (int j = 0; j < VEC; j++) p[j] = s[j];
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; j++) s[j] = 0.0f;
+      key = next[k];
+      inner = true;
+    }
   }
 }
 
-// Runs that begin in a chunk and end in another.
+// Runs that begin in a chunk and end in another, by 256 columns.
 template <typename O> __global__ __launch_bounds__(256) void embed_join_kernel(RunArgs a) {
   const int64_t chunk = blockIdx.x, i0 = chunk * a.chunk, i1 = i0 + a.chunk;
   if (i1 >= a.n) return;
   const uint32_t key = a.keys[i1 - 1];
   if (key >= a.v || a.keys[i1] != key) return;
   if (i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key) return;   // begun before
+  // the chunks after it that begin with the same key: a lane looks at each
+  const int lane = threadIdx.x & 63;
+  int64_t last = chunk + 1;
+  for (;;) {
+    const int64_t k = last + 1 + lane;
+    const uint64_t goes_on = __ballot(k < a.n_chunks && a.keys[min(k * a.chunk, a.n - 1)] == key);
+    const int more = goes_on == ~uint64_t(0) ? 64 : __ffsll((unsigned long long)~goes_on) - 1;
+    last += more;
+    if (more < 64) break;
+  }
   const int c = (int)blockIdx.y * 256 + (int)threadIdx.x;
   if (c >= a.h) return;
   float s[1] = {a.part[(a.n_chunks + chunk) * a.h + c]};
-  for (int64_t k = chunk + 1; k < a.n_chunks; k++) {
-    s[0] += a.part[k * a.h + c];
-    if ((k + 1) * a.chunk >= a.n || a.keys[(k + 1) * a.chunk] != key) break;
+  for (int64_t k = chunk + 1; k <= last; k += 8) {
+    float p[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) p[j] = a.part[min(k + j, last) * a.h + c];
+#pragma unroll
+    for (int j = 0; j < 8; j++) s[0] += k + j <= last ? p[j] : 0.0f;
   }
   put_row<O, 1>(a, key, c, s);
 }
@@ -261,12 +428,12 @@ void plan_embedding_backward(EmbedPlan* p) {
   int bits = 1;
   while ((p->v >> bits) != 0) bits++;      // of the key v
   p->passes = (bits + kSortBits - 1) / kSortBits;
-  p->sort_blocks = (int)((p->n + kSortItems - 1) / kSortItems);
-  p->chunk = 32;
+  p->sort_blocks = p->n <= kSortAlone ? 0 : (int)((p->n + kSortItems - 1) / kSortItems);
+  p->chunk = p->n <= 16384 ? 16 : 32;
   while (p->chunk < (1 << 20) && p->n / p->chunk > 4096) p->chunk *= 2;
   p->n_chunks = (p->n + p->chunk - 1) / p->chunk;
   size_t o = 0;
-  for (int k = 0; k < 2; k++) {
+  for (int k = 0; k < (p->sort_blocks > 0 ? 2 : 1); k++) {
     p->w_keys[k] = o;
     o += up256(size_t(p->n) * 4);
     p->w_at[k] = o;
@@ -327,13 +494,6 @@ template <typename T, typename O> static void embed_runs_t(const EmbedPlan& p, c
   embed_join_kernel<O><<<dim3((unsigned)p.n_chunks, (unsigned)((p.h + 255) / 256)), 256, 0, st>>>(a);
 }
 
-template <typename O> static void embed_zero_t(const EmbedPlan& p, void* gw, hipStream_t st) {
-  if ((reinterpret_cast<uintptr_t>(gw) & 15) == 0)
-    embed_zero_kernel<O, 16 / sizeof(O)><<<4096, 256, 0, st>>>(static_cast<O*>(gw), p.v * p.h);
-  else
-    embed_zero_kernel<O, 1><<<4096, 256, 0, st>>>(static_cast<O*>(gw), p.v * p.h);
-}
-
 template <typename T> static void embed_runs_o(const EmbedPlan& p, const RunArgs& a, hipStream_t st) {
   if (p.grad_dtype == FLCE_BF16) embed_runs_t<T, bf16>(p, a, st);
   else if (p.grad_dtype == FLCE_F16) embed_runs_t<T, f16>(p, a, st);
@@ -342,28 +502,54 @@ template <typename T> static void embed_runs_o(const EmbedPlan& p, const RunArgs
 
 hipError_t launch_embedding_backward(const EmbedPlan& p, const void* ids, const void* grad, void* grad_weight, char* ws,
                                      hipStream_t st) {
-  if (!p.accumulate) {
-    if (p.grad_dtype == FLCE_BF16) embed_zero_t<bf16>(p, grad_weight, st);
-    else if (p.grad_dtype == FLCE_F16) embed_zero_t<f16>(p, grad_weight, st);
-    else embed_zero_t<float>(p, grad_weight, st);
-  }
-  if (p.n == 0) return hipGetLastError();
   SortArgs s{};
   s.e = embed_args(p, ids);
-  s.hist = reinterpret_cast<uint32_t*>(ws + p.w_hist);
-  s.blocks = p.sort_blocks;
-  int to = 0;
-  for (int k = 0; k < p.passes; k++, to ^= 1) {
-    s.shift = k * kSortBits;
-    s.first = k == 0;
-    s.keys = reinterpret_cast<const uint32_t*>(ws + p.w_keys[to ^ 1]);
-    s.at = reinterpret_cast<const uint32_t*>(ws + p.w_at[to ^ 1]);
-    s.keys_out = reinterpret_cast<uint32_t*>(ws + p.w_keys[to]);
-    s.at_out = reinterpret_cast<uint32_t*>(ws + p.w_at[to]);
-    sort_count_kernel<<<p.sort_blocks, 1024, 0, st>>>(s);
-    sort_scan_kernel<<<1, 1024, 0, st>>>(s.hist, (int64_t)kSortBins * p.sort_blocks);
-    sort_place_kernel<<<p.sort_blocks, 1024, 0, st>>>(s);
+  const int64_t bytes = p.v * p.h * (int64_t)bytes_of(p.grad_dtype);
+  const bool zeros = !p.accumulate && (reinterpret_cast<uintptr_t>(grad_weight) & 15) == 0;
+  if (!p.accumulate && !zeros)
+    embed_zero_kernel<<<4096, 256, 0, st>>>(static_cast<uint16_t*>(grad_weight), bytes / 2);
+  // the launches' shares of the zeros
+  const bool alone = p.sort_blocks == 0;
+  const int launches = alone ? 1 : 3 * p.passes;
+  const int64_t pieces = zeros ? (bytes + kZeroPiece - 1) / kZeroPiece : 0;
+  int done = 0;
+  auto blocks_with_zeros = [&](int sorting) {
+    const int64_t from = pieces * done / launches, until = pieces * (done + 1) / launches;
+    done++;
+    s.z.to = static_cast<char*>(grad_weight);
+    s.z.from = from * kZeroPiece;
+    s.z.until = until * kZeroPiece < bytes ? until * kZeroPiece : bytes;
+    s.z.first = sorting;
+    const int64_t n = until - from;
+    return (unsigned)(sorting + (n < 65536 ? n : 65536));
+  };
+  s.passes = p.passes;
+  if (alone) {
+    s.first = 1;
+    s.keys_out = reinterpret_cast<uint32_t*>(ws + p.w_keys[0]);
+    s.at_out = reinterpret_cast<uint32_t*>(ws + p.w_at[0]);
+    const unsigned blocks = blocks_with_zeros(p.n > 0 ? 1 : 0);
+    if (blocks > 0) sort_alone_kernel<<<blocks, 1024, 0, st>>>(s);
+  } else {
+    s.hist = reinterpret_cast<uint32_t*>(ws + p.w_hist);
+    s.blocks = p.sort_blocks;
+    int to = 0;
+    for (int k = 0; k < p.passes; k++, to ^= 1) {
+      s.shift = k * kSortBits;
+      s.first = k == 0;
+      s.keys = reinterpret_cast<const uint32_t*>(ws + p.w_keys[to ^ 1]);
+      s.at = reinterpret_cast<const uint32_t*>(ws + p.w_at[to ^ 1]);
+      s.keys_out = reinterpret_cast<uint32_t*>(ws + p.w_keys[to]);
+      s.at_out = reinterpret_cast<uint32_t*>(ws + p.w_at[to]);
+      unsigned blocks = blocks_with_zeros(p.sort_blocks);
+      sort_count_kernel<<<blocks, 1024, 0, st>>>(s);
+      blocks = blocks_with_zeros(1);
+      sort_scan_kernel<<<blocks, 1024, 0, st>>>(s);
+      blocks = blocks_with_zeros(p.sort_blocks);
+      sort_place_kernel<<<blocks, 1024, 0, st>>>(s);
+    }
   }
+  if (p.n == 0) return hipGetLastError();
   RunArgs a{};
   a.keys = s.keys_out;
   a.at = s.at_out;
