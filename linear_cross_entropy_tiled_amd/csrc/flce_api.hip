@@ -329,7 +329,7 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   const int64_t n64 = (P.N + 63) / 64, h64 = (P.H + 63) / 64;
   const int64_t wg_target = 3 * kTargetWorkgroups;   // small workgroups that share the chip
   L.bn = P.N <= 16 ? 16 : 64;
-  L.vt_large = P.N <= 16 || P.mx ? 0 : (int)large_vocab_tiles(P, P.V);
+  L.vt_large = P.N <= 16 ? 0 : (int)large_vocab_tiles(P, P.V);
   if (L.vt_large > 0) L.S_large = forward_splits(P.n_tt, L.vt_large);
   const int64_t rest = P.V - int64_t(L.vt_large) * 256;
   if (rest > 0) {
@@ -357,6 +357,12 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
       L.f_hmx = L.f_bytes;
       L.f_wmx = align_up(L.f_hmx + size_t(P.N) * L.ld_mx, 256);
       L.f_bytes = align_up(L.f_wmx + size_t(P.V) * L.ld_mx, 256);
+    }
+    if (L.vt_large > 0) {
+      const size_t tile = size_t((P.H + 127) / 128) * 2048;   // kMxStage bytes a stage
+      L.f_tmx_w = L.f_bytes;
+      L.f_tmx_h = L.f_tmx_w + L.vt_large * tile;
+      L.f_bytes = L.f_tmx_h + P.n_tt * tile;
     }
   }
 

@@ -16,6 +16,7 @@ struct LpPlan {
   // MXFP4 scale rows of a length that is no multiple of 4 are copied to rows of ld_mx
   int ld_mx;
   size_t f_hmx, f_wmx;
+  size_t f_tmx_w, f_tmx_h;    // scales in the large tiles' order
   size_t f_bytes;
 
   // Up to 64 tokens in 16 bits: the logit gradient is held as the sum of two 16-bit
@@ -48,6 +49,8 @@ struct LpTileArgs {
   const uint8_t* hidden_mx;   // MXFP4: scale bytes, rows of ld_hmx (a multiple of 4)
   const uint8_t* weight_mx;
   uint32_t ld_hmx, ld_wmx;
+  const uint8_t* hidden_tmx;  // the same in the large tiles' order (launch_tile_scales)
+  const uint8_t* weight_tmx;
   const void* targets;
   int tgt_i32;
   int N, H, V;                // H: elements of a row, of MXFP4 its bytes

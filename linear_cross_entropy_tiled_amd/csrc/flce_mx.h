@@ -24,5 +24,14 @@ hipError_t launch_dequantize_mx(int dtype, const uint8_t* q, const uint8_t* scal
                                 hipStream_t st);
 // Scale rows of `cols` bytes to rows of `ld` bytes, a multiple of 4.
 hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int ld, uint8_t* out, hipStream_t st);
+// Scales (rows of ld bytes, a multiple of 4; 0 past the last row and block) in the order of the 256 x 256 loop, for
+// `tiles` tiles of 256 rows each, stages of 256 values: the weight's and the hidden states', one launch.
+struct MxTiles {
+  const uint8_t* scale;
+  int64_t rows;
+  int tiles;
+  uint8_t* out;
+};
+hipError_t launch_tile_scales(const MxTiles& a, const MxTiles& b, int ld, int stages, hipStream_t st);
 
 }  // namespace flce

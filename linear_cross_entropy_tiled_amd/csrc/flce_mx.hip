@@ -109,4 +109,46 @@ hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int l
   return hipGetLastError();
 }
 
+// 64 rows by 16 stages (128 blocks) a workgroup, through LDS: bytes of four rows become a word.
+struct MxTileArgs {
+  MxTiles t[2];
+  int ld, stages, chunks;   // chunks of 16 stages
+};
+__global__ __launch_bounds__(256) void mx_tile_kernel(MxTileArgs a) {
+  __shared__ uint32_t lds[64][33];
+  const int per_first = a.t[0].tiles * 4 * a.chunks;
+  const int which = (int)blockIdx.x >= per_first, id = (int)blockIdx.x - (which ? per_first : 0);
+  const MxTiles t = a.t[which];
+  const int chunk = id % a.chunks, unit = id / a.chunks;   // unit: 64 rows
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const int i = k * 256 + tid, r = i >> 5, c = (i & 31) * 4 + chunk * 128;
+    const int64_t row = (int64_t)unit * 64 + r;
+    lds[r][i & 31] = row < t.rows && c < a.ld ? *reinterpret_cast<const uint32_t*>(t.scale + row * a.ld + c) : 0u;
+  }
+  __syncthreads();
+  uint32_t* out = reinterpret_cast<uint32_t*>(t.out) + (int64_t)(unit >> 2) * a.stages * 512;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const int i = k * 256 + tid, lane = i & 63, s = (i >> 6) & 1, kt = chunk * 16 + (i >> 7);
+    if (kt >= a.stages) continue;
+    uint32_t v = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      v |= ((lds[16 * j + (lane & 15)][(i >> 7) * 2 + s] >> (8 * (lane >> 4))) & 255u) << (8 * j);
+    out[(int64_t)kt * 512 + s * 256 + (unit & 3) * 64 + lane] = v;
+  }
+}
+hipError_t launch_tile_scales(const MxTiles& a, const MxTiles& b, int ld, int stages, hipStream_t st) {
+  MxTileArgs m;
+  m.t[0] = a;
+  m.t[1] = b;
+  m.ld = ld;
+  m.stages = stages;
+  m.chunks = (stages + 15) / 16;
+  mx_tile_kernel<<<(unsigned)((a.tiles + b.tiles) * 4 * m.chunks), 256, 0, st>>>(m);
+  return hipGetLastError();
+}
+
 }  // namespace flce
