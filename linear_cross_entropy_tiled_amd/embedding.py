@@ -10,6 +10,16 @@ from . import (DTYPES, FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32, _dtype_n
 from .logprobs import differentiable, first_order, on_device, raise_for, stream_handle
 
 
+@functools.lru_cache(maxsize=1024)
+def _params(n, h, v, ignore_index, dtype, grad_dtype, flags, scale):
+    return flce_embedding_params(n, h, v, ignore_index, dtype, grad_dtype, flags, scale)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(n, h, v):
+    return flce_embedding_workspace_size(flce_embedding_params(n, h, v, -100, 0, 0, 0, 1.0))
+
+
 def _check_ids(ids):
     import torch
     if ids.dtype not in (torch.int64, torch.int32):
@@ -25,7 +35,7 @@ def _check_places(named):
             raise ValueError(f"{name} must be contiguous")
     dev = named[0][1].device
     for name, t in named:
-        if t is not None and (t.device.type != "cuda" or t.device != dev):
+        if t is not None and (not t.is_cuda or t.device != dev):
             raise ValueError(f"{name} must be on {named[0][0]}' GPU ({dev}), not {t.device}")
 
 
@@ -38,7 +48,7 @@ def _run_backward(p, ids, grad, grad_weight):
     import torch
     dev = grad.device
     with on_device(dev):
-        ws_bytes = flce_embedding_workspace_size(p)
+        ws_bytes = _workspace(p.n_tokens, p.hidden, p.vocab)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         raise_for(flce_embedding_backward(p, _ptr(ids), _ptr(grad), _ptr(grad_weight), _ptr(workspace), ws_bytes,
                                           stream_handle(dev)), "flce_embedding_backward")
@@ -46,10 +56,9 @@ def _run_backward(p, ids, grad, grad_weight):
 
 
 def _forward(p, ids, weight):
-    import torch
     dev = weight.device
     with on_device(dev):
-        out = torch.empty((ids.shape[0], weight.shape[1]), dtype=weight.dtype, device=dev)
+        out = weight.new_empty((p.n_tokens, p.hidden))
         raise_for(flce_embedding_forward(p, _ptr(ids), _ptr(weight), _ptr(out), stream_handle(dev)),
                   "flce_embedding_forward")
     return out
@@ -63,14 +72,14 @@ def _function():
         @staticmethod
         def forward(ctx, weight, ids, p):
             ctx.save_for_backward(ids)
-            ctx.p, ctx.like = p, (weight.shape, weight.dtype)
+            ctx.p = p
             return _forward(p, ids, weight)
 
         @first_order
         def backward(ctx, g):
             ids, = ctx.saved_tensors
-            shape, dtype = ctx.like
-            return _run_backward(ctx.p, ids, g.contiguous(), torch.empty(shape, dtype=dtype, device=g.device)), None, None
+            g = g.contiguous()
+            return _run_backward(ctx.p, ids, g, g.new_empty((ctx.p.vocab, ctx.p.hidden))), None, None
 
     return Embedding
 
@@ -87,7 +96,7 @@ def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100):
     dtype = DTYPES[_dtype_name(weight)]
     _check_scale(scale)
     _check_places([("ids", ids), ("weight", weight)])
-    p = flce_embedding_params(ids.shape[0], weight.shape[1], weight.shape[0], ignore_index, dtype, dtype, flags, scale)
+    p = _params(ids.shape[0], weight.shape[1], weight.shape[0], int(ignore_index), dtype, dtype, flags, float(scale))
     if differentiable(weight):
         return _function().apply(weight, ids, p)
     return _forward(p, ids, weight)
@@ -116,8 +125,8 @@ def embedding_backward(grad, ids, vocab: int, *, scale: float = 1.0, ignore_inde
         raise ValueError(f"invalid grad_weight_dtype {grad_weight_dtype!r}")
     _check_places([("ids", ids), ("grad", grad), ("grad_weight", grad_weight)])
     grad_weight_dtype = grad_weight_dtype or dtype
-    p = flce_embedding_params(ids.shape[0], grad.shape[1], vocab, ignore_index, DTYPES[dtype],
-                              DTYPES[grad_weight_dtype], flags, scale)
+    p = _params(ids.shape[0], grad.shape[1], int(vocab), int(ignore_index), DTYPES[dtype], DTYPES[grad_weight_dtype], flags,
+                float(scale))
     if grad_weight is None:
         kinds = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
         grad_weight = torch.empty((vocab, grad.shape[1]), dtype=kinds[grad_weight_dtype], device=grad.device)
