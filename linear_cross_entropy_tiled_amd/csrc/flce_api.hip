@@ -359,7 +359,7 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
       L.f_bytes = align_up(L.f_wmx + size_t(P.V) * L.ld_mx, 256);
     }
     if (L.vt_large > 0) {
-      const size_t tile = size_t((P.H + 127) / 128) * 2048;   // kMxStage bytes a stage
+      const size_t tile = size_t((P.H + 127) / 128) * kMxStage;
       L.f_tmx_w = L.f_bytes;
       L.f_tmx_h = L.f_tmx_w + L.vt_large * tile;
       L.f_bytes = L.f_tmx_h + P.n_tt * tile;

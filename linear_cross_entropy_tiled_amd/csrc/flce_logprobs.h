@@ -74,6 +74,9 @@ hipError_t launch_logprobs_backward(const Plan& pl, const LpPlan& lp, const LpGr
 hipError_t launch_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
                            hipStream_t st);
 
+// MXFP4's large tiles (flce_mx_tiles.hip): nwg workgroups, token tile by split.
+void launch_mx_tiles(const Plan& pl, const LpTileArgs& a, int nwg, hipStream_t st);
+
 // Small-tile kernels (flce_small.hip).
 void launch_lp_small(const Plan& pl, int bn, const LpTileArgs& a, int n_tt, hipStream_t st);
 void launch_dlogits_small(const Plan& pl, const DlogitsArgs& d, hipStream_t st);

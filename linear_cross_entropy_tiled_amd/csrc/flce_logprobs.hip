@@ -14,21 +14,19 @@
 //
 // With 8-bit operands (a frozen scorer's head) the accumulator is the exact int32
 // product; one multiplication by the vocabulary row's scale and one by the token's
-// turn it into the logit, and the rest is the same.  MXFP4 operands carry their scales into
-// the matrix instructions and give fp32 logits, as the 16-bit types do.
+// turn it into the logit, and the rest is the same.  (MXFP4 operands: flce_mx_tiles.hip.)
 #include <math.h>
 
 #include "flce_device.h"
 #include "flce_logprobs.h"
 #include "flce_lp_state.h"
-#include "flce_mx_device.h"
 
 namespace flce {
 
 template <typename T, bool HAS_BIAS, bool SOFTCAP>
 __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
   constexpr int E = sizeof(T);
-  constexpr bool MX = is_mx<T>, I8 = E == 1 && !MX;
+  constexpr bool I8 = E == 1;
   typedef typename BiasOf<T>::type B;
   constexpr int BE = sizeof(B);
   const int L = xcd_logical_id(blockIdx.x, gridDim.x);
@@ -120,11 +118,7 @@ __global__ __launch_bounds__(kThreads, 1) void lp_tiles_kernel(LpTileArgs a) {
     da.cols_valid = 0;
     da.k_bytes = a.H * E;
     zero_acc(acc);
-    if constexpr (MX)
-      tile_mainloop_mx(da, db, a.weight_tmx + (size_t)(v0 / 256) * KT * kMxStage,
-                       a.hidden_tmx + (size_t)tt * KT * kMxStage, KT, sh, acc);
-    else
-      tile_mainloop<T, true, true>(da, db, KT, sh, acc);
+    tile_mainloop<T, true, true>(da, db, KT, sh, acc);
 
     // per token column: pass 1 turns the accumulator into u and takes the maximum
     // over the rows below V, pass 2 adds 2^x and x 2^x, x = y - m <= 0
@@ -480,7 +474,7 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
         (void)launch_tile_scales(w, h, lp.ld_mx, stages, st);
         a.weight_tmx = w.out;
         a.hidden_tmx = h.out;
-        launch_lp_tiles<mx4>(pl, a, nwg, st);
+        launch_mx_tiles(pl, a, nwg, st);
       } else if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
       else if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
       else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);

@@ -132,7 +132,7 @@ hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int l
   return hipGetLastError();
 }
 
-// 64 rows by 16 stages (128 blocks) a workgroup, through LDS: bytes of four rows become a word.
+// 64 rows by 16 stages (128 blocks) a workgroup, through LDS.
 struct MxTileArgs {
   MxTiles t[2];
   int ld, stages, chunks;   // chunks of 16 stages
@@ -151,16 +151,30 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxTileArgs a) {
     lds[r][i & 31] = row < t.rows && c < a.ld ? *reinterpret_cast<const uint32_t*>(t.scale + row * a.ld + c) : 0u;
   }
   __syncthreads();
-  uint32_t* out = reinterpret_cast<uint32_t*>(t.out) + (int64_t)(unit >> 2) * a.stages * 512;
+  uint32_t* out = reinterpret_cast<uint32_t*>(t.out) + (int64_t)(unit >> 2) * a.stages * (kMxStage / 4);
+  auto scale = [&](int row, int block) { return (lds[row][block >> 2] >> (8 * (block & 3))) & 255u; };
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    const int i = k * 256 + tid, lane = i & 63, s = (i >> 6) & 1, kt = chunk * 16 + (i >> 7);
+    // a stage's 128 words of these 64 rows: two halves of a's words, or two words of b
+    const int i = k * 256 + tid, stage = i >> 7, kt = chunk * 16 + stage, lane = (i >> 1) & 63;
     if (kt >= a.stages) continue;
-    uint32_t v = 0;
+    if (which == 0) {
+      // two sub-steps' halves, 32 rows each: bytes 2 (unit % 2) and up of the words
+      const int p = i & 1, half = unit & 1, sub = (unit >> 1) & 1;
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-      v |= ((lds[16 * j + (lane & 15)][(i >> 7) * 2 + s] >> (8 * (lane >> 4))) & 255u) << (8 * j);
-    out[(int64_t)kt * 512 + s * 256 + (unit & 3) * 64 + lane] = v;
+      for (int q = 0; q < 2; q++) {
+        const int s = 2 * p + q, block = 8 * stage + 2 * s + (lane >> 5);
+        const uint32_t v = scale(lane & 31, block) | scale(32 + (lane & 31), block) << 8;
+        reinterpret_cast<uint16_t*>(out + (int64_t)kt * 512 + sub * 256 + lane * 4 + s)[half] = (uint16_t)v;
+      }
+    } else {
+      const int p = i & 1;
+      uint32_t v = 0;
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        v |= scale(32 * (j & 1) + (lane & 31), 8 * stage + 2 * (2 * p + (j >> 1)) + (lane >> 5)) << (8 * j);
+      out[(int64_t)kt * 512 + (unit & 3) * 128 + lane * 2 + p] = v;
+    }
   }
 }
 hipError_t launch_tile_scales(const MxTiles& a, const MxTiles& b, int ld, int stages, hipStream_t st) {
