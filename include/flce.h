@@ -428,11 +428,14 @@ int flce_dequantize_mxfp4(int dtype, const void* q, const void* scale, int64_t r
                           void* stream);
 
 /* Bytes of device workspace flce_logprobs_mxfp4 needs.  Host only.  params as for
- * flce_logprobs_int8, with hidden % 32 == 0 and at most 2^18, and N*H below 2^31. */
+ * flce_logprobs_int8 (dtype: of hidden states that are not quantised), with hidden % 32 == 0 and
+ * at most 2^18, and N*H below 2^31. */
 int flce_logprobs_mxfp4_workspace_size(const flce_params* p, size_t* bytes);
 
-/* hidden (N, H / 2) and weight (V, H / 2): codes, 16-byte aligned as bias (fp32, or NULL) is; their scales
- * (N, H / 32) and (V, H / 32): 4-byte aligned.  Outputs and rows without a target as flce_logprobs_forward. */
+/* weight (V, H / 2): codes, 16-byte aligned as hidden and bias (fp32, or NULL) are; weight_scale (V, H / 32):
+ * 4-byte aligned.  hidden: codes (N, H / 2) with their hidden_scale (N, H / 32, 4-byte aligned), or, with
+ * hidden_scale NULL, values (N, H) of params->dtype, which are quantised in the workspace as by
+ * flce_quantize_mxfp4.  Outputs and rows without a target as flce_logprobs_forward. */
 int flce_logprobs_mxfp4(const flce_params* p, const void* hidden, const void* hidden_scale, const void* weight,
                         const void* weight_scale, const float* bias, const void* targets, float* logps, float* entropy,
                         float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -353,9 +353,11 @@ void plan_logprobs(const Plan& P, LpPlan* out) {
   if (P.mx) {
     const int blocks = (int)(P.H / 16);
     L.ld_mx = (blocks + 3) / 4 * 4;
+    L.f_q = L.f_bytes;
+    L.f_hmx = align_up(L.f_q + size_t(P.N) * P.H, 256);
+    L.f_bytes = align_up(L.f_hmx + size_t(P.N) * L.ld_mx, 256);
     if (L.ld_mx != blocks) {
-      L.f_hmx = L.f_bytes;
-      L.f_wmx = align_up(L.f_hmx + size_t(P.N) * L.ld_mx, 256);
+      L.f_wmx = L.f_bytes;
       L.f_bytes = align_up(L.f_wmx + size_t(P.V) * L.ld_mx, 256);
     }
     if (L.vt_large > 0) {
@@ -556,9 +558,11 @@ enum class Scores { kTrained, kInt8, kMx };
 static int logprobs_plan(const flce_params* p, Scores kind, Plan* pl, LpPlan* lp) {
   flce_params q;
   const bool int8 = kind == Scores::kInt8, mx = kind == Scores::kMx;
+  int x_dtype = FLCE_BF16;
   if (p && kind != Scores::kTrained) {   // no backward: neither its chunk nor the type it would have limits the sizes
     if (!valid_dtype(p->dtype)) return FLCE_ERR_INVALID_ARG;
     q = *p;
+    x_dtype = p->dtype;
     q.dtype = q.grad_weight_dtype = FLCE_BF16;
     q.vocab_chunk = 256;
     if (mx) {   // planned by the row's bytes
@@ -579,6 +583,7 @@ static int logprobs_plan(const flce_params* p, Scores kind, Plan* pl, LpPlan* lp
   if (mx) {
     if (pl->H > kMaxMxHidden / 2) return FLCE_ERR_UNSUPPORTED;
     pl->int8 = pl->mx = true;
+    pl->x_dtype = x_dtype;
     pl->esize = 1;
   }
   plan_logprobs(*pl, lp);
@@ -722,7 +727,7 @@ int flce_logprobs_mxfp4(const flce_params* p, const void* hidden, const void* hi
   if (rc != FLCE_OK) return rc;
   pl.has_bias = bias != nullptr;
   if (!workspace || !weight || !weight_scale) return FLCE_ERR_INVALID_ARG;
-  if (pl.N > 0 && (!hidden || !hidden_scale || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
+  if (pl.N > 0 && (!hidden || !targets || !logps || !lse)) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(bias) || !aligned4(weight_scale) ||
       !aligned16(workspace) || !targets_aligned(pl, targets) || !aligned4(hidden_scale) || !aligned4(logps) ||
       !aligned4(entropy) || !aligned4(lse))

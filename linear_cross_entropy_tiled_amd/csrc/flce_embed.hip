@@ -67,14 +67,16 @@ constexpr int64_t kZeroPiece = 64 * 1024;
 // One workgroup of 1024.
 __device__ __forceinline__ void write_zeros(const ZeroArgs& z, int block) {
   for (int64_t at = z.from + block * kZeroPiece; at < z.until; at += ((int64_t)gridDim.x - z.first) * kZeroPiece) {
-    const int64_t end = min(at + kZeroPiece, z.until);
+    char* to = z.to + at + threadIdx.x * 16;
+    const i32x4 zeros = {0, 0, 0, 0};
+    if (at + kZeroPiece <= z.until) {
 #pragma unroll
-    for (int k = 0; k < kZeroPiece / 16384; k++) {
-      const int64_t i = at + k * 16384 + threadIdx.x * 16;
-      if (i + 16 <= end) *reinterpret_cast<i32x4*>(z.to + i) = i32x4{0, 0, 0, 0};
-      else
-        for (int64_t j = i; j < end; j++) z.to[j] = 0;
+      for (int k = 0; k < kZeroPiece / 16384; k++) *reinterpret_cast<i32x4*>(to + k * 16384) = zeros;
+      continue;
     }
+    const int64_t whole = z.until / 16 * 16;   // the last piece, and the bytes after its last whole 16
+    for (int64_t i = at + threadIdx.x * 16; i < whole; i += 16384) *reinterpret_cast<i32x4*>(z.to + i) = zeros;
+    if (threadIdx.x < z.until - whole) z.to[whole + threadIdx.x] = 0;
   }
 }
 // A gradient that is not 16-byte aligned.

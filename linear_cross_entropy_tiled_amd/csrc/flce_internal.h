@@ -16,6 +16,7 @@ struct Plan {
   bool has_bias;
   bool int8;                     // hidden and weight are 8-bit (log-probabilities only)
   bool mx;                       // they are MXFP4: H counts bytes, two values each
+  int x_dtype;                   // MXFP4: of hidden states that are not quantised yet
   bool accum_gw, accum_gb;       // backward adds into grad_weight / grad_bias
   bool tgt_i32;                  // targets are int32 (else int64)
   bool gw_accum_out;             // one-pass path: sum grad_weight over the blocks in its own dtype

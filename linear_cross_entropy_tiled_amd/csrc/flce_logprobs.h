@@ -13,9 +13,10 @@ struct LpPlan {
   int bn;
   int vt_large, S_large, S_small;
   int N_pad;
-  // MXFP4 scale rows of a length that is no multiple of 4 are copied to rows of ld_mx
+  // MXFP4: hidden states' codes and scales where they are quantised in the call; scale rows
+  // of a length that is no multiple of 4 are copied to rows of ld_mx
   int ld_mx;
-  size_t f_hmx, f_wmx;
+  size_t f_q, f_hmx, f_wmx;
   size_t f_tmx_w, f_tmx_h;    // scales in the large tiles' order
   size_t f_bytes;
 
@@ -64,7 +65,8 @@ struct LpTileArgs {
 };
 
 void plan_logprobs(const Plan& pl, LpPlan* lp);
-// pl.int8, pl.mx: 8- and 4-bit operands with their scales (fp32 and bytes), bias in fp32.
+// pl.int8, pl.mx: 8- and 4-bit operands with their scales (fp32 and bytes), bias in fp32; of pl.mx hidden may be values
+// of pl.x_dtype, without scales.
 hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden, const void* weight, const void* bias,
                            const void* hidden_scale, const void* weight_scale, const void* targets, float* logps,
                            float* entropy, float* lse, char* ws, hipStream_t st);

@@ -436,18 +436,44 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
     a.hidden_scale = static_cast<const float*>(hidden_scale);
     a.weight_scale = static_cast<const float*>(weight_scale);
     if (pl.mx) {
-      const int blocks = (int)(pl.H / 16);
-      a.hidden_mx = static_cast<const uint8_t*>(hidden_scale);
-      a.weight_mx = static_cast<const uint8_t*>(weight_scale);
-      a.ld_hmx = a.ld_wmx = (uint32_t)lp.ld_mx;
-      if (lp.ld_mx != blocks) {
-        uint8_t* hs = reinterpret_cast<uint8_t*>(ws + lp.f_hmx);
-        uint8_t* wsc = reinterpret_cast<uint8_t*>(ws + lp.f_wmx);
-        (void)launch_pad_scales(a.hidden_mx, pl.N, blocks, lp.ld_mx, hs, st);
-        (void)launch_pad_scales(a.weight_mx, pl.V, blocks, lp.ld_mx, wsc, st);
-        a.hidden_mx = hs;
-        a.weight_mx = wsc;
+      MxPrep m{};
+      m.n = pl.N;
+      m.blocks = (int)(pl.H / 16);
+      m.ld = lp.ld_mx;
+      if (!hidden_scale) {   // hidden holds values: quantised here
+        m.x = hidden;
+        m.q = reinterpret_cast<uint8_t*>(ws + lp.f_q);
+        m.scale = reinterpret_cast<uint8_t*>(ws + lp.f_hmx);
+        a.hidden = reinterpret_cast<const char*>(m.q);
+        a.hidden_mx = m.scale;
+      } else {
+        a.hidden_mx = static_cast<const uint8_t*>(hidden_scale);
+        if (m.ld != m.blocks) {
+          uint8_t* padded = reinterpret_cast<uint8_t*>(ws + lp.f_hmx);
+          (void)launch_pad_scales(a.hidden_mx, pl.N, m.blocks, m.ld, padded, st);
+          a.hidden_mx = padded;
+        }
       }
+      a.weight_mx = static_cast<const uint8_t*>(weight_scale);
+      if (m.ld != m.blocks) {
+        uint8_t* padded = reinterpret_cast<uint8_t*>(ws + lp.f_wmx);
+        (void)launch_pad_scales(a.weight_mx, pl.V, m.blocks, m.ld, padded, st);
+        a.weight_mx = padded;
+      }
+      a.ld_hmx = a.ld_wmx = (uint32_t)m.ld;
+      if (lp.vt_large > 0) {
+        m.stages = (int)((pl.H + kBKB - 1) / kBKB);
+        m.w_tiles = lp.vt_large;
+        m.h_tiles = (int)pl.n_tt;
+        m.w_scale = a.weight_mx;
+        m.w_rows = pl.V;
+        m.h_scale = a.hidden_mx;
+        m.w_out = reinterpret_cast<uint8_t*>(ws + lp.f_tmx_w);
+        m.h_out = reinterpret_cast<uint8_t*>(ws + lp.f_tmx_h);
+        a.weight_tmx = m.w_out;
+        a.hidden_tmx = m.h_out;
+      }
+      (void)launch_mx_prep(pl.x_dtype, m, st);
     }
     a.targets = targets;
     a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
@@ -467,15 +493,8 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
       a.S = lp.S_large;
       a.s_first = 0;
       const int nwg = (int)pl.n_tt * a.S;
-      if (pl.mx) {
-        const int stages = (int)((pl.H + kBKB - 1) / kBKB);
-        const MxTiles w{a.weight_mx, pl.V, lp.vt_large, reinterpret_cast<uint8_t*>(ws + lp.f_tmx_w)};
-        const MxTiles h{a.hidden_mx, pl.N, (int)pl.n_tt, reinterpret_cast<uint8_t*>(ws + lp.f_tmx_h)};
-        (void)launch_tile_scales(w, h, lp.ld_mx, stages, st);
-        a.weight_tmx = w.out;
-        a.hidden_tmx = h.out;
-        launch_mx_tiles(pl, a, nwg, st);
-      } else if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
+      if (pl.mx) launch_mx_tiles(pl, a, nwg, st);
+      else if (pl.int8) launch_lp_tiles<int8_t>(pl, a, nwg, st);
       else if (pl.dtype == FLCE_BF16) launch_lp_tiles<bf16>(pl, a, nwg, st);
       else if (pl.dtype == FLCE_F16) launch_lp_tiles<f16>(pl, a, nwg, st);
       else launch_lp_tiles<float>(pl, a, nwg, st);

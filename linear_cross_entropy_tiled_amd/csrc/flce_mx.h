@@ -32,12 +32,21 @@ hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int l
 //  b (the hidden states): for each 64 rows and lane two words; byte 2 (s % 2) + n of word s / 2 is row 32 n + l % 32.
 // Both in one launch.
 constexpr int kMxStage = 2048;
-struct MxTiles {
-  const uint8_t* scale;
-  int64_t rows;
-  int tiles;
-  uint8_t* out;
+// What a call's matrix kernels read, made in one launch: the hidden states' codes and scales where x is given (rows of
+// ld scale bytes, as the small tiles take them), and with `stages` the scales in the large tiles' order.
+struct MxPrep {
+  int64_t n;                   // hidden states
+  int blocks, ld, stages;      // of a row; scale bytes from row to row (a multiple of 4); 0 stages: no large tiles
+  int w_tiles, h_tiles;        // large tiles of 256 rows
+  const void* x;               // hidden states to quantise, or NULL
+  uint8_t* q;
+  uint8_t* scale;
+  const uint8_t* w_scale;      // the weight's, rows of ld bytes
+  int64_t w_rows;
+  const uint8_t* h_scale;      // the hidden states' where x is NULL
+  uint8_t* w_out;
+  uint8_t* h_out;
 };
-hipError_t launch_tile_scales(const MxTiles& a, const MxTiles& b, int ld, int stages, hipStream_t st);
+hipError_t launch_mx_prep(int dtype, const MxPrep& p, hipStream_t st);
 
 }  // namespace flce

@@ -275,13 +275,13 @@ def _check_mx(name, q, scale):
     import torch
     if q.dim() != 2 or scale.dim() != 2:
         raise ValueError(f"{name} and {name}_scale must be 2-D, got {tuple(q.shape)} and {tuple(scale.shape)}")
-    for what, t in ((name, q), (f"{name}_scale", scale)):
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{what} must be uint8 (quantize_mxfp4), not {t.dtype}")
-    if q.shape[1] == 0 or q.shape[1] % 16:
-        raise ValueError(f"rows of {name} must be a multiple of 16 bytes (32 values) long, got {q.shape[1]}")
-    if tuple(scale.shape) != (q.shape[0], q.shape[1] // 16):
-        raise ValueError(f"{name}_scale must have shape {(q.shape[0], q.shape[1] // 16)}, got {tuple(scale.shape)}")
+    if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
+        raise TypeError(f"{name} and {name}_scale must be uint8 (quantize_mxfp4), not {q.dtype} and {scale.dtype}")
+    rows, cols = q.shape
+    if cols == 0 or cols % 16:
+        raise ValueError(f"rows of {name} must be a multiple of 16 bytes (32 values) long, got {cols}")
+    if scale.shape != (rows, cols // 16):
+        raise ValueError(f"{name}_scale must have shape {(rows, cols // 16)}, got {tuple(scale.shape)}")
 
 
 def dequantize_mxfp4(q, scale, dtype=None):
@@ -306,6 +306,13 @@ def dequantize_mxfp4(q, scale, dtype=None):
     return x
 
 
+@functools.lru_cache(maxsize=1024)
+def _mx_plan(n, h, v, dtype, logit_scale, softcap, ignore_index, targets_int32):
+    p = make_params(n, h, v, dtype=dtype, logit_scale=logit_scale, softcap=softcap, ignore_index=ignore_index,
+                    reduction="none", targets_int32=targets_int32)
+    return p, flce_logprobs_mxfp4_workspace_size(p)
+
+
 def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
                          logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
                          return_entropy: bool = False):
@@ -318,14 +325,15 @@ def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hi
     v, h = weight.shape[0], 2 * weight.shape[1]
     if hidden_scale is not None:
         _check_mx("hidden", hidden, hidden_scale)
+        n, cols, dtype = hidden.shape[0], 2 * hidden.shape[1], "bf16"
     else:
         if hidden.dim() != 2:
             raise ValueError(f"hidden must be 2-D, got {tuple(hidden.shape)}")
-        _dtype_name(hidden)
-    n, cols = hidden.shape[0], hidden.shape[1] * (1 if hidden_scale is None else 2)
+        dtype = _dtype_name(hidden)
+        n, cols = hidden.shape
     if cols != h:
         raise ValueError(f"weight has {h} columns, hidden has {cols}")
-    _targets_int32(targets)
+    int32 = _targets_int32(targets)
     if targets.dim() != 1 or targets.shape[0] != n:
         raise ValueError(f"targets must have shape ({n},), got {tuple(targets.shape)}")
     if bias is not None:
@@ -333,30 +341,32 @@ def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hi
             raise TypeError(f"bias must be float32, not {bias.dtype}")
         if bias.dim() != 1 or bias.shape[0] != v:
             raise ValueError(f"bias must have shape ({v},), got {tuple(bias.shape)}")
-    named = [("hidden", hidden), ("weight", weight), ("targets", targets), ("weight_scale", weight_scale),
-             ("bias", bias), ("hidden_scale", hidden_scale)]
+    named = [("hidden", hidden), ("weight", weight), ("targets", targets), ("weight_scale", weight_scale)]
+    if bias is not None:
+        named.append(("bias", bias))
+    if hidden_scale is not None:
+        named.append(("hidden_scale", hidden_scale))
+    dev = hidden.device
     for name, t in named:
-        if t is not None and not t.is_contiguous():
+        if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    for name, t in named:
-        if t is not None and (t.device.type != "cuda" or t.device != hidden.device):
-            raise ValueError(f"{name} must be on hidden's GPU ({hidden.device}), not {t.device}")
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be on hidden's GPU ({dev}), not {t.device}")
     recorded = torch.is_grad_enabled()
-    for name, t in named:
+    for name, t in (("hidden", hidden), ("bias", bias)):     # the others are integers
         if t is not None and ((recorded and t.requires_grad) or has_tangent(t)):
             raise ValueError(f"4-bit scores have no gradient: detach {name}, or use token_logprobs")
-    p = make_params(n, h, v, logit_scale=logit_scale, softcap=softcap, ignore_index=ignore_index, reduction="none",
-                    targets_int32=_targets_int32(targets))
-    dev = hidden.device
+    p, ws_bytes = _mx_plan(n, h, v, dtype, float(logit_scale), float(softcap or 0.0), int(ignore_index), int32)
     with on_device(dev):
-        ws_bytes = flce_logprobs_mxfp4_workspace_size(p)
-        hidden, weight, weight_scale, bias, hidden_scale = map(_aligned16,
-                                                               (hidden, weight, weight_scale, bias, hidden_scale))
-        if hidden_scale is None:
-            hidden, hidden_scale = _quantize_mx(hidden)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        logps, entropy, lse = (torch.empty(n, dtype=torch.float32, device=dev) for _ in range(3))
-        raise_for(flce_logprobs_mxfp4(p, _ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale), _ptr(bias),
-                                      _ptr(targets), _ptr(logps), _ptr(entropy), _ptr(lse), _ptr(workspace), ws_bytes,
-                                      stream_handle(dev)), "flce_logprobs_mxfp4")
+        hidden, weight, weight_scale = _aligned16(hidden), _aligned16(weight), _aligned16(weight_scale)
+        bias, hidden_scale = _aligned16(bias), _aligned16(hidden_scale)
+        # one allocation: the workspace, then the log-sum-exps, which nobody asked for
+        workspace = torch.empty(ws_bytes + 4 * n, dtype=torch.uint8, device=dev)
+        logps = torch.empty(n, dtype=torch.float32, device=dev)
+        entropy = torch.empty(n, dtype=torch.float32, device=dev) if return_entropy else None
+        at = workspace.data_ptr()
+        raise_for(flce_logprobs_mxfp4(p, hidden.data_ptr(), _ptr(hidden_scale), weight.data_ptr(),
+                                      weight_scale.data_ptr(), _ptr(bias), targets.data_ptr(), logps.data_ptr(),
+                                      _ptr(entropy), at + ws_bytes, at, ws_bytes, stream_handle(dev)),
+                  "flce_logprobs_mxfp4")
     return (logps, entropy) if return_entropy else logps

@@ -94,7 +94,7 @@ def test_abi_codes():
     def call(x=16, s=16, w=16, ws=16, b=None, t=16, lp=16, lse=16, work=16, n=need):
         return flce.flce_logprobs_mxfp4(p, x, s, w, ws, b, t, lp, None, lse, work, n, None)
 
-    for name in ("x", "s", "w", "ws", "t", "lp", "lse", "work"):
+    for name in ("x", "w", "ws", "t", "lp", "lse", "work"):    # (without s, x holds values)
         assert call(**{name: None}) == bad, name
     for name in ("x", "w", "b", "work"):
         assert call(**{name: 24}) == odd, name
