@@ -192,7 +192,6 @@ template <bool HAS_BIAS, bool SOFTCAP> __global__ __launch_bounds__(kThreads, 1)
   // the accumulator times s_u is u = y, or with the cap u = v / cap, y = cap log2(e) tanh(u)
   const float s_u = SOFTCAP ? a.scale / a.cap : a.scale * kLog2e;
   const float cap2 = a.cap * kLog2e;
-  auto capped = [&](float u) { return cap2 * tanh_of<true>(u); };
 
   const char* sc_a = scales[0] + wm * 1024 + lane * 16;
   const char* sc_b = scales[0] + kMxStage + wn * 512 + lane * 8;
@@ -205,12 +204,20 @@ template <bool HAS_BIAS, bool SOFTCAP> __global__ __launch_bounds__(kThreads, 1)
   for (int vt = vt_begin; vt < vt_end; ++vt) {
     const int v0 = a.v_first + vt * 256;
     f32x16 acc[kMxM][kMxN];
+    // the sums begin with the bias (a lane holds rows 32 mi + 8 q + 4 (lane / 32) + r in acc[mi][ni][4 q + r])
+    const int lane_row = 4 * (lane >> 5);
 #pragma unroll
     for (int mi = 0; mi < kMxM; mi++)
 #pragma unroll
-      for (int ni = 0; ni < kMxN; ni++)
+      for (int q = 0; q < 4; q++) {
+        float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (HAS_BIAS)
+          lds_vec4<float>(bias_lds[(vt - vt_begin) & 1], wm * kWaveM + 32 * mi + 8 * q + lane_row, b4);
 #pragma unroll
-        for (int i = 0; i < 16; i++) acc[mi][ni][i] = 0.0f;
+        for (int ni = 0; ni < kMxN; ni++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) acc[mi][ni][4 * q + r] = b4[r];
+      }
     // (the first fragments are read here, and not with the tile before's last ones, so that none is live in its
     // epilogue)
     MxFrags f;
@@ -248,73 +255,73 @@ template <bool HAS_BIAS, bool SOFTCAP> __global__ __launch_bounds__(kThreads, 1)
       sb = sb_next;
     }
 
-    // The tile's logits: a lane holds 64 rows of each of its two token columns, rows
-    // 32 mi + 8 q + 4 (lane / 32) + r in acc[mi][ni][4 q + r].
+    // A lane holds 64 rows of each of its two token columns.  y replaces the sums.
     const int vw = v0 + wm * kWaveM;
-    const int n_valid = a.V - vw, lane_row = 4 * (lane >> 5);
-    const bool ragged = n_valid < kWaveM;
-    const int lim = n_valid - lane_row;   // element (mi, q, r) is below V iff 32 mi + 8 q + r < lim
-    const char* bias_tile = bias_lds[(vt - vt_begin) & 1];
+    const int n_valid = a.V - vw;
 #pragma unroll
     for (int ni = 0; ni < kMxN; ni++) {
-      float mu = kMasked;
 #pragma unroll
       for (int mi = 0; mi < kMxM; mi++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-          float sb4[4];
-          if constexpr (HAS_BIAS) {
-            lds_vec4<float>(bias_tile, wm * kWaveM + 32 * mi + 8 * q + lane_row, sb4);
+          float u[4];
 #pragma unroll
-            for (int r = 0; r < 4; r++) sb4[r] *= s_u;
+          for (int r = 0; r < 4; r++) u[r] = acc[mi][ni][4 * q + r] * s_u;
+          if constexpr (SOFTCAP) {
+            float th[4];
+            tanh4(u, th);
+#pragma unroll
+            for (int r = 0; r < 4; r++) u[r] = cap2 * th[r];
           }
 #pragma unroll
-          for (int r = 0; r < 4; r++) {
-            float u = acc[mi][ni][4 * q + r];
-            u = HAS_BIAS ? fmaf(u, s_u, sb4[r]) : u * s_u;
-            acc[mi][ni][4 * q + r] = u;
-            if (!ragged || 32 * mi + 8 * q + r < lim) mu = fmaxf(mu, u);
-          }
+          for (int r = 0; r < 4; r++) acc[mi][ni][4 * q + r] = u[r];
         }
-      // (a block without a finite logit: see lp_tiles_kernel)
-      const float mx = SOFTCAP && lim > 0 ? capped(mu) : mu;
-      const int rel = tgt[ni] - vw;
-      const bool hit = rel >= 0 && rel < kWaveM && ((rel >> 2) & 1) == (lane >> 5);
-      if (__builtin_amdgcn_ballot_w64(hit)) {
-        const int rel_l = rel - lane_row;
-        float ut = 0.0f;
+      if (n_valid < kWaveM) {
+        // rows past V lie below every maximum and add 0.  (Their number is opaque, or the comparisons of both columns
+        // are made together and 128 scalar registers kept for them.)
+        int lim = n_valid - lane_row;
+        asm volatile("" : "+v"(lim));
 #pragma unroll
         for (int mi = 0; mi < kMxM; mi++)
 #pragma unroll
           for (int i = 0; i < 16; i++)
-            if (32 * mi + 8 * (i >> 2) + (i & 3) == rel_l) ut = acc[mi][ni][i];
-        if (hit) st[ni].yt = SOFTCAP ? capped(ut) : ut;
+            if (32 * mi + 8 * (i >> 2) + (i & 3) >= lim) acc[mi][ni][i] = 2.0f * kMasked;
       }
-      const float m_new = fmaxf(st[ni].m, mx);
+      float mu = kMasked;   // stays where there is no finite logit
+#pragma unroll
+      for (int mi = 0; mi < kMxM; mi++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) mu = fmaxf(mu, acc[mi][ni][i]);
+      const int rel = tgt[ni] - vw;
+      const bool hit = rel >= 0 && rel < kWaveM && ((rel >> 2) & 1) == (lane >> 5);
+      if (__builtin_amdgcn_ballot_w64(hit)) {
+        int rel_l = rel - lane_row;
+        asm volatile("" : "+v"(rel_l));
+        float yt = 0.0f;
+#pragma unroll
+        for (int mi = 0; mi < kMxM; mi++)
+#pragma unroll
+          for (int i = 0; i < 16; i++)
+            if (32 * mi + 8 * (i >> 2) + (i & 3) == rel_l) yt = acc[mi][ni][i];
+        if (hit) st[ni].yt = yt;
+      }
+      const float m_new = fmaxf(st[ni].m, mu);
       const float dm = st[ni].l == 0.0f ? 0.0f : st[ni].m - m_new;
       const float alpha = fast_exp2(dm);
       float se0 = 0.f, se1 = 0.f, sx0 = 0.f, sx1 = 0.f;
 #pragma unroll
       for (int mi = 0; mi < kMxM; mi++)
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          float u[4], th[4];
-#pragma unroll
-          for (int r = 0; r < 4; r++) u[r] = acc[mi][ni][4 * q + r];
-          if constexpr (SOFTCAP) tanh4(u, th);
-#pragma unroll
-          for (int r = 0; r < 4; r++) {
-            float x = SOFTCAP ? fmaf(cap2, th[r], -m_new) : u[r] - m_new;
-            if (ragged && 32 * mi + 8 * q + r >= lim) x = kMasked;
-            const float e = fast_exp2(x);
-            const float xf = SOFTCAP ? x : fmaxf(x, kMasked);   // 0 and not NaN times a logit of -inf
-            if (r & 1) {
-              se1 += e;
-              sx1 = fmaf(e, xf, sx1);
-            } else {
-              se0 += e;
-              sx0 = fmaf(e, xf, sx0);
-            }
+        for (int i = 0; i < 16; i++) {
+          const float x = acc[mi][ni][i] - m_new, e = fast_exp2(x);
+          // a logit of -inf, which only a bias gives, is to add 0 and not 0 times infinity
+          const float xf = SOFTCAP || !HAS_BIAS ? x : fmaxf(x, kMasked);
+          if (i & 1) {
+            se1 += e;
+            sx1 = fmaf(e, xf, sx1);
+          } else {
+            se0 += e;
+            sx0 = fmaf(e, xf, sx0);
           }
         }
       st[ni].T = fmaf(fmaf(dm, st[ni].l, st[ni].T), alpha, sx0 + sx1);
