@@ -9,8 +9,7 @@
 
 namespace flce {
 
-constexpr int kSortItems = 8192;     // ids of a workgroup of a pass: 16 waves, 8 each of their 64 lanes
-constexpr int kSortAlone = 16384;    // ids that one workgroup sorts by itself
+constexpr int kSortAlone = 16384;    // tokens up to which the sort is one launch
 constexpr int kSortBits = 9;         // of a pass: two for a vocabulary below 2^18
 constexpr int kSortBins = 1 << kSortBits;
 
@@ -23,7 +22,8 @@ struct EmbedPlan {
   int64_t ignore_index;
   // backward
   int passes;                  // of the sort, kSortBits each
-  int sort_blocks;
+  int sort_parts;              // one launch: workgroups, each with the ids of its part
+  int sort_waves, sort_blocks; // else: waves of a workgroup (512 ids each), workgroups
   int chunk;                   // sorted ids a workgroup sums
   int64_t n_chunks;
   size_t w_keys[2], w_at[2], w_hist, w_part, w_bytes;   // workspace offsets

@@ -1,8 +1,8 @@
 // Token embedding, out_i = scale weight[id_i], and its gradient
 //   grad_weight_v = scale sum over the tokens i with id_i = v of grad_i.
 //
-// The gradient sorts the tokens by their id (stable, so that a row's tokens are summed in
-// their order and results do not depend on timing), then sums each run of equal ids in
+// The gradient brings tokens of the same id together (in their order, so that results do
+// not depend on timing), then sums each run of equal ids in
 // fp32 and rounds it once.  Runs are summed by chunks of sorted tokens, not by rows: a
 // frequent token's run of thousands is spread over many workgroups.  The part of a run
 // that reaches over a chunk's edge is left in fp32 and a second kernel adds the parts.
@@ -64,18 +64,17 @@ struct ZeroArgs {
 };
 constexpr int64_t kZeroPiece = 64 * 1024;
 
-// One workgroup of 1024.
-__device__ __forceinline__ void write_zeros(const ZeroArgs& z, int block) {
+template <int THREADS> __device__ __forceinline__ void write_zeros(const ZeroArgs& z, int block) {
   for (int64_t at = z.from + block * kZeroPiece; at < z.until; at += ((int64_t)gridDim.x - z.first) * kZeroPiece) {
     char* to = z.to + at + threadIdx.x * 16;
     const i32x4 zeros = {0, 0, 0, 0};
     if (at + kZeroPiece <= z.until) {
 #pragma unroll
-      for (int k = 0; k < kZeroPiece / 16384; k++) *reinterpret_cast<i32x4*>(to + k * 16384) = zeros;
+      for (int k = 0; k < (int)kZeroPiece / (16 * THREADS); k++) *reinterpret_cast<i32x4*>(to + k * 16 * THREADS) = zeros;
       continue;
     }
     const int64_t whole = z.until / 16 * 16;   // the last piece, and the bytes after its last whole 16
-    for (int64_t i = at + threadIdx.x * 16; i < whole; i += 16384) *reinterpret_cast<i32x4*>(z.to + i) = zeros;
+    for (int64_t i = at + threadIdx.x * 16; i < whole; i += 16 * THREADS) *reinterpret_cast<i32x4*>(z.to + i) = zeros;
     if (threadIdx.x < z.until - whole) z.to[whole + threadIdx.x] = 0;
   }
 }
@@ -91,7 +90,7 @@ struct SortArgs {
   EmbedArgs e;
   ZeroArgs z;
   int shift, first;            // bits already sorted; first pass: keys come from the ids
-  int passes;                  // sort_alone_kernel
+  int passes, parts;           // sort_parts_kernel
   const uint32_t* keys;
   const uint32_t* at;
   uint32_t* keys_out;
@@ -104,74 +103,105 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i) {
   return a.first ? row_of(a.e, i) : a.keys[i];
 }
 
-// Ranks `rounds` items a lane by digit within their wave: a wave's items are neighbours (item k of a lane is number
-// 64 k + lane); in a round the lanes with the same digit find each other by ballots, and the first of them counts
-// for all.  bins: the wave's counts, zeroed before, its items by digit after.
-template <int ROUNDS>
-__device__ __forceinline__ void wave_ranks(const uint32_t (&key)[ROUNDS], int shift, int n_here, uint32_t* bins, int lane,
-                                           uint32_t (&rank)[ROUNDS]) {
+// Ranks items by digit within their wave, a round of 64 after the other: the lanes of a round with the same digit find
+// each other by ballots, and the first of them counts for all.  bins: the wave's counts, zeroed before, its items by
+// digit after.
+__device__ __forceinline__ uint32_t round_rank(uint32_t key, bool here, int shift, uint32_t* bins, int lane) {
+  const uint32_t digit = (key >> shift) & (kSortBins - 1);
+  uint64_t same = __ballot(here);
 #pragma unroll
-  for (int k = 0; k < ROUNDS; k++) {
-    const bool here = k * 64 + lane < n_here;
-    const uint32_t digit = (key[k] >> shift) & (kSortBins - 1);
-    uint64_t same = __ballot(here);
-#pragma unroll
-    for (int b = 0; b < kSortBits; b++) {
-      const bool bit = (digit >> b) & 1;
-      const uint64_t m = __ballot(bit);
-      same &= bit ? m : ~m;
-    }
-    const uint64_t below = same & ((uint64_t(1) << lane) - 1);
-    rank[k] = here ? bins[digit] + (uint32_t)__popcll(below) : 0u;
-    wave_lds_sync();
-    if (here && below == 0) bins[digit] += (uint32_t)__popcll(same);
-    wave_lds_sync();
+  for (int b = 0; b < kSortBits; b++) {
+    const bool bit = (digit >> b) & 1;
+    const uint64_t m = __ballot(bit);
+    same &= bit ? m : ~m;
   }
+  const uint64_t below = same & ((uint64_t(1) << lane) - 1);
+  const uint32_t rank = here ? bins[digit] + (uint32_t)__popcll(below) : 0u;
+  wave_lds_sync();
+  if (here && below == 0) bins[digit] += (uint32_t)__popcll(same);
+  wave_lds_sync();
+  return rank;
 }
 
-// Up to kSortAlone tokens: all passes by one workgroup, in LDS (8192 tokens: 69 us as three launches a pass of 8 bits,
-// 10 us here).
-__global__ __launch_bounds__(1024) void sort_alone_kernel(SortArgs a) {
-  constexpr int kRounds = kSortAlone / 1024, kPerWave = kSortAlone / 16;
+// Up to kSortAlone tokens, one launch.  Equal ids have to be neighbours, no more: ids fall into parts by a hash, a
+// workgroup reads all ids, keeps its part's (in their order), sorts those in LDS, and writes them after the parts
+// before its own, whose ids it has counted too.  So no workgroup waits for another, and with Zipf's ids the one that
+// holds the most frequent sorts an eighth of the tokens.  (16000 tokens, V = 32000: one workgroup for all 43 us; three
+// launches a pass 66 us for 32768.)  Tokens without a row come last.
+__global__ __launch_bounds__(1024) void sort_parts_kernel(SortArgs a) {
+  constexpr int kRounds = kSortAlone / 1024;
   __shared__ uint32_t keys[kSortAlone];
   __shared__ uint16_t ats[kSortAlone];
   __shared__ uint32_t bins[16][kSortBins];
-  __shared__ uint32_t totals[8];
+  __shared__ uint32_t totals[16], before[16], none[16];
   if ((int)blockIdx.x >= a.z.first) {
-    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    write_zeros<1024>(a.z, (int)blockIdx.x - a.z.first);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = (int)a.e.n;
-  // the items, spread evenly over the waves
-  const int rounds = (n + 1023) / 1024, i0 = wave * rounds * 64, n_here = min(max(n - i0, 0), rounds * 64);
+  const uint32_t v = (uint32_t)a.e.v, own = blockIdx.x;
+  const uint64_t lanes_below = (uint64_t(1) << lane) - 1;
   uint32_t key[kRounds], at[kRounds], rank[kRounds];
+  {
+    // a wave's ids are neighbours
+    const int rounds = (n + 1023) / 1024, i0 = wave * rounds * 64, n_here = min(max(n - i0, 0), rounds * 64);
+    uint32_t mine = 0, less = 0, missing = 0;
+#pragma unroll
+    for (int k = 0; k < kRounds; k++) key[k] = k * 64 + lane < n_here ? row_of(a.e, i0 + k * 64 + lane) : v;
+#pragma unroll
+    for (int k = 0; k < kRounds; k++) {
+      if (k >= rounds) break;
+      const bool here = k * 64 + lane < n_here;
+      const uint32_t part = ((key[k] * 2654435761u) >> 16) % (uint32_t)a.parts;
+      const uint64_t m = __ballot(here && key[k] < v && part == own);
+      rank[k] = (m >> lane) & 1 ? mine + (uint32_t)__popcll(m & lanes_below) : 0xFFFFFFFFu;
+      mine += (uint32_t)__popcll(m);
+      less += (uint32_t)__popcll(__ballot(here && key[k] < v && part < own));
+      missing += (uint32_t)__popcll(__ballot(here && key[k] == v));
+    }
+    if (lane == 0) {
+      totals[wave] = mine;
+      before[wave] = less;
+      none[wave] = missing;
+    }
+    __syncthreads();
+    uint32_t base = 0;
+    for (int w = 0; w < wave; w++) base += totals[w];
+#pragma unroll
+    for (int k = 0; k < kRounds; k++) {
+      if (k >= rounds) break;
+      if (rank[k] == 0xFFFFFFFFu) continue;
+      keys[base + rank[k]] = key[k];
+      ats[base + rank[k]] = (uint16_t)(i0 + k * 64 + lane);
+    }
+  }
+  uint32_t count = 0, start = 0, missing = 0;
+  for (int w = 0; w < 16; w++) {
+    count += totals[w];
+    start += before[w];
+    missing += none[w];
+  }
+  if (own == 0)   // the tokens without a row, after all others
+    for (uint32_t i = tid; i < missing; i += 1024) {
+      a.keys_out[n - missing + i] = v;
+      a.at_out[n - missing + i] = 0;
+    }
+  __syncthreads();
+  const int rounds = ((int)count + 1023) / 1024, i0 = wave * rounds * 64, n_here = min(max((int)count - i0, 0), rounds * 64);
 #pragma unroll
   for (int k = 0; k < kRounds; k++) {
-    const int i = i0 + k * 64 + lane;
-    key[k] = k * 64 + lane < n_here ? row_of(a.e, i) : 0u;
-    at[k] = (uint32_t)i;
+    if (k * 64 + lane >= n_here) continue;
+    key[k] = keys[i0 + k * 64 + lane];
+    at[k] = ats[i0 + k * 64 + lane];
   }
   for (int pass = 0; pass < a.passes; pass++) {
     const int shift = pass * kSortBits;
     for (int k = tid; k < 16 * kSortBins; k += 1024) bins[k / kSortBins][k % kSortBins] = 0;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kRounds; k++) {   // (as wave_ranks, up to the rounds there are)
+    for (int k = 0; k < kRounds; k++) {
       if (k >= rounds) break;
-      const bool here = k * 64 + lane < n_here;
-      const uint32_t digit = (key[k] >> shift) & (kSortBins - 1);
-      uint64_t same = __ballot(here);
-#pragma unroll
-      for (int b = 0; b < kSortBits; b++) {
-        const bool bit = (digit >> b) & 1;
-        const uint64_t m = __ballot(bit);
-        same &= bit ? m : ~m;
-      }
-      const uint64_t below = same & ((uint64_t(1) << lane) - 1);
-      rank[k] = here ? bins[wave][digit] + (uint32_t)__popcll(below) : 0u;
-      wave_lds_sync();
-      if (here && below == 0) bins[wave][digit] += (uint32_t)__popcll(same);
-      wave_lds_sync();
+      rank[k] = round_rank(key[k], k * 64 + lane < n_here, shift, bins[wave], lane);
     }
     __syncthreads();
     // exclusive scan in the order (digit, wave): a thread's digit over the waves, then the digits
@@ -205,8 +235,8 @@ __global__ __launch_bounds__(1024) void sort_alone_kernel(SortArgs a) {
       if (k * 64 + lane >= n_here) continue;
       const uint32_t to = bins[wave][(key[k] >> shift) & (kSortBins - 1)] + rank[k];
       if (last) {
-        a.keys_out[to] = key[k];
-        a.at_out[to] = at[k];
+        a.keys_out[start + to] = key[k];
+        a.at_out[start + to] = at[k];
       } else {
         keys[to] = key[k];
         ats[to] = (uint16_t)at[k];
@@ -226,39 +256,45 @@ __global__ __launch_bounds__(1024) void sort_alone_kernel(SortArgs a) {
 static_assert(kSortBins == 8 * 64, "the scan's digits are eight waves'");
 
 // More tokens, three launches a pass: counts by workgroup, an exclusive scan of them in
-// the order (digit, workgroup), then every item to its place.
-__global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a) {
+// the order (digit, workgroup), then every item to its place.  A workgroup of W waves
+// takes 512 W items.
+constexpr int kWaveRounds = 8;
+template <int W> __global__ __launch_bounds__(64 * W) void sort_count_kernel(SortArgs a) {
   __shared__ uint32_t bins[kSortBins];
   if ((int)blockIdx.x >= a.z.first) {
-    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    write_zeros<64 * W>(a.z, (int)blockIdx.x - a.z.first);
     return;
   }
   const int tid = threadIdx.x;
-  if (tid < kSortBins) bins[tid] = 0;
+  for (int k = tid; k < kSortBins; k += 64 * W) bins[k] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kSortItems;
+  const int64_t i0 = (int64_t)blockIdx.x * (64 * W * kWaveRounds);
 #pragma unroll
-  for (int k = 0; k < kSortItems / 1024; k++) {
-    const int64_t i = i0 + k * 1024 + tid;
+  for (int k = 0; k < kWaveRounds; k++) {
+    const int64_t i = i0 + k * 64 * W + tid;
     if (i < a.e.n) atomicAdd(&bins[(sort_key(a, i) >> a.shift) & (kSortBins - 1)], 1u);   // counts: any order
   }
   __syncthreads();
-  if (tid < kSortBins) a.hist[(int64_t)tid * a.blocks + blockIdx.x] = bins[tid];
+  for (int k = tid; k < kSortBins; k += 64 * W) a.hist[(int64_t)k * a.blocks + blockIdx.x] = bins[k];
 }
 
 // In place, one workgroup.
 __global__ __launch_bounds__(1024) void sort_scan_kernel(SortArgs a) {
   __shared__ uint32_t waves[16];
   if ((int)blockIdx.x >= a.z.first) {
-    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    write_zeros<1024>(a.z, (int)blockIdx.x - a.z.first);
     return;
   }
-  const int64_t n = (int64_t)kSortBins * a.blocks;
+  const int64_t n4 = (int64_t)kSortBins / 4 * a.blocks;   // four counts a thread
   const int tid = threadIdx.x, lane = tid & 63;
+  i32x4* hist = reinterpret_cast<i32x4*>(a.hist);
   uint32_t before = 0;
-  for (int64_t i0 = 0; i0 < n; i0 += 1024) {
-    const uint32_t own = i0 + tid < n ? a.hist[i0 + tid] : 0u;
-    uint32_t x = own;
+  i32x4 ahead = tid < n4 ? hist[tid] : i32x4{0, 0, 0, 0};
+  for (int64_t i0 = 0; i0 < n4; i0 += 1024) {
+    const i32x4 own = ahead;
+    if (i0 + 1024 < n4) ahead = i0 + 1024 + tid < n4 ? hist[i0 + 1024 + tid] : i32x4{0, 0, 0, 0};
+    const uint32_t sum = (uint32_t)(own[0] + own[1] + own[2] + own[3]);
+    uint32_t x = sum;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const uint32_t y = __shfl_up(x, o);
@@ -272,46 +308,50 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(SortArgs a) {
       if (w < tid >> 6) base += waves[w];
       total += waves[w];
     }
-    if (i0 + tid < n) a.hist[i0 + tid] = base + x - own;
+    i32x4 out;
+    out[0] = (int)(base + x - sum);
+#pragma unroll
+    for (int j = 1; j < 4; j++) out[j] = out[j - 1] + own[j - 1];
+    if (i0 + tid < n4) hist[i0 + tid] = out;
     before += total;
     __syncthreads();
   }
 }
 
-__global__ __launch_bounds__(1024) void sort_place_kernel(SortArgs a) {
-  constexpr int kRounds = kSortItems / 1024;
-  __shared__ uint32_t bins[16][kSortBins];
+template <int W> __global__ __launch_bounds__(64 * W) void sort_place_kernel(SortArgs a) {
+  __shared__ uint32_t bins[W][kSortBins];
   if ((int)blockIdx.x >= a.z.first) {
-    write_zeros(a.z, (int)blockIdx.x - a.z.first);
+    write_zeros<64 * W>(a.z, (int)blockIdx.x - a.z.first);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int k = tid; k < 16 * kSortBins; k += 1024) bins[k / kSortBins][k % kSortBins] = 0;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortItems + wave * (kSortItems / 16);
-  const int n_here = (int)min(max(a.e.n - i0, (int64_t)0), (int64_t)kSortItems / 16);
-  uint32_t key[kRounds], at[kRounds], rank[kRounds];
+  for (int k = tid; k < W * kSortBins; k += 64 * W) bins[k / kSortBins][k % kSortBins] = 0;
+  const int64_t i0 = (int64_t)(blockIdx.x * W + wave) * (64 * kWaveRounds);
+  const int n_here = (int)min(max(a.e.n - i0, (int64_t)0), (int64_t)64 * kWaveRounds);
+  uint32_t key[kWaveRounds], at[kWaveRounds], rank[kWaveRounds];
 #pragma unroll
-  for (int k = 0; k < kRounds; k++) {
+  for (int k = 0; k < kWaveRounds; k++) {
     const int64_t i = i0 + k * 64 + lane;
     const bool here = k * 64 + lane < n_here;
     key[k] = here ? sort_key(a, i) : 0u;
     at[k] = here && !a.first ? a.at[i] : (uint32_t)i;
   }
   __syncthreads();
-  wave_ranks<kRounds>(key, a.shift, n_here, bins[wave], lane, rank);
-  __syncthreads();
-  if (tid < kSortBins) {
-    uint32_t s = a.hist[(int64_t)tid * a.blocks + blockIdx.x];
 #pragma unroll
-    for (int w = 0; w < 16; w++) {
-      const uint32_t c = bins[w][tid];
-      bins[w][tid] = s;
+  for (int k = 0; k < kWaveRounds; k++) rank[k] = round_rank(key[k], k * 64 + lane < n_here, a.shift, bins[wave], lane);
+  __syncthreads();
+  for (int d = tid; d < kSortBins; d += 64 * W) {
+    uint32_t s = a.hist[(int64_t)d * a.blocks + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+      const uint32_t c = bins[w][d];
+      bins[w][d] = s;
       s += c;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kRounds; k++) {
+  for (int k = 0; k < kWaveRounds; k++) {
     if (k * 64 + lane >= n_here) continue;
     const uint32_t to = bins[wave][(key[k] >> a.shift) & (kSortBins - 1)] + rank[k];
     a.keys_out[to] = key[k];
@@ -323,7 +363,7 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(SortArgs a) {
 // Sums of runs
 // ---------------------------------------------------------------------------
 struct RunArgs {
-  const uint32_t* keys;        // sorted; tokens without a row last
+  const uint32_t* keys;        // equal ones next to each other; tokens without a row last
   const uint32_t* at;
   int64_t n, v;
   int h, chunk;
@@ -352,57 +392,82 @@ __device__ __forceinline__ void put_row(const RunArgs& a, uint32_t row, int c, c
   *to = o;
 }
 
+// VEC elements as they are loaded, in a register type: 16 bytes, or one element as its value.
+template <typename T, int VEC> struct Loaded {
+  i32x4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const i32x4*>(p); }
+  __device__ __forceinline__ float get(int j) const {
+    typedef T V __attribute__((ext_vector_type(VEC)));
+    return (float)__builtin_bit_cast(V, raw)[j];
+  }
+};
+template <typename T> struct Loaded<T, 1> {
+  float raw;
+  __device__ __forceinline__ void load(const T* p) { raw = (float)*p; }
+  __device__ __forceinline__ float get(int) const { return raw; }
+};
+
 // One chunk of sorted tokens by 256 VEC columns; the rows of kAhead tokens are in flight at a time.
-constexpr int kAhead = 8;
+constexpr int kAhead = 8;   // divides 64
 template <typename T, typename O, int VEC> __global__ __launch_bounds__(256) void embed_runs_kernel(RunArgs a) {
-  typedef T V __attribute__((ext_vector_type(VEC)));
   const int64_t chunk = blockIdx.x, i0 = chunk * a.chunk, i1 = min(i0 + a.chunk, a.n);
-  const int c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * VEC;
+  const int lane = threadIdx.x & 63, c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * VEC;
   uint32_t key = a.keys[i0];
-  if (c >= a.h || key >= a.v) return;
+  // whole waves only: a lane past the row's end holds tokens for the others (and reads the row's last piece)
+  if (c - lane * VEC >= a.h || key >= a.v) return;
+  const bool in = c < a.h;
+  const int c_read = min(c, a.h - VEC);
   float s[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; j++) s[j] = 0.0f;
   bool inner = i0 == 0 || a.keys[i0 - 1] != key;   // the run began here
-  for (int64_t i = i0; i < i1; i += kAhead) {
-    V g[kAhead];
-    uint32_t next[kAhead];
+  for (int64_t i = i0; i < i1; i += 64) {
+    // a lane's token and the key after its own, for the wave's scalar registers
+    const int64_t mine = min(i + lane, i1 - 1);   // past the chunk's end its last token again, not added
+    const int at = (int)a.at[mine], after = (int)(mine + 1 < a.n ? a.keys[mine + 1] : (uint32_t)a.v);
+    const int here = (int)min(i1 - i, (int64_t)64);
+    for (int b = 0; b < here; b += kAhead) {
+      Loaded<T, VEC> g[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; k++) {
-      const int64_t at = min(i + k, i1 - 1);   // past the chunk's end its last token again, not added
-      next[k] = at + 1 < a.n ? a.keys[at + 1] : (uint32_t)a.v;
-      g[k] = *reinterpret_cast<const V*>(static_cast<const T*>(a.grad) + (int64_t)a.at[at] * a.h + c);
-    }
+      for (int k = 0; k < kAhead; k++)
+        g[k].load(static_cast<const T*>(a.grad) + (int64_t)(uint32_t)__builtin_amdgcn_readlane(at, b + k) * a.h + c_read);
+      // (else the compiler moves each load down to its use, and they wait for memory one after the other)
 #pragma unroll
-    for (int k = 0; k < kAhead; k++) {
-      if (i + k >= i1 || key >= a.v) return;
+      for (int k = 0; k < kAhead; k++) asm volatile("" : "+v"(g[k].raw));
 #pragma unroll
-      for (int j = 0; j < VEC; j++) s[j] += (float)g[k][j];
-      if (next[k] == key && i + k + 1 < i1) continue;
-      if (inner && next[k] != key) {
-        put_row<O, VEC>(a, key, c, s);
-      } else {
-        float* p = a.part + ((inner ? a.n_chunks : 0) + chunk) * a.h + c;
+      for (int k = 0; k < kAhead; k++) {
+        if (b + k >= here || key >= a.v) return;
 #pragma unroll
-        for (int j = 0; j < VEC; j++) p[j] = s[j];
+        for (int j = 0; j < VEC; j++) s[j] += g[k].get(j);
+        const uint32_t next = (uint32_t)__builtin_amdgcn_readlane(after, b + k);
+        if (next == key && i + b + k + 1 < i1) continue;
+        if (inner && next != key) {
+          if (in) put_row<O, VEC>(a, key, c, s);
+        } else if (in) {
+          float* p = a.part + ((inner ? a.n_chunks : 0) + chunk) * a.h + c;
+#pragma unroll
+          for (int j = 0; j < VEC; j++) p[j] = s[j];
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; j++) s[j] = 0.0f;
+        key = next;
+        inner = true;
       }
-#pragma unroll
-      for (int j = 0; j < VEC; j++) s[j] = 0.0f;
-      key = next[k];
-      inner = true;
     }
   }
 }
 
-// Runs that begin in a chunk and end in another, by 256 columns.
-template <typename O> __global__ __launch_bounds__(256) void embed_join_kernel(RunArgs a) {
+// Runs that begin in a chunk and end in another, by 64 VEC columns: the parts in four ranges, a wave each.
+template <typename O, int VEC> __global__ __launch_bounds__(256) void embed_join_kernel(RunArgs a) {
+  typedef float V __attribute__((ext_vector_type(VEC)));
+  __shared__ V sums[4][64];
   const int64_t chunk = blockIdx.x, i0 = chunk * a.chunk, i1 = i0 + a.chunk;
   if (i1 >= a.n) return;
   const uint32_t key = a.keys[i1 - 1];
   if (key >= a.v || a.keys[i1] != key) return;
   if (i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key) return;   // begun before
   // the chunks after it that begin with the same key: a lane looks at each
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t last = chunk + 1;
   for (;;) {
     const int64_t k = last + 1 + lane;
@@ -411,17 +476,31 @@ template <typename O> __global__ __launch_bounds__(256) void embed_join_kernel(R
     last += more;
     if (more < 64) break;
   }
-  const int c = (int)blockIdx.y * 256 + (int)threadIdx.x;
-  if (c >= a.h) return;
-  float s[1] = {a.part[(a.n_chunks + chunk) * a.h + c]};
-  for (int64_t k = chunk + 1; k <= last; k += 8) {
-    float p[8];
+  const int c = ((int)blockIdx.y * 64 + lane) * VEC, at = min(c, a.h - VEC);
+  // part 0 is this chunk's own, the others' follow
+  const int64_t parts = last - chunk + 1, p0 = parts * wave / 4, p1 = parts * (wave + 1) / 4;
+  V s;
 #pragma unroll
-    for (int j = 0; j < 8; j++) p[j] = a.part[min(k + j, last) * a.h + c];
+  for (int j = 0; j < VEC; j++) s[j] = 0.0f;
+  for (int64_t p = p0; p < p1; p += 8) {
+    V v[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) s[0] += k + j <= last ? p[j] : 0.0f;
+    for (int k = 0; k < 8; k++) {   // eight in flight; past the last one it again, not added
+      const int64_t q = min(p + k, p1 - 1);
+      v[k] = *reinterpret_cast<const V*>(a.part + ((q == 0 ? a.n_chunks : q) + chunk) * a.h + at);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (p + k < p1) s += v[k];
   }
-  put_row<O, 1>(a, key, c, s);
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || c >= a.h) return;
+  const V all = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+  float out[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) out[j] = all[j];
+  put_row<O, VEC>(a, key, c, out);
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -430,7 +509,17 @@ void plan_embedding_backward(EmbedPlan* p) {
   int bits = 1;
   while ((p->v >> bits) != 0) bits++;      // of the key v
   p->passes = (bits + kSortBits - 1) / kSortBits;
-  p->sort_blocks = p->n <= kSortAlone ? 0 : (int)((p->n + kSortItems - 1) / kSortItems);
+  p->sort_parts = p->sort_blocks = 0;
+  if (p->n <= kSortAlone) {
+    const int64_t parts = (p->n + 511) / 512;
+    p->sort_parts = (int)(parts < 32 ? parts : 32);
+  } else {
+    // small workgroups: 32768 tokens' last launch of a pass took 17 us by workgroups of 16 waves.  The scan, one
+    // workgroup's, has a count for each digit and workgroup.
+    p->sort_waves = p->n <= (1 << 18) ? 4 : 16;
+    const int64_t items = 64 * kWaveRounds * p->sort_waves;
+    p->sort_blocks = (int)((p->n + items - 1) / items);
+  }
   p->chunk = p->n <= 16384 ? 16 : 32;
   while (p->chunk < (1 << 20) && p->n / p->chunk > 4096) p->chunk *= 2;
   p->n_chunks = (p->n + p->chunk - 1) / p->chunk;
@@ -493,7 +582,10 @@ template <typename T, typename O> static void embed_runs_t(const EmbedPlan& p, c
   const dim3 grid((unsigned)p.n_chunks, (unsigned)((p.h + per - 1) / per));
   if (vec) embed_runs_kernel<T, O, kVec><<<grid, 256, 0, st>>>(a);
   else embed_runs_kernel<T, O, 1><<<grid, 256, 0, st>>>(a);
-  embed_join_kernel<O><<<dim3((unsigned)p.n_chunks, (unsigned)((p.h + 255) / 256)), 256, 0, st>>>(a);
+  if (p.h % 4 == 0 && (reinterpret_cast<uintptr_t>(a.gw) & (4 * sizeof(O) - 1)) == 0)
+    embed_join_kernel<O, 4><<<dim3((unsigned)p.n_chunks, (unsigned)((p.h + 255) / 256)), 256, 0, st>>>(a);
+  else
+    embed_join_kernel<O, 1><<<dim3((unsigned)p.n_chunks, (unsigned)((p.h + 63) / 64)), 256, 0, st>>>(a);
 }
 
 template <typename T> static void embed_runs_o(const EmbedPlan& p, const RunArgs& a, hipStream_t st) {
@@ -526,12 +618,13 @@ hipError_t launch_embedding_backward(const EmbedPlan& p, const void* ids, const 
     return (unsigned)(sorting + (n < 65536 ? n : 65536));
   };
   s.passes = p.passes;
+  s.parts = p.sort_parts;
   if (alone) {
     s.first = 1;
     s.keys_out = reinterpret_cast<uint32_t*>(ws + p.w_keys[0]);
     s.at_out = reinterpret_cast<uint32_t*>(ws + p.w_at[0]);
-    const unsigned blocks = blocks_with_zeros(p.n > 0 ? 1 : 0);
-    if (blocks > 0) sort_alone_kernel<<<blocks, 1024, 0, st>>>(s);
+    const unsigned blocks = blocks_with_zeros(p.sort_parts);
+    if (blocks > 0) sort_parts_kernel<<<blocks, 1024, 0, st>>>(s);
   } else {
     s.hist = reinterpret_cast<uint32_t*>(ws + p.w_hist);
     s.blocks = p.sort_blocks;
@@ -544,11 +637,13 @@ hipError_t launch_embedding_backward(const EmbedPlan& p, const void* ids, const 
       s.keys_out = reinterpret_cast<uint32_t*>(ws + p.w_keys[to]);
       s.at_out = reinterpret_cast<uint32_t*>(ws + p.w_at[to]);
       unsigned blocks = blocks_with_zeros(p.sort_blocks);
-      sort_count_kernel<<<blocks, 1024, 0, st>>>(s);
+      if (p.sort_waves == 4) sort_count_kernel<4><<<blocks, 256, 0, st>>>(s);
+      else sort_count_kernel<16><<<blocks, 1024, 0, st>>>(s);
       blocks = blocks_with_zeros(1);
       sort_scan_kernel<<<blocks, 1024, 0, st>>>(s);
       blocks = blocks_with_zeros(p.sort_blocks);
-      sort_place_kernel<<<blocks, 1024, 0, st>>>(s);
+      if (p.sort_waves == 4) sort_place_kernel<4><<<blocks, 256, 0, st>>>(s);
+      else sort_place_kernel<16><<<blocks, 1024, 0, st>>>(s);
     }
   }
   if (p.n == 0) return hipGetLastError();
