@@ -19,7 +19,10 @@ _SAME_DEVICE = contextlib.nullcontext()
 def on_device(device):
     """The library launches on the current device: makes it the tensors'."""
     import torch
-    if device.index is None or device.index == torch.cuda.current_device():
+    # (current_device() asks the same after looking whether the runtime is up, which it is where there are tensors: 4 us
+    # in a backward's thread)
+    current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if device.index is None or device.index == current():
         return _SAME_DEVICE
     return torch.cuda.device(device)
 
