@@ -34,6 +34,7 @@ from typing import Optional
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "libflce.so")
+TORCH_LIB_PATH = os.path.join(_PKG_DIR, "libflce_torch.so")
 
 FLCE_OK = 0
 FLCE_ERR_INVALID_ARG = -1
@@ -304,6 +305,26 @@ def load(path: Optional[str] = None):
     lib.flce_embedding_backward.restype = ctypes.c_int
     _lib = lib
     return lib
+
+
+_torch_ops = None
+
+
+def torch_ops():
+    """The operators of libflce_torch.so (autograd nodes in C++), bound to the library that load() loaded."""
+    global _torch_ops
+    if _torch_ops is None:
+        import torch
+        lib = load()
+        if not os.path.exists(TORCH_LIB_PATH):
+            raise FileNotFoundError(
+                f"{TORCH_LIB_PATH} is missing: build it with `python -m linear_cross_entropy_tiled_amd.build`")
+        torch.ops.load_library(TORCH_LIB_PATH)
+        torch.ops.flce._bind([ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "flce_layer_norm_forward", "flce_layer_norm_backward", "flce_embedding_forward", "flce_embedding_backward",
+            "flce_status_string")])
+        _torch_ops = torch.ops.flce
+    return _torch_ops
 
 
 # ----------------------------------------------------------------------------- raw C entry points

@@ -1,4 +1,5 @@
-"""Builds libflce.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Builds libflce.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and libflce_torch.so
+(autograd nodes over the C ABI, host code against the installed PyTorch) with the host compiler.
 
     python -m linear_cross_entropy_tiled_amd.build [--verbose] [--host-sanitizers]
 
@@ -28,6 +29,7 @@ SOURCES = ["flce_api.hip", "flce_forward.hip", "flce_backward.hip", "flce_chunke
            "flce_noalloc.hip", "flce_logprobs.hip", "flce_small.hip", "flce_mx.hip", "flce_mx_tiles.hip",
            "flce_align.hip", "flce_align_api.hip", "flce_norm.hip", "flce_embed.hip",
            "flce_ends_api.hip"]
+TORCH_LIB_PATH = os.path.join(PKG_DIR, "libflce_torch.so")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -46,6 +48,26 @@ def hipcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found (ROCm is required to build libflce.so)")
+
+
+def build_torch(verbose: bool = False) -> str:
+    """libflce_torch.so.  It links nothing of libflce.so: the package hands it the entry points of the one it loaded."""
+    import torch
+    from torch.utils import cpp_extension
+    cxx = os.environ.get("CXX") or shutil.which("g++") or hipcc()
+    out = TORCH_LIB_PATH + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",           # what PyTorch's own headers ask for
+           *(f"-I{p}" for p in cpp_extension.include_paths("cuda")), os.path.join(CSRC, "flce_torch.cpp"), "-o", out,
+           *(f"-L{p}" for p in cpp_extension.library_paths("cuda")), "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        print(r.stdout.decode(errors="replace"), file=sys.stderr)
+        raise RuntimeError("compiling libflce_torch.so failed")
+    os.replace(out, TORCH_LIB_PATH)
+    return TORCH_LIB_PATH
 
 
 SAN_LIB_PATH = os.path.join(PKG_DIR, "libflce_hostsan.so")
@@ -117,3 +139,4 @@ if __name__ == "__main__":
         print(build_host_sanitized(verbose="--verbose" in sys.argv))
     else:
         print(build(verbose="--verbose" in sys.argv))
+        print(build_torch(verbose="--verbose" in sys.argv))

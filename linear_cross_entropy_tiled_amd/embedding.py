@@ -1,4 +1,5 @@
-"""Token embedding: the torch side of flce_embedding_* (include/flce.h has the formulas)."""
+"""Token embedding: the torch side of flce_embedding_* (include/flce.h has the formulas).  The autograd node is C++
+(csrc/flce_torch.cpp)."""
 from __future__ import annotations
 
 import functools
@@ -6,8 +7,8 @@ import math
 from typing import Optional
 
 from . import (DTYPES, FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32, _dtype_name, _ptr, flce_embedding_backward,
-               flce_embedding_forward, flce_embedding_params, flce_embedding_workspace_size)
-from .logprobs import differentiable, first_order, on_device, raise_for, stream_handle
+               flce_embedding_params, flce_embedding_workspace_size, torch_ops)
+from .logprobs import has_tangent, on_device, raise_for, stream_handle
 
 
 @functools.lru_cache(maxsize=1024)
@@ -55,33 +56,9 @@ def _run_backward(p, ids, grad, grad_weight):
     return grad_weight
 
 
-def _forward(p, ids, weight):
-    dev = weight.device
-    with on_device(dev):
-        out = weight.new_empty((p.n_tokens, p.hidden))
-        raise_for(flce_embedding_forward(p, _ptr(ids), _ptr(weight), _ptr(out), stream_handle(dev)),
-                  "flce_embedding_forward")
-    return out
-
-
 @functools.lru_cache(maxsize=None)
-def _function():
-    import torch
-
-    class Embedding(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, weight, ids, p):
-            ctx.save_for_backward(ids)
-            ctx.p = p
-            return _forward(p, ids, weight)
-
-        @first_order
-        def backward(ctx, g):
-            ids, = ctx.saved_tensors
-            g = g.contiguous()
-            return _run_backward(ctx.p, ids, g, g.new_empty((ctx.p.vocab, ctx.p.hidden))), None, None
-
-    return Embedding
+def _op():
+    return torch_ops()._embedding.default
 
 
 def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100):
@@ -90,16 +67,16 @@ def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100):
     ids (N,) are int64 or int32.  A token whose id is ``ignore_index``, or no row of weight, gives 0 and takes no
     gradient (so a slice of the vocabulary may be looked up with ``ids - first``).  The gradient is a whole (V, H)
     tensor; ``embedding_backward`` adds it to one that is there, as for a head that shares the weight."""
-    flags = _check_ids(ids)
+    _check_ids(ids)
     if weight.dim() != 2 or 0 in weight.shape:
         raise ValueError(f"weight must be 2-D and not empty, got {tuple(weight.shape)}")
-    dtype = DTYPES[_dtype_name(weight)]
+    _dtype_name(weight)
     _check_scale(scale)
     _check_places([("ids", ids), ("weight", weight)])
-    p = _params(ids.shape[0], weight.shape[1], weight.shape[0], int(ignore_index), dtype, dtype, flags, float(scale))
-    if differentiable(weight):
-        return _function().apply(weight, ids, p)
-    return _forward(p, ids, weight)
+    workspace = _workspace(ids.shape[0], weight.shape[1], weight.shape[0])
+    if has_tangent(weight):
+        raise NotImplementedError("embedding has no forward-mode derivative")
+    return _op()(ids, weight, float(scale), int(ignore_index), workspace)
 
 
 def embedding_backward(grad, ids, vocab: int, *, scale: float = 1.0, ignore_index: int = -100,

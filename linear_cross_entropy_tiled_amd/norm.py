@@ -1,12 +1,12 @@
-"""Layer norm of hidden states: the torch side of flce_layer_norm_* (include/flce.h has the formulas)."""
+"""Layer norm of hidden states: the torch side of flce_layer_norm_* (include/flce.h has the formulas).  The autograd
+node is C++ (csrc/flce_torch.cpp)."""
 from __future__ import annotations
 
 import functools
 import math
 
-from . import (DTYPES, _dtype_name, _ptr, flce_layer_norm_backward, flce_layer_norm_forward,
-               flce_layer_norm_workspace_size, flce_norm_params)
-from .logprobs import differentiable, first_order, on_device, raise_for, stream_handle
+from . import DTYPES, _dtype_name, flce_layer_norm_workspace_size, flce_norm_params, torch_ops
+from .logprobs import has_tangent
 
 
 def rows_apart(t):
@@ -20,13 +20,9 @@ def row_stride(t):
 
 
 @functools.lru_cache(maxsize=1024)
-def _params(rows, cols, ld_x, ld_grad, dtype, param_dtype, eps):
-    return flce_norm_params(rows, cols, ld_x, ld_grad, dtype, param_dtype, eps, 0)
-
-
-@functools.lru_cache(maxsize=1024)
-def _workspace(rows, cols):
-    return flce_layer_norm_workspace_size(flce_norm_params(rows, cols, 0, 0, 0, 0, 0.0, 0))
+def _workspace(rows, cols, ld_x, dtype, param_dtype, eps):
+    """Bytes of the backward's workspace; refuses what the C entry points would."""
+    return flce_layer_norm_workspace_size(flce_norm_params(rows, cols, ld_x, 0, dtype, param_dtype, eps, 0))
 
 
 def _check_vector(t, name, x, h):
@@ -40,7 +36,7 @@ def _check_vector(t, name, x, h):
 
 
 def _check(x, weight, bias, eps):
-    """Types, shapes, layout and device.  The kernels trust all of them.  Returns the call's parameters."""
+    """Types, shapes, layout and device.  The kernels trust all of them.  Returns the backward's workspace size."""
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
     dtype = param_dtype = DTYPES[_dtype_name(x)]
@@ -65,57 +61,12 @@ def _check(x, weight, bias, eps):
     for name, t in (("x", x), ("weight", weight), ("bias", bias)):
         if t is not None and (not t.is_cuda or t.device != dev):
             raise ValueError(f"{name} must be on x's GPU ({dev}), not {t.device}")
-    return _params(n, h, row_stride(x), 0, dtype, param_dtype, eps)
-
-
-def _forward(p, x, weight, bias, keep):
-    import torch
-    dev = x.device
-    with on_device(dev):
-        y = x.new_empty(x.shape)
-        stats = torch.empty((2, p.rows), dtype=torch.float32, device=dev) if keep else None
-        at = _ptr(stats)
-        raise_for(flce_layer_norm_forward(p, x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), at,
-                                          at + 4 * p.rows if keep else None, stream_handle(dev)),
-                  "flce_layer_norm_forward")
-    return y, stats
+    return _workspace(n, h, row_stride(x), dtype, param_dtype, eps)
 
 
 @functools.lru_cache(maxsize=None)
-def _function():
-    import torch
-
-    class LayerNorm(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, weight, bias, p):
-            y, stats = _forward(p, x, weight, bias, True)
-            ctx.save_for_backward(x, weight, bias, stats)
-            ctx.p = p
-            return y
-
-        @first_order
-        def backward(ctx, g):
-            x, weight, bias, stats = ctx.saved_tensors
-            p, dev = ctx.p, x.device
-            if not g.is_contiguous():
-                if rows_apart(g):
-                    p = _params(p.rows, p.cols, p.ld_x, row_stride(g), p.dtype, p.param_dtype, p.eps)
-                else:
-                    g = g.contiguous()
-            need_x, need_w, need_b, _ = ctx.needs_input_grad
-            with on_device(dev):
-                gx = x.new_empty(x.shape) if need_x else None
-                gw = torch.empty_like(weight) if need_w else None
-                gb = torch.empty_like(bias) if need_b else None
-                ws_bytes = _workspace(p.rows, p.cols) if need_w or need_b else 0
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-                at = stats.data_ptr()
-                raise_for(flce_layer_norm_backward(p, x.data_ptr(), _ptr(weight), at, at + 4 * p.rows, g.data_ptr(),
-                                                   _ptr(gx), _ptr(gw), _ptr(gb), _ptr(workspace), ws_bytes,
-                                                   stream_handle(dev)), "flce_layer_norm_backward")
-            return gx, gw, gb, None
-
-    return LayerNorm
+def _op():
+    return torch_ops()._layer_norm.default
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
@@ -124,7 +75,8 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
 
     weight and bias (H,) are of x's dtype or both fp32; without them ones and zeros.  Rows of x are contiguous, at
     any distance.  H may be any size up to 2^20; rows of whole 16-byte pieces run faster."""
-    p = _check(x, weight, bias, float(eps))
-    if differentiable(x, weight, bias):
-        return _function().apply(x, weight, bias, p)
-    return _forward(p, x, weight, bias, False)[0]
+    eps = float(eps)
+    workspace = _check(x, weight, bias, eps)
+    if has_tangent(x, weight, bias):
+        raise NotImplementedError("layer_norm has no forward-mode derivative")
+    return _op()(x, weight, bias, eps, workspace)

@@ -162,6 +162,28 @@ def test_gradient_along_differences(flce_lib):
     assert abs(slope - (grad * v).sum()) <= (tol * np.abs(v)).sum() + 1e-9 * np.abs(grad * v).sum()
 
 
+def test_no_second_derivative(flce_lib):
+    import torch
+    ids, w, g = problem(30, 8, 12, "float32", seed=3)
+    ids, w, g = ids.cuda(), w.cuda().requires_grad_(True), torch.nan_to_num(g).cuda().requires_grad_(True)
+    want, = torch.autograd.grad(flce_lib.embedding(ids, w), w, g)
+    got, = torch.autograd.grad(flce_lib.embedding(ids, w), w, g, create_graph=True)
+    assert torch.equal(got, want)
+    with pytest.raises(RuntimeError):
+        got.sum().backward()
+    with torch.no_grad():
+        assert not flce_lib.embedding(ids, w).requires_grad
+
+
+def test_non_contiguous_upstream_gradient(flce_lib):
+    import torch
+    ids, w, _ = problem(50, 24, 30, "float32", seed=6)
+    leaf = w.cuda().requires_grad_(True)
+    flce_lib.embedding(ids.cuda(), leaf).sum().backward()
+    want, tol = grad_bound(ids.numpy(), 30, np.ones((50, 24)), 1.0, "float32")
+    assert np.all(np.abs(np64(leaf.grad) - want) <= tol)
+
+
 def test_repeats_are_bitwise_equal_on_another_stream(flce_lib):
     import torch
     ids, w, g = problem(20000, 64, 500, "bfloat16", seed=7)

@@ -201,6 +201,45 @@ def test_gradients_along_differences(flce_lib):
         assert abs(slope - (np64(grad) * v).sum()) <= tol
 
 
+def test_no_second_derivative(flce_lib):
+    """create_graph gives the same gradients; differentiating them is refused, not answered with zeros."""
+    import torch
+    x, w, b, g = (t.cuda() for t in problem(5, 40, "float32", "float32"))
+    leaves = [t.requires_grad_(True) for t in (x, w, b)]
+    want = torch.autograd.grad(flce_lib.layer_norm(*leaves), leaves, g)
+    got = torch.autograd.grad(flce_lib.layer_norm(*leaves), leaves, g, create_graph=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    with pytest.raises(RuntimeError):
+        got[0].sum().backward()
+
+
+def test_backward_twice_and_retained(flce_lib):
+    import torch
+    x, w, b, g = (t.cuda() for t in problem(30, 64, "float32", "float32"))
+    leaves = [t.requires_grad_(True) for t in (x, w, b)]
+    y = flce_lib.layer_norm(*leaves)
+    first = torch.autograd.grad(y, leaves, g, retain_graph=True)
+    assert all(torch.equal(p, q) for p, q in zip(torch.autograd.grad(y, leaves, g), first))
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, leaves, g)
+    y = flce_lib.layer_norm(*leaves)
+    with torch.no_grad():
+        x.add_(1)                                            # what the backward needs is gone
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, leaves, g)
+
+
+def test_under_no_grad_and_inference_mode(flce_lib):
+    import torch
+    x, w, b, _ = (t.cuda() for t in problem(9, 72, "bfloat16", "float32"))
+    want = flce_lib.layer_norm(x, w, b)
+    x.requires_grad_(True)
+    with torch.no_grad():
+        assert torch.equal(flce_lib.layer_norm(x, w, b), want) and not flce_lib.layer_norm(x, w, b).requires_grad
+    with torch.inference_mode():
+        assert torch.equal(flce_lib.layer_norm(x, w, b), want)
+
+
 def test_repeats_are_bitwise_equal_on_another_stream(flce_lib):
     import torch
     x, w, b, g = (t.cuda() for t in problem(1500, 512, "bfloat16", "float32"))
