@@ -1,6 +1,6 @@
 // Small-tile matrix loop, for problems that give the 256 x 256 loop of
 // flce_device.h too few tiles for the chip: C[64 x BN] += A[64 x K] . B[BN x K]^T
-// by 4 waves, BN 64 (2 x 2 waves of 32 x 32) or 16 (4 x 1 waves of 16 x 16).
+// by 4 waves, BN 64 (2 x 2 waves of 32 x 32), 32 (2 x 2 waves of 32 x 16; MXFP4 only) or 16 (4 x 1 waves of 16 x 16).
 //
 // Operands, fragments and accumulator layout are those of the large loop (stages of
 // 128 bytes of K per row, K-major or M/N-major); n stage buffers keep n - 1 stages of
@@ -24,12 +24,12 @@ constexpr int kStageA = kBMs * kBKB;                             // 8 KiB
 // workgroup is worth 5%.  Four at BN 16 (40 KiB, 42 with the sides), three workgroups as
 // well: 4 tokens at V = 128256 in 8 bits took 114 us, with three buffers 136, with five
 // within 2% of four.
-template <typename T> constexpr int stages(int bn) { return bn == 16 ? 4 : (sizeof(T) == 4 ? 2 : 3); }
+template <typename T> constexpr int stages(int bn) { return bn <= 32 ? 4 : (sizeof(T) == 4 ? 2 : 3); }
 constexpr int stage_bytes(int bn) { return (kBMs + bn) * kBKB; }
 template <typename T> constexpr int lds_bytes(int bn) { return stages<T>(bn) * stage_bytes(bn); }
 
 template <int BN> struct Shape {
-  static constexpr int WM = BN == 64 ? 2 : 4, WN = 4 / WM;       // waves
+  static constexpr int WM = BN == 16 ? 4 : 2, WN = 4 / WM;       // waves
   static constexpr int MI = kBMs / 16 / WM, NI = BN / 16 / WN;   // 16 x 16 tiles per wave
 };
 

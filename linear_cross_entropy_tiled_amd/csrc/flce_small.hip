@@ -482,7 +482,8 @@ template <typename T> static void lp_small_bn(const Plan& pl, int bn, const LpTi
   else lp_small_t<T, 64>(pl, a, n_tt, st);
 }
 void launch_lp_small(const Plan& pl, int bn, const LpTileArgs& a, int n_tt, hipStream_t st) {
-  if (pl.mx) lp_small_bn<mx4>(pl, bn, a, n_tt, st);
+  if (pl.mx && bn == 32) lp_small_t<mx4, 32>(pl, a, n_tt, st);
+  else if (pl.mx) lp_small_bn<mx4>(pl, bn, a, n_tt, st);
   else if (pl.int8) lp_small_bn<int8_t>(pl, bn, a, n_tt, st);
   else if (pl.dtype == FLCE_BF16) lp_small_bn<bf16>(pl, bn, a, n_tt, st);
   else if (pl.dtype == FLCE_F16) lp_small_bn<f16>(pl, bn, a, n_tt, st);
