@@ -28,25 +28,30 @@ __device__ __forceinline__ uint32_t row_of(const EmbedArgs& a, int64_t i) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward: one wave a token, VEC elements (16 bytes, or 1 where rows are not aligned) a lane
+// Forward: one wave a token, VEC elements (16 bytes, or 1 where rows are not aligned) a lane,
+// kPieces of them in flight
 // ---------------------------------------------------------------------------
 template <typename T, int VEC> __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedArgs a) {
   typedef T V __attribute__((ext_vector_type(VEC)));
+  constexpr int kPieces = 8;
   const int lane = threadIdx.x & 63;
   for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < a.n; i += (int64_t)gridDim.x * 4) {
     const uint32_t r = row_of(a, i);
-    const T* w = static_cast<const T*>(a.weight) + (int64_t)r * a.h;
+    const bool there = r < a.v;
+    const T* w = static_cast<const T*>(a.weight) + (there ? (int64_t)r * a.h : 0);
     T* out = static_cast<T*>(a.out) + i * a.h;
-    for (int c = lane * VEC; c < a.h; c += 64 * VEC) {
-      V x;
+    for (int c0 = lane * VEC; c0 < a.h; c0 += kPieces * 64 * VEC) {
+      V x[kPieces];
 #pragma unroll
-      for (int j = 0; j < VEC; j++) x[j] = (T)0.0f;
-      if (r < a.v) {
-        x = *reinterpret_cast<const V*>(w + c);
+      for (int k = 0; k < kPieces; k++) x[k] = *reinterpret_cast<const V*>(w + min(c0 + k * 64 * VEC, a.h - VEC));
 #pragma unroll
-        for (int j = 0; j < VEC; j++) x[j] = (T)((float)x[j] * a.scale);
+      for (int k = 0; k < kPieces; k++) {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) x[k][j] = there ? (T)((float)x[k][j] * a.scale) : (T)0.0f;
       }
-      *reinterpret_cast<V*>(out + c) = x;
+#pragma unroll
+      for (int k = 0; k < kPieces; k++)
+        if (c0 + k * 64 * VEC < a.h) *reinterpret_cast<V*>(out + c0 + k * 64 * VEC) = x[k];
     }
   }
 }
