@@ -311,7 +311,7 @@ _torch_ops = None
 
 
 def torch_ops():
-    """The operators of libflce_torch.so (autograd nodes in C++), bound to the library that load() loaded."""
+    """The operators of libflce_torch.so, bound to the library that load() loaded."""
     global _torch_ops
     if _torch_ops is None:
         import torch
@@ -322,7 +322,7 @@ def torch_ops():
         torch.ops.load_library(TORCH_LIB_PATH)
         torch.ops.flce._bind([ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "flce_layer_norm_forward", "flce_layer_norm_backward", "flce_embedding_forward", "flce_embedding_backward",
-            "flce_status_string")])
+            "flce_quantize_mxfp4", "flce_dequantize_mxfp4", "flce_logprobs_mxfp4", "flce_status_string")])
         _torch_ops = torch.ops.flce
     return _torch_ops
 

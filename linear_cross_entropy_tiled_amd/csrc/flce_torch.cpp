@@ -1,11 +1,14 @@
-// The autograd side of layer_norm and embedding for PyTorch: two operators whose nodes are
-// C++.  Argument checks stand in the Python functions in front of them (norm.py,
-// embedding.py); the work is that of the C ABI, whose entry points are handed over by
-// address once, so that this library runs on whichever build of libflce.so is loaded.
+// The PyTorch side of layer_norm and embedding, operators whose autograd nodes are C++, and
+// of the MXFP4 calls.  Argument checks stand in the Python functions in front of them
+// (norm.py, embedding.py, logprobs.py); the work is that of the C ABI, whose entry points are
+// handed over by address once, so that this library runs on whichever build of libflce.so
+// is loaded.
 //
 // Why not a Python autograd function, as the other operators have: autograd runs a GPU
 // node's backward on a thread of its own, and Python that wakes up there runs at half its
 // speed.  A layer norm training step of 515 x 1023 took 115 us that way and takes 76 so, of which 15 are the GPU's.
+// The MXFP4 calls have no node; their few microseconds of GPU time wait for allocations and argument lists in Python
+// (250 x 4096 values to 4 bits and back: 18.7 us, 7 of them the GPU's).
 #include <ATen/ATen.h>
 #include <ATen/hip/impl/HIPGuardImplMasqueradingAsCUDA.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
@@ -14,6 +17,7 @@
 #include <torch/library.h>
 
 #include <optional>
+#include <tuple>
 
 #include "../../include/flce.h"
 
@@ -28,16 +32,22 @@ struct EntryPoints {
   decltype(&flce_layer_norm_backward) norm_backward = nullptr;
   decltype(&flce_embedding_forward) embedding_forward = nullptr;
   decltype(&flce_embedding_backward) embedding_backward = nullptr;
+  decltype(&flce_quantize_mxfp4) quantize = nullptr;
+  decltype(&flce_dequantize_mxfp4) dequantize = nullptr;
+  decltype(&flce_logprobs_mxfp4) scores = nullptr;
   decltype(&flce_status_string) status_string = nullptr;
 } g;
 
 void bind(at::IntArrayRef at) {
-  TORCH_CHECK(at.size() == 5, "five entry points are expected");
+  TORCH_CHECK(at.size() == 8, "eight entry points are expected");
   g.norm_forward = reinterpret_cast<decltype(g.norm_forward)>(at[0]);
   g.norm_backward = reinterpret_cast<decltype(g.norm_backward)>(at[1]);
   g.embedding_forward = reinterpret_cast<decltype(g.embedding_forward)>(at[2]);
   g.embedding_backward = reinterpret_cast<decltype(g.embedding_backward)>(at[3]);
-  g.status_string = reinterpret_cast<decltype(g.status_string)>(at[4]);
+  g.quantize = reinterpret_cast<decltype(g.quantize)>(at[4]);
+  g.dequantize = reinterpret_cast<decltype(g.dequantize)>(at[5]);
+  g.scores = reinterpret_cast<decltype(g.scores)>(at[6]);
+  g.status_string = reinterpret_cast<decltype(g.status_string)>(at[7]);
 }
 
 void ok(int rc, const char* where) {
@@ -189,10 +199,56 @@ Tensor embedding(const Tensor& ids, const Tensor& weight, double scale, int64_t 
   return embedding_forward(ids, weight, scale, ignore_index);
 }
 
+// ----------------------------------------------------------------------------- MXFP4
+
+std::tuple<Tensor, Tensor> quantize_mxfp4(const Tensor& x) {
+  const Guard guard(x.device());
+  const int64_t rows = x.size(0), cols = x.size(1);
+  const auto bytes = x.options().dtype(at::kByte).requires_grad(false);
+  const Tensor q = at::empty({rows, cols / 2}, bytes), scale = at::empty({rows, cols / 32}, bytes);
+  ok(g.quantize(type_of(x), data(x), rows, cols, data(q), data(scale), stream_of(x)), "flce_quantize_mxfp4");
+  return {q, scale};
+}
+
+Tensor dequantize_mxfp4(const Tensor& q, const Tensor& scale, at::ScalarType dtype) {
+  const Guard guard(q.device());
+  const int64_t rows = q.size(0), cols = 2 * q.size(1);
+  const Tensor x = at::empty({rows, cols}, q.options().dtype(dtype));
+  ok(g.dequantize(type_of(x), data(q), data(scale), rows, cols, data(x), stream_of(q)), "flce_dequantize_mxfp4");
+  return x;
+}
+
+// params: the address of the call's flce_params, which outlives it; workspace: its bytes.
+std::tuple<Tensor, std::optional<Tensor>> logprobs_mxfp4(const Tensor& hidden, const std::optional<Tensor>& hidden_scale,
+                                                         const Tensor& weight, const Tensor& weight_scale,
+                                                         const std::optional<Tensor>& bias, const Tensor& targets,
+                                                         int64_t params, int64_t workspace, bool want_entropy) {
+  const Guard guard(hidden.device());
+  const int64_t n = hidden.size(0);
+  const auto floats = weight.options().dtype(at::kFloat);
+  // one allocation: the workspace, then the log-sum-exps, which nobody asked for
+  const Tensor room = at::empty({workspace + 4 * n}, weight.options()), logps = at::empty({n}, floats);
+  std::optional<Tensor> entropy;
+  if (want_entropy) entropy = at::empty({n}, floats);
+  char* at = static_cast<char*>(data(room));
+  ok(g.scores(reinterpret_cast<const flce_params*>(params), data(hidden), data(hidden_scale.value_or(Tensor())),
+              data(weight), data(weight_scale), static_cast<const float*>(data(bias.value_or(Tensor()))), data(targets),
+              static_cast<float*>(data(logps)), entropy ? static_cast<float*>(data(*entropy)) : nullptr,
+              reinterpret_cast<float*>(at + workspace), at, (size_t)workspace, stream_of(hidden)),
+     "flce_logprobs_mxfp4");
+  return {logps, entropy};
+}
+
 }  // namespace
 
 TORCH_LIBRARY(flce, m) {
   m.def("_bind(int[] entry_points) -> ()", bind);
   m.def("_layer_norm(Tensor x, Tensor? weight, Tensor? bias, float eps, int workspace) -> Tensor", layer_norm);
+  m.def("_quantize_mxfp4(Tensor x) -> (Tensor, Tensor)", quantize_mxfp4);
+  m.def("_dequantize_mxfp4(Tensor q, Tensor scale, ScalarType dtype) -> Tensor", dequantize_mxfp4);
+  m.def(
+      "_logprobs_mxfp4(Tensor hidden, Tensor? hidden_scale, Tensor weight, Tensor weight_scale, Tensor? bias, "
+      "Tensor targets, int params, int workspace, bool entropy) -> (Tensor, Tensor?)",
+      logprobs_mxfp4);
   m.def("_embedding(Tensor ids, Tensor weight, float scale, int ignore_index, int workspace) -> Tensor", embedding);
 }

@@ -3,14 +3,14 @@ flce_logprobs_* (include/flce.h has the formulas)."""
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import functools
 from typing import Optional
 
 from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError, _dtype_name, _ptr, _stream_handle,
-               _targets_int32, _validate, flce_dequantize_mxfp4, flce_logprobs_backward, flce_logprobs_forward,
-               flce_logprobs_int8, flce_logprobs_int8_workspace_size, flce_logprobs_mxfp4,
-               flce_logprobs_mxfp4_workspace_size, flce_logprobs_workspace_size, flce_quantize_int8,
-               flce_quantize_mxfp4, make_params)
+               _targets_int32, _validate, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_int8,
+               flce_logprobs_int8_workspace_size, flce_logprobs_mxfp4_workspace_size, flce_logprobs_workspace_size,
+               flce_quantize_int8, make_params, torch_ops)
 
 
 _SAME_DEVICE = contextlib.nullcontext()
@@ -246,15 +246,10 @@ def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hid
 
 # ----------------------------------------------------------------------------- 4-bit scoring
 
-def _quantize_mx(x):
-    import torch
-    dev = x.device
-    with on_device(dev):
-        q = torch.empty((x.shape[0], x.shape[1] // 2), dtype=torch.uint8, device=dev)
-        scale = torch.empty((x.shape[0], x.shape[1] // 32), dtype=torch.uint8, device=dev)
-        raise_for(flce_quantize_mxfp4(DTYPES[_dtype_name(x)], _ptr(x), x.shape[0], x.shape[1], _ptr(q), _ptr(scale),
-                                      stream_handle(dev)), "flce_quantize_mxfp4")
-    return q, scale
+@functools.lru_cache(maxsize=None)
+def _mx_ops():
+    ops = torch_ops()
+    return ops._quantize_mxfp4.default, ops._dequantize_mxfp4.default, ops._logprobs_mxfp4.default
 
 
 def quantize_mxfp4(x):
@@ -269,9 +264,9 @@ def quantize_mxfp4(x):
         raise ValueError(f"rows must be a multiple of 32 long, got {x.shape[1]}")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"x must be on a GPU, not {x.device}")
-    return _quantize_mx(_aligned16(x.detach()))
+    return _mx_ops()[0](_aligned16(x))
 
 
 def _check_mx(name, q, scale):
@@ -299,14 +294,9 @@ def dequantize_mxfp4(q, scale, dtype=None):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     for name, t in (("q", q), ("scale", scale)):
-        if t.device.type != "cuda" or t.device != q.device:
+        if not t.is_cuda or t.device != q.device:
             raise ValueError(f"{name} must be on q's GPU ({q.device}), not {t.device}")
-    dev, q = q.device, _aligned16(q)
-    with on_device(dev):
-        x = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=dtype, device=dev)
-        raise_for(flce_dequantize_mxfp4(DTYPES[_dtype_name(x)], _ptr(q), _ptr(scale), x.shape[0], x.shape[1], _ptr(x),
-                                        stream_handle(dev)), "flce_dequantize_mxfp4")
-    return x
+    return _mx_ops()[1](_aligned16(q), scale, dtype)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -360,16 +350,7 @@ def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hi
         if t is not None and ((recorded and t.requires_grad) or has_tangent(t)):
             raise ValueError(f"4-bit scores have no gradient: detach {name}, or use token_logprobs")
     p, ws_bytes = _mx_plan(n, h, v, dtype, float(logit_scale), float(softcap or 0.0), int(ignore_index), int32)
-    with on_device(dev):
-        hidden, weight, weight_scale = _aligned16(hidden), _aligned16(weight), _aligned16(weight_scale)
-        bias, hidden_scale = _aligned16(bias), _aligned16(hidden_scale)
-        # one allocation: the workspace, then the log-sum-exps, which nobody asked for
-        workspace = torch.empty(ws_bytes + 4 * n, dtype=torch.uint8, device=dev)
-        logps = torch.empty(n, dtype=torch.float32, device=dev)
-        entropy = torch.empty(n, dtype=torch.float32, device=dev) if return_entropy else None
-        at = workspace.data_ptr()
-        raise_for(flce_logprobs_mxfp4(p, hidden.data_ptr(), _ptr(hidden_scale), weight.data_ptr(),
-                                      weight_scale.data_ptr(), _ptr(bias), targets.data_ptr(), logps.data_ptr(),
-                                      _ptr(entropy), at + ws_bytes, at, ws_bytes, stream_handle(dev)),
-                  "flce_logprobs_mxfp4")
+    logps, entropy = _mx_ops()[2](_aligned16(hidden), _aligned16(hidden_scale), _aligned16(weight),
+                                  _aligned16(weight_scale), _aligned16(bias), targets, ctypes.addressof(p), ws_bytes,
+                                  return_entropy)
     return (logps, entropy) if return_entropy else logps
