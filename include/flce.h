@@ -612,8 +612,9 @@ int flce_embedding_backward(const flce_embedding_params* p, const void* ids, con
  * and backward:
  *   mean = sum_j x_j / cols,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / cols + eps),
  *   y_j = weight_j (x_j - mean) rstd + bias_j.
- * Everything is formed in fp32 and rounded once.  Pointers need the alignment of
- * their element only (the workspace 16 bytes); 16-byte aligned rows run faster.
+ * Everything is formed in fp32 (so the sum of a row's squares has to stay in its
+ * range) and rounded once.  Pointers need the alignment of their element only (the
+ * workspace 16 bytes); 16-byte aligned rows run faster.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int64_t rows;               /* >= 0, at most 2^31                                      */

@@ -287,6 +287,9 @@ int plan_forward_backward(Plan* pl, int64_t block_rows) {
 // time is about its rounds of tiles over the CUs times a tile's work over the rate that
 // its tiles reach; the small tiles' rate is the share below of the large ones'.
 // ---------------------------------------------------------------------------
+// (MXFP4, with the 8-bit operands' share, us small against large: 100 tokens H = 4096 V = 128256 132, 97 and mixed 87;
+// 200 2048 32000 34, 30; 400 4096 8000 34, 37; 1000 4096 8000 54, 40; 100 1024 50001 25.5, 24.2; 1000 4096 2000 24, 37.
+// The rule's choice is within 6% of the faster in these and 40 more.)
 static double small_rate(const Plan& P) { return P.int8 ? 0.35 : (P.dtype == FLCE_F32 ? 0.8 : 0.4); }
 
 // Time of tiles in units of (rows x columns of a large tile's pass over K by one CU).

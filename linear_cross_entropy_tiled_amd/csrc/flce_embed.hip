@@ -6,6 +6,10 @@
 // fp32 and rounds it once.  Runs are summed by chunks of sorted tokens, not by rows: a
 // frequent token's run of thousands is spread over many workgroups.  The part of a run
 // that reaches over a chunk's edge is left in fp32 and a second kernel adds the parts.
+//
+// What bounds it is memory, and of the whole gradient mostly its zeros.  N = 8192, H = 4096,
+// V = 128256, bf16, Zipf's ids: forward 24 us; zeros and sort 163 us (1.05 GB at 6.4 TB/s,
+// where a plain fill reaches 6.9), runs 36, joins 10.
 #include "flce_device.h"
 #include "flce_embed.h"
 
@@ -365,7 +369,9 @@ template <int W> __global__ __launch_bounds__(64 * W) void sort_place_kernel(Sor
 }
 
 // ---------------------------------------------------------------------------
-// Sums of runs
+// Sums of runs, by chunks of 16 tokens (32 beyond 16384, more where there would be over 4096
+// chunks).  N = 8192 above in chunks of 8 / 16 / 32 / 64: runs 36 / 36 / 36 / 79 us, joins 15 /
+// 9 / 7 / 6; N = 1000, H = 4096: runs 7 / 9 / 14 / 57.
 // ---------------------------------------------------------------------------
 struct RunArgs {
   const uint32_t* keys;        // equal ones next to each other; tokens without a row last

@@ -182,6 +182,34 @@ def test_quantized_states_and_slices(flce_lib, n, h):
         assert torch.equal(part, alone)
 
 
+@pytest.mark.parametrize("h", [224, 256])
+def test_quantized_states_in_large_tiles(flce_lib, h):
+    """Codes and scales that are given, in rows that need padding (7 scales) and in whole ones."""
+    import torch
+    x, w, b, t = _problem(1030, h, 9001, seed=h)
+    q, s = flce_lib.quantize_mxfp4(w.cuda())
+    xq, xs = flce_lib.quantize_mxfp4(x.cuda())
+    got = flce_lib.token_logprobs_mxfp4(xq, q, s, t.cuda(), b.cuda(), hidden_scale=xs, return_entropy=True)
+    want = flce_lib.token_logprobs_mxfp4(x.cuda(), q, s, t.cuda(), b.cuda(), return_entropy=True)
+    assert all(torch.equal(p, r) for p, r in zip(got, want))
+    _check(_np(got[0]), _np(got[1]), mo.values(*mo.quantize(x.double().numpy())),
+           mo.values(*mo.quantize(w.double().numpy())), b.double().numpy(), t.numpy())
+
+
+@pytest.mark.parametrize("n", [7, 1500])
+def test_scale_of_either_sign_and_zero(flce_lib, n):
+    """A negative logit_scale turns the order of the logits round; with 0 every entry has the same probability."""
+    import torch
+    x, w, b, t = _problem(n, 128, 3003, seed=n, ignored=0.0)
+    q, s = flce_lib.quantize_mxfp4(w.cuda())
+    values = mo.values(*mo.quantize(x.double().numpy())), mo.values(*mo.quantize(w.double().numpy()))
+    lp, ent = flce_lib.token_logprobs_mxfp4(x.cuda(), q, s, t.cuda(), b.cuda(), logit_scale=-0.8, return_entropy=True)
+    _check(_np(lp), _np(ent), *values, b.double().numpy(), t.numpy(), scale=-0.8)
+    lp, ent = flce_lib.token_logprobs_mxfp4(x.cuda(), q, s, t.cuda(), b.cuda(), logit_scale=0.0, return_entropy=True)
+    want = np.log(3003.0)
+    assert np.all(np.abs(_np(lp) + want) <= 48 * U32 * (want + 1)) and np.all(np.abs(_np(ent) - want) <= 48 * U32 * (want + 1))
+
+
 @pytest.mark.parametrize("n", [4, 90, 600])
 def test_masked_rows_and_entries(flce_lib, n):
     """NaN states of ignored rows stay there; targets out of range count as ignored; a bias of -inf takes entries out;
