@@ -142,3 +142,64 @@ def test_the_step_as_a_graph(flce_lib):
         torch.cuda.synchronize()
         for p, r in zip(out, step()):
             assert torch.equal(p, r)
+
+
+def test_recomputed_in_the_backward_pass(flce_lib):
+    """Under activation checkpointing, and with what the operators save packed to the host: the same gradients."""
+    import torch
+    from torch.utils.checkpoint import checkpoint
+    w, gain, shift, ids, targets, _, _ = _model(7)
+
+    def grads(how):
+        leaves = _leaves(w, gain, shift)
+        loss = how(lambda a, b, c: _forward(flce_lib, a, b, c, ids, targets)[2][0].sum(), leaves)
+        return (loss.detach(), *torch.autograd.grad(loss, leaves))
+
+    def packed(f, leaves):
+        with torch.autograd.graph.save_on_cpu():
+            return f(*leaves)
+
+    want = grads(lambda f, leaves: f(*leaves))
+    for how in (lambda f, leaves: checkpoint(lambda *a: f(*a), *leaves, use_reentrant=False), packed):
+        for p, r in zip(grads(how), want):
+            assert torch.equal(p, r)
+
+
+def test_steps_on_two_threads(flce_lib):
+    """Two threads, each with its own stream, model and library calls, at the same time: neither's results change."""
+    import threading
+
+    import torch
+    problems = [_model(seed) for seed in (11, 12)]
+    problems = [(*p, *flce_lib.quantize_mxfp4(p[0])) for p in problems]
+
+    def step(p):
+        w, gain, shift, ids, targets, _, _, q, s = p
+        leaves = _leaves(w, gain, shift)
+        _, y, (lp, _) = _forward(flce_lib, *leaves, ids, targets)
+        return (flce_lib.token_logprobs_mxfp4(y.detach(), q, s, targets), lp.detach(),
+                *torch.autograd.grad(lp.sum(), leaves))
+
+    want = [step(p) for p in problems]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def run(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[k] += [step(problems[k]) for _ in range(20)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:      # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for k in (0, 1):
+        assert len(got[k]) == 20
+        for out in got[k]:
+            for p, r in zip(out, want[k]):
+                assert torch.equal(p, r)
