@@ -325,17 +325,29 @@ template <bool HAS_BIAS, bool SOFTCAP> __global__ __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i++) {
           const float x = acc[mi][ni][i] - m_new, e = fast_exp2(x);
-          // a logit of -inf, which only a bias gives, is to add 0 and not 0 times infinity
-          const float xf = SOFTCAP || !HAS_BIAS ? x : fmaxf(x, kMasked);
           if (i & 1) {
             se1 += e;
-            sx1 = fmaf(e, xf, sx1);
+            sx1 = fmaf(e, x, sx1);
           } else {
             se0 += e;
-            sx0 = fmaf(e, xf, sx0);
+            sx0 = fmaf(e, x, sx0);
           }
         }
-      st[ni].T = fmaf(fmaf(dm, st[ni].l, st[ni].T), alpha, sx0 + sx1);
+      float sx = sx0 + sx1;
+      // a logit of -inf (a bias, or a sum past fp32's range) is to add 0 and not 0 times infinity: seldom, so the sum is
+      // formed again.  (A maximum per logit takes 1 to 4%, this half of it; both columns' sums in one place spill.)
+      if (!SOFTCAP && __builtin_amdgcn_ballot_w64(sx != sx)) {
+        float again = 0.0f;
+#pragma unroll
+        for (int mi = 0; mi < kMxM; mi++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const float x = acc[mi][ni][i] - m_new;
+            again = fmaf(fast_exp2(x), fmaxf(x, kMasked), again);
+          }
+        sx = sx != sx ? again : sx;   // (a column's sum does not depend on its neighbours)
+      }
+      st[ni].T = fmaf(fmaf(dm, st[ni].l, st[ni].T), alpha, sx);
       st[ni].l = fmaf(st[ni].l, alpha, se0 + se1);
       st[ni].m = m_new;
     }

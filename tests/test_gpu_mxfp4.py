@@ -237,6 +237,29 @@ def test_masked_rows_and_entries(flce_lib, n):
            b.double().numpy()[keep], T, rows=rows)
 
 
+@pytest.mark.parametrize("n,v", [(4, 3003), (90, 3003), (1030, 9001)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_logits_past_the_range(flce_lib, n, v, bias):
+    """A logit whose products leave fp32's range downwards has probability 0, as has one with a bias of -inf (whole
+    tiles of them here): the other entries' log-probabilities and the entropy are those without it."""
+    import torch
+    x, w, b, t = _problem(n, 128, v, seed=n, ignored=0.0, bias=bias)
+    x, w = x.abs() + 1, w.clone()
+    w[17] = -2.0 ** 127
+    out = np.zeros(v, dtype=bool)
+    out[17] = True
+    if bias:
+        out[100:900] = True
+        b[100:900] = -float("inf")
+    keep = np.flatnonzero(~out)
+    place = np.cumsum(~out) - 1
+    t[torch.from_numpy(out)[t]] = 18
+    q, s = flce_lib.quantize_mxfp4(w.cuda())
+    lp, ent = flce_lib.token_logprobs_mxfp4(x.cuda(), q, s, t.cuda(), None if b is None else b.cuda(), return_entropy=True)
+    _check(_np(lp), _np(ent), mo.values(*mo.quantize(x.double().numpy())), mo.values(*mo.quantize(w.double().numpy()))[keep],
+           None if b is None else b.double().numpy()[keep], place[t.numpy()])
+
+
 def test_no_tokens_and_all_ignored(flce_lib):
     import torch
     x, w, b, t = _problem(20, 64, 300, seed=1)
