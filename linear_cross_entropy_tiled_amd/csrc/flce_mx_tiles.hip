@@ -14,10 +14,10 @@
 //    with bias and softcap, before it was cut): the sums begin with the bias, two logits share
 //    a comparison, rows past V are masked in the last tile only.
 //
-// What bounds it: N = 8192, H = 4096, V = 128256 takes 1.95 to 2.1 ms, 4.1 to 4.4 PFLOP/s (the
+// What bounds it: N = 8192, H = 4096, V = 128256 takes 1.89 to 2.1 ms, 4.1 to 4.6 PFLOP/s (the
 // library's largest MXFP4 product 3.0), matrix units busy 65%, and the board's power: with 64
 // stages of random data the clock is 1.56 GHz, of zeros 2.08 at the same cycles.  With few
-// stages the epilogue: N = 1000, H = 2048, V = 50001, bias, softcap 69 us, units busy 33%.
+// stages the epilogue: N = 1000, H = 2048, V = 50001, bias, softcap 68 us, units busy 33%.
 // The steps there, whole calls in us: 64 x 64 tiles alone 6273 and 177; 256 x 256 with 16 x 16
 // instructions 2204 and 103; 32 x 32 and one run of stages 2190 and 102, prepared in one launch
 // 2140 and 100; the epilogue 2000 and 88.
