@@ -21,43 +21,82 @@
 
 namespace flce {
 
-template <typename P> __device__ __forceinline__ float param(const void* p, int i, float none) {
-  return p ? (float)static_cast<const P*>(p)[i] : none;
+// VEC neighbouring values of a parameter vector of T or fp32, in pieces of up to 16 bytes (to which it is aligned).
+template <typename P, int VEC> __device__ __forceinline__ void param_piece(const P* p, float* out) {
+  constexpr int kMost = 16 / sizeof(P), kPiece = VEC < kMost ? VEC : kMost;
+  typedef P V __attribute__((ext_vector_type(kPiece)));
+#pragma unroll
+  for (int k = 0; k < VEC; k += kPiece) {
+    const V v = *reinterpret_cast<const V*>(p + k);
+#pragma unroll
+    for (int j = 0; j < kPiece; j++) out[k + j] = (float)v[j];
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void param_at(const void* p, int dtype, int i, bool in, float none, float* out) {
+#pragma unroll
+  for (int j = 0; j < VEC; j++) out[j] = in ? none : 0.0f;
+  if (!p || !in) return;
+  if (dtype == FLCE_F32) param_piece<float, VEC>(static_cast<const float*>(p) + i, out);
+  else param_piece<T, VEC>(static_cast<const T*>(p) + i, out);
 }
 
-// The sum over a workgroup of 256, on every thread.
+// The sum over a workgroup of 1024, on every thread.
 __device__ __forceinline__ float block_sum(float v, float* lds) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+  v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; k++) v += lds[k];
   __syncthreads();
   return v;
 }
 
 // ---------------------------------------------------------------------------
-// Rows of any length (beyond 16384): one workgroup a row; the passes after the first
-// read the row from cache (4096 x 32768 in bf16: 348 us forward, 552 backward, three times
-// what reading and writing once would take).
+// Rows of any length (beyond 16384): one workgroup a row, VEC columns a thread at a time; the
+// passes after the first read the row from cache, the column sums read x and dy again.
+// 4096 x 32768 in bf16, fp32 parameters: 164 us forward (reading and writing once takes 114),
+// 337 backward (171 so); 64 x 131072 26 and 52.  By 256 threads of one column at a time 335,
+// 577 and 321, 328.
 // ---------------------------------------------------------------------------
-template <typename T, typename P> __global__ __launch_bounds__(256) void norm_fwd_any_kernel(NormArgs a) {
-  __shared__ float lds[4];
+template <typename T, int VEC> __global__ __launch_bounds__(1024) void norm_fwd_any_kernel(NormArgs a) {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  __shared__ float lds[16];
   const float inv = 1.0f / (float)a.cols;
+  const int c0 = (int)threadIdx.x * VEC;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ld_x;
     T* y = static_cast<T*>(a.y) + r * a.cols;
     float s = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += 256) s += (float)x[c];
+#pragma unroll 4
+    for (int c = c0; c < a.cols; c += 1024 * VEC) {
+      const V v = *reinterpret_cast<const V*>(x + c);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) s += (float)v[j];
+    }
     const float mean = block_sum(s, lds) * inv;
     s = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += 256) {
-      const float d = (float)x[c] - mean;
-      s = fmaf(d, d, s);
+#pragma unroll 4
+    for (int c = c0; c < a.cols; c += 1024 * VEC) {
+      const V v = *reinterpret_cast<const V*>(x + c);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const float d = (float)v[j] - mean;
+        s = fmaf(d, d, s);
+      }
     }
     const float rstd = 1.0f / sqrtf(fmaf(block_sum(s, lds), inv, a.eps));
-    for (int c = threadIdx.x; c < a.cols; c += 256)
-      y[c] = (T)fmaf(((float)x[c] - mean) * rstd, param<P>(a.weight, c, 1.0f), param<P>(a.bias, c, 0.0f));
+    for (int c = c0; c < a.cols; c += 1024 * VEC) {
+      V v = *reinterpret_cast<const V*>(x + c);
+      float w[VEC], b[VEC];
+      param_at<T, VEC>(a.weight, a.param_dtype, c, true, 1.0f, w);
+      param_at<T, VEC>(a.bias, a.param_dtype, c, true, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[j] = (T)fmaf(((float)v[j] - mean) * rstd, w[j], b[j]);
+      *reinterpret_cast<V*>(y + c) = v;
+    }
     if (a.mean && threadIdx.x == 0) {
       a.mean[r] = mean;
       a.rstd[r] = rstd;
@@ -65,49 +104,77 @@ template <typename T, typename P> __global__ __launch_bounds__(256) void norm_fw
   }
 }
 
-template <typename T, typename P> __global__ __launch_bounds__(256) void norm_dx_any_kernel(NormArgs a) {
-  __shared__ float lds[4];
+template <typename T, int VEC> __global__ __launch_bounds__(1024) void norm_dx_any_kernel(NormArgs a) {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  __shared__ float lds[16];
   const float inv = 1.0f / (float)a.cols;
+  const int c0 = (int)threadIdx.x * VEC;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ld_x;
     const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
     T* dx = static_cast<T*>(a.dx) + r * a.cols;
     const float mean = a.mean[r], rstd = a.rstd[r];
     float s1 = 0.0f, s2 = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += 256) {
-      const float d = (float)dy[c] * param<P>(a.weight, c, 1.0f);
-      s1 += d;
-      s2 = fmaf(d, ((float)x[c] - mean) * rstd, s2);
+#pragma unroll 2
+    for (int c = c0; c < a.cols; c += 1024 * VEC) {
+      const V v = *reinterpret_cast<const V*>(x + c), g = *reinterpret_cast<const V*>(dy + c);
+      float w[VEC];
+      param_at<T, VEC>(a.weight, a.param_dtype, c, true, 1.0f, w);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const float d = (float)g[j] * w[j];
+        s1 += d;
+        s2 = fmaf(d, ((float)v[j] - mean) * rstd, s2);
+      }
     }
     s1 = block_sum(s1, lds) * inv;
     s2 = block_sum(s2, lds) * inv;
-    for (int c = threadIdx.x; c < a.cols; c += 256) {
-      const float d = (float)dy[c] * param<P>(a.weight, c, 1.0f), xhat = ((float)x[c] - mean) * rstd;
-      dx[c] = (T)(rstd * (d - fmaf(xhat, s2, s1)));
+    for (int c = c0; c < a.cols; c += 1024 * VEC) {
+      V v = *reinterpret_cast<const V*>(x + c);
+      const V g = *reinterpret_cast<const V*>(dy + c);
+      float w[VEC];
+      param_at<T, VEC>(a.weight, a.param_dtype, c, true, 1.0f, w);
+#pragma unroll
+      for (int j = 0; j < VEC; j++)
+        v[j] = (T)(rstd * ((float)g[j] * w[j] - fmaf(((float)v[j] - mean) * rstd, s2, s1)));
+      *reinterpret_cast<V*>(dx + c) = v;
     }
   }
 }
 
-// Column sums of one range of rows: 64 columns by 4 threads each.
-template <typename T> __global__ __launch_bounds__(256) void norm_columns_any_kernel(NormArgs a) {
-  __shared__ float lds[2][4][64];
-  const int tid = threadIdx.x, sub = tid >> 6, c = (int)blockIdx.x * 64 + (tid & 63);
+// Column sums of one range of rows: 64 VEC columns by 4 threads each.
+template <typename T, int VEC> __global__ __launch_bounds__(256) void norm_columns_any_kernel(NormArgs a) {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  __shared__ float lds[2][4][VEC][64];
+  const int tid = threadIdx.x, sub = tid >> 6, lane = tid & 63, c = ((int)blockIdx.x * 64 + lane) * VEC;
   const int64_t r0 = a.rows * blockIdx.y / a.parts, r1 = a.rows * (blockIdx.y + 1) / a.parts;
-  float sw = 0.0f, sb = 0.0f;
+  float sw[VEC], sb[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) sw[j] = sb[j] = 0.0f;
   if (c < a.cols) {
+#pragma unroll 4
     for (int64_t r = r0 + sub; r < r1; r += 4) {
-      const float g = (float)static_cast<const T*>(a.dy)[r * a.ld_dy + c];
-      const float xhat = ((float)static_cast<const T*>(a.x)[r * a.ld_x + c] - a.mean[r]) * a.rstd[r];
-      sw = fmaf(g, xhat, sw);
-      sb += g;
+      const V g = *reinterpret_cast<const V*>(static_cast<const T*>(a.dy) + r * a.ld_dy + c);
+      const V x = *reinterpret_cast<const V*>(static_cast<const T*>(a.x) + r * a.ld_x + c);
+      const float mean = a.mean[r], rstd = a.rstd[r];
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        sw[j] = fmaf((float)g[j], ((float)x[j] - mean) * rstd, sw[j]);
+        sb[j] += (float)g[j];
+      }
     }
   }
-  lds[0][sub][tid & 63] = sw;
-  lds[1][sub][tid & 63] = sb;
+#pragma unroll
+  for (int j = 0; j < VEC; j++) {
+    lds[0][sub][j][lane] = sw[j];
+    lds[1][sub][j][lane] = sb[j];
+  }
   __syncthreads();
-  if (sub < 2 && c < a.cols)
-    a.part[((int64_t)blockIdx.y * 2 + sub) * a.cols + c] =
-        (lds[sub][0][tid & 63] + lds[sub][1][tid & 63]) + (lds[sub][2][tid & 63] + lds[sub][3][tid & 63]);
+  if (sub >= 2 || c >= a.cols) return;
+#pragma unroll
+  for (int j = 0; j < VEC; j++)
+    a.part[((int64_t)blockIdx.y * 2 + sub) * a.cols + c + j] =
+        (lds[sub][0][j][lane] + lds[sub][1][j][lane]) + (lds[sub][2][j][lane] + lds[sub][3][j][lane]);
 }
 
 // The ranges' sums: 64 columns of dweight (blockIdx.y 0) or dbias (1), 16 threads to a column, each every 16th range.
@@ -139,26 +206,6 @@ template <typename P> __global__ __launch_bounds__(1024) void norm_parts_kernel(
 // ---------------------------------------------------------------------------
 // Rows in registers
 // ---------------------------------------------------------------------------
-// VEC neighbouring values of a parameter vector of T or fp32, in pieces of up to 16 bytes (to which it is aligned).
-template <typename P, int VEC> __device__ __forceinline__ void param_piece(const P* p, float* out) {
-  constexpr int kMost = 16 / sizeof(P), kPiece = VEC < kMost ? VEC : kMost;
-  typedef P V __attribute__((ext_vector_type(kPiece)));
-#pragma unroll
-  for (int k = 0; k < VEC; k += kPiece) {
-    const V v = *reinterpret_cast<const V*>(p + k);
-#pragma unroll
-    for (int j = 0; j < kPiece; j++) out[k + j] = (float)v[j];
-  }
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void param_at(const void* p, int dtype, int i, bool in, float none, float* out) {
-#pragma unroll
-  for (int j = 0; j < VEC; j++) out[j] = in ? none : 0.0f;
-  if (!p || !in) return;
-  if (dtype == FLCE_F32) param_piece<float, VEC>(static_cast<const float*>(p) + i, out);
-  else param_piece<T, VEC>(static_cast<const T*>(p) + i, out);
-}
-
 // A thread's columns of a row: CPT of them in pieces of VEC, TPR threads a row.
 template <typename T, int VEC, int CPT, int TPR> struct RowPart {
   static constexpr int NV = CPT / VEC;
@@ -395,27 +442,27 @@ template <typename T, int VEC> static void norm_rows(const NormArgs& a, bool bac
   }
 }
 
-template <typename T, typename P> static void norm_any(const NormArgs& a, bool back, hipStream_t st) {
+template <typename T, int VEC> static void norm_any(const NormArgs& a, bool back, hipStream_t st) {
   const unsigned wgs = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
   if (!back) {
-    norm_fwd_any_kernel<T, P><<<wgs, 256, 0, st>>>(a);
+    norm_fwd_any_kernel<T, VEC><<<wgs, 1024, 0, st>>>(a);
     return;
   }
-  if (a.rows > 0 && a.dx) norm_dx_any_kernel<T, P><<<wgs, 256, 0, st>>>(a);
+  if (a.rows > 0 && a.dx) norm_dx_any_kernel<T, VEC><<<wgs, 1024, 0, st>>>(a);
   if (a.dw || a.db)
-    norm_columns_any_kernel<T><<<dim3((unsigned)((a.cols + 63) / 64), (unsigned)a.parts), 256, 0, st>>>(a);
+    norm_columns_any_kernel<T, VEC><<<dim3((unsigned)((a.cols + 64 * VEC - 1) / (64 * VEC)), (unsigned)a.parts), 256, 0, st>>>(a);
 }
 
 template <typename T> static void norm_t(const NormArgs& a, bool back, hipStream_t st) {
-  if (a.cols > kRegisterCols) {
-    if (a.param_dtype == FLCE_F32) norm_any<T, float>(a, back, st);
-    else norm_any<T, T>(a, back, st);
-    return;
-  }
   constexpr int kVec = 16 / sizeof(T);
   const bool vec = rows16(a.x, a.ld_x, a.dtype) && rows16(back ? a.dx : a.y, a.cols, a.dtype) &&
                    (!back || rows16(a.dy, a.ld_dy, a.dtype)) && rows16(a.weight, 0, a.dtype) &&
                    rows16(a.bias, 0, a.dtype);
+  if (a.cols > kRegisterCols) {
+    if (vec) norm_any<T, kVec>(a, back, st);
+    else norm_any<T, 1>(a, back, st);
+    return;
+  }
   if (vec) norm_rows<T, kVec>(a, back, st);
   else norm_rows<T, 1>(a, back, st);
 }

@@ -80,7 +80,7 @@ def check(flce_lib, x, w, b, g, dtype, pdtype, eps=1e-5, on=None):
 
 
 SHAPES = [(1, 1), (3, 7), (5, 64), (16, 4096), (70, 1023), (33, 5000), (2, 16392), (700, 128), (300, 520), (9, 40000),
-          (4, 8192), (1, 2048), (257, 1024), (6, 4104), (5, 16384), (3, 1 << 17)]
+          (4, 8192), (1, 2048), (257, 1024), (6, 4104), (5, 16384), (3, 1 << 17), (66, 16385), (130, 17000)]
 
 
 @pytest.mark.parametrize("dtype,pdtype", [("float32", "float32"), ("bfloat16", "bfloat16"), ("bfloat16", "float32"),
