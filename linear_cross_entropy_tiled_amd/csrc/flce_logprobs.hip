@@ -436,6 +436,7 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
     a.hidden_scale = static_cast<const float*>(hidden_scale);
     a.weight_scale = static_cast<const float*>(weight_scale);
     if (pl.mx) {
+      hipError_t e = hipSuccess;   // a launcher that returns its error takes it from the check at the end
       MxPrep m{};
       m.n = pl.N;
       m.blocks = (int)(pl.H / 16);
@@ -450,14 +451,16 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
         a.hidden_mx = static_cast<const uint8_t*>(hidden_scale);
         if (m.ld != m.blocks) {
           uint8_t* padded = reinterpret_cast<uint8_t*>(ws + lp.f_hmx);
-          (void)launch_pad_scales(a.hidden_mx, pl.N, m.blocks, m.ld, padded, st);
+          e = launch_pad_scales(a.hidden_mx, pl.N, m.blocks, m.ld, padded, st);
+          if (e != hipSuccess) return e;
           a.hidden_mx = padded;
         }
       }
       a.weight_mx = static_cast<const uint8_t*>(weight_scale);
       if (m.ld != m.blocks) {
         uint8_t* padded = reinterpret_cast<uint8_t*>(ws + lp.f_wmx);
-        (void)launch_pad_scales(a.weight_mx, pl.V, m.blocks, m.ld, padded, st);
+        e = launch_pad_scales(a.weight_mx, pl.V, m.blocks, m.ld, padded, st);
+        if (e != hipSuccess) return e;
         a.weight_mx = padded;
       }
       a.ld_hmx = a.ld_wmx = (uint32_t)m.ld;
@@ -473,7 +476,8 @@ hipError_t launch_logprobs(const Plan& pl, const LpPlan& lp, const void* hidden,
         a.weight_tmx = m.w_out;
         a.hidden_tmx = m.h_out;
       }
-      (void)launch_mx_prep(pl.x_dtype, m, st);
+      e = launch_mx_prep(pl.x_dtype, m, st);
+      if (e != hipSuccess) return e;
     }
     a.targets = targets;
     a.tgt_i32 = pl.tgt_i32 ? 1 : 0;
