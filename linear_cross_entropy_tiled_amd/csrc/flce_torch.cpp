@@ -218,23 +218,33 @@ Tensor dequantize_mxfp4(const Tensor& q, const Tensor& scale, at::ScalarType dty
   return x;
 }
 
-// params: the address of the call's flce_params, which outlives it; workspace: its bytes.
-std::tuple<Tensor, std::optional<Tensor>> logprobs_mxfp4(const Tensor& hidden, const std::optional<Tensor>& hidden_scale,
-                                                         const Tensor& weight, const Tensor& weight_scale,
-                                                         const std::optional<Tensor>& bias, const Tensor& targets,
-                                                         int64_t params, int64_t workspace, bool want_entropy) {
+// workspace: its bytes.  hidden without scales holds values.  The entropies are undefined where they are not wanted.
+std::tuple<Tensor, Tensor> logprobs_mxfp4(const Tensor& hidden, const std::optional<Tensor>& hidden_scale,
+                                          const Tensor& weight, const Tensor& weight_scale,
+                                          const std::optional<Tensor>& bias, const Tensor& targets, double logit_scale,
+                                          double softcap, int64_t ignore_index, int64_t workspace, bool want_entropy) {
   const Guard guard(hidden.device());
   const int64_t n = hidden.size(0);
+  flce_params p{};
+  p.n_tokens = n;
+  p.hidden = 2 * weight.size(1);
+  p.vocab = weight.size(0);
+  p.ignore_index = ignore_index;
+  p.dtype = p.grad_weight_dtype = hidden_scale ? FLCE_BF16 : type_of(hidden);
+  p.reduction = FLCE_REDUCTION_NONE;
+  p.flags = targets.scalar_type() == at::kInt ? FLCE_TARGETS_INT32 : 0;
+  p.logit_scale = (float)logit_scale;
+  p.softcap = (float)softcap;
   const auto floats = weight.options().dtype(at::kFloat);
   // one allocation: the workspace, then the log-sum-exps, which nobody asked for
   const Tensor room = at::empty({workspace + 4 * n}, weight.options()), logps = at::empty({n}, floats);
-  std::optional<Tensor> entropy;
+  Tensor entropy;
   if (want_entropy) entropy = at::empty({n}, floats);
   char* at = static_cast<char*>(data(room));
-  ok(g.scores(reinterpret_cast<const flce_params*>(params), data(hidden), data(hidden_scale.value_or(Tensor())),
-              data(weight), data(weight_scale), static_cast<const float*>(data(bias.value_or(Tensor()))), data(targets),
-              static_cast<float*>(data(logps)), entropy ? static_cast<float*>(data(*entropy)) : nullptr,
-              reinterpret_cast<float*>(at + workspace), at, (size_t)workspace, stream_of(hidden)),
+  ok(g.scores(&p, data(hidden), data(hidden_scale.value_or(Tensor())), data(weight), data(weight_scale),
+              static_cast<const float*>(data(bias.value_or(Tensor()))), data(targets), static_cast<float*>(data(logps)),
+              static_cast<float*>(data(entropy)), reinterpret_cast<float*>(at + workspace), at, (size_t)workspace,
+              stream_of(hidden)),
      "flce_logprobs_mxfp4");
   return {logps, entropy};
 }
@@ -248,7 +258,8 @@ TORCH_LIBRARY(flce, m) {
   m.def("_dequantize_mxfp4(Tensor q, Tensor scale, ScalarType dtype) -> Tensor", dequantize_mxfp4);
   m.def(
       "_logprobs_mxfp4(Tensor hidden, Tensor? hidden_scale, Tensor weight, Tensor weight_scale, Tensor? bias, "
-      "Tensor targets, int params, int workspace, bool entropy) -> (Tensor, Tensor?)",
+      "Tensor targets, float logit_scale, float softcap, int ignore_index, int workspace, bool entropy) -> "
+      "(Tensor, Tensor)",
       logprobs_mxfp4);
   m.def("_embedding(Tensor ids, Tensor weight, float scale, int ignore_index, int workspace) -> Tensor", embedding);
 }

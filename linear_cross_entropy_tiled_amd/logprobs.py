@@ -3,7 +3,6 @@ flce_logprobs_* (include/flce.h has the formulas)."""
 from __future__ import annotations
 
 import contextlib
-import ctypes
 import functools
 from typing import Optional
 
@@ -300,10 +299,11 @@ def dequantize_mxfp4(q, scale, dtype=None):
 
 
 @functools.lru_cache(maxsize=1024)
-def _mx_plan(n, h, v, dtype, logit_scale, softcap, ignore_index, targets_int32):
-    p = make_params(n, h, v, dtype=dtype, logit_scale=logit_scale, softcap=softcap, ignore_index=ignore_index,
-                    reduction="none", targets_int32=targets_int32)
-    return p, flce_logprobs_mxfp4_workspace_size(p)
+def _mx_workspace(n, h, v, dtype, logit_scale, softcap, ignore_index, targets_int32):
+    """Bytes of the call's workspace; refuses what the C entry point would."""
+    return flce_logprobs_mxfp4_workspace_size(
+        make_params(n, h, v, dtype=dtype, logit_scale=logit_scale, softcap=softcap, ignore_index=ignore_index,
+                    reduction="none", targets_int32=targets_int32))
 
 
 def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
@@ -349,8 +349,9 @@ def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hi
     for name, t in (("hidden", hidden), ("bias", bias)):     # the others are integers
         if t is not None and ((recorded and t.requires_grad) or has_tangent(t)):
             raise ValueError(f"4-bit scores have no gradient: detach {name}, or use token_logprobs")
-    p, ws_bytes = _mx_plan(n, h, v, dtype, float(logit_scale), float(softcap or 0.0), int(ignore_index), int32)
+    logit_scale, softcap, ignore_index = float(logit_scale), float(softcap or 0.0), int(ignore_index)
+    ws_bytes = _mx_workspace(n, h, v, dtype, logit_scale, softcap, ignore_index, int32)
     logps, entropy = _mx_ops()[2](_aligned16(hidden), _aligned16(hidden_scale), _aligned16(weight),
-                                  _aligned16(weight_scale), _aligned16(bias), targets, ctypes.addressof(p), ws_bytes,
-                                  return_entropy)
+                                  _aligned16(weight_scale), _aligned16(bias), targets, logit_scale, softcap, ignore_index,
+                                  ws_bytes, return_entropy)
     return (logps, entropy) if return_entropy else logps
