@@ -1,8 +1,10 @@
 // The PyTorch side of layer_norm and embedding, operators whose autograd nodes are C++, and
-// of the MXFP4 calls.  Argument checks stand in the Python functions in front of them
-// (norm.py, embedding.py, logprobs.py); the work is that of the C ABI, whose entry points are
-// handed over by address once, so that this library runs on whichever build of libflce.so
-// is loaded.
+// of the MXFP4 calls.  The Python functions in front of them (norm.py, embedding.py,
+// logprobs.py) check arguments and say what is wrong with them; types, sizes, layout and
+// device, which the kernels trust, are checked here again, since a recorded graph calls
+// these operators without Python, with tensors other than the recorded ones.  The work is
+// that of the C ABI, whose entry points are handed over by address once, so that this
+// library runs on whichever build of libflce.so is loaded.
 //
 // Why not a Python autograd function, as the other operators have: autograd runs a GPU
 // node's backward on a thread of its own, and Python that wakes up there runs at half its
@@ -52,6 +54,21 @@ void bind(at::IntArrayRef at) {
 
 void ok(int rc, const char* where) {
   TORCH_CHECK(rc == FLCE_OK, where, ": ", g.status_string(rc), " (", rc, ")");
+}
+
+bool is_value(at::ScalarType t) { return t == at::kFloat || t == at::kBFloat16 || t == at::kHalf; }
+bool is_id(const Tensor& t) { return t.scalar_type() == at::kLong || t.scalar_type() == at::kInt; }
+// A contiguous tensor of these sizes, on the GPU of `first`.
+bool is_whole(const Tensor& t, at::IntArrayRef sizes, const Tensor& first) {
+  return t.sizes() == sizes && t.is_contiguous() && t.is_cuda() && t.device() == first.device();
+}
+bool is_codes(const Tensor& q, const Tensor& scale, const Tensor& first) {
+  return q.dim() == 2 && q.size(1) > 0 && q.size(1) % 16 == 0 && q.scalar_type() == at::kByte &&
+         is_whole(q, q.sizes(), first) && scale.scalar_type() == at::kByte &&
+         is_whole(scale, {q.size(0), q.size(1) / 16}, first);
+}
+void expect(bool taken, const char* where) {
+  TORCH_CHECK(taken, where, ": a tensor of a type, size, layout or device that this call does not take");
 }
 
 int32_t type_of(const Tensor& t) {
@@ -135,8 +152,17 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
   }
 };
 
+bool is_param(const std::optional<Tensor>& t, const Tensor& x) {
+  return !t || !t->defined() ||
+         ((t->scalar_type() == x.scalar_type() || t->scalar_type() == at::kFloat) && is_whole(*t, {x.size(1)}, x));
+}
+
 Tensor layer_norm(const Tensor& x, const std::optional<Tensor>& weight, const std::optional<Tensor>& bias, double eps,
                   int64_t workspace) {
+  const bool both = weight && weight->defined() && bias && bias->defined();
+  expect(x.dim() == 2 && x.size(1) > 0 && is_value(x.scalar_type()) && x.is_cuda() && rows_apart(x) &&
+             is_param(weight, x) && is_param(bias, x) && (!both || weight->scalar_type() == bias->scalar_type()),
+         "layer_norm");
   const auto recorded = [](const std::optional<Tensor>& t) { return t && t->defined() && t->requires_grad(); };
   if (at::GradMode::is_enabled() && (x.requires_grad() || recorded(weight) || recorded(bias)))
     return LayerNorm::apply(x, weight, bias, eps, workspace);
@@ -194,6 +220,9 @@ struct Embedding : torch::autograd::Function<Embedding> {
 };
 
 Tensor embedding(const Tensor& ids, const Tensor& weight, double scale, int64_t ignore_index, int64_t workspace) {
+  expect(ids.dim() == 1 && is_id(ids) && is_whole(ids, ids.sizes(), weight) && weight.dim() == 2 && weight.size(0) > 0 &&
+             weight.size(1) > 0 && is_value(weight.scalar_type()) && is_whole(weight, weight.sizes(), weight),
+         "embedding");
   if (at::GradMode::is_enabled() && weight.requires_grad())
     return Embedding::apply(weight, ids, scale, ignore_index, workspace);
   return embedding_forward(ids, weight, scale, ignore_index);
@@ -202,6 +231,8 @@ Tensor embedding(const Tensor& ids, const Tensor& weight, double scale, int64_t 
 // ----------------------------------------------------------------------------- MXFP4
 
 std::tuple<Tensor, Tensor> quantize_mxfp4(const Tensor& x) {
+  expect(x.dim() == 2 && x.size(1) > 0 && x.size(1) % 32 == 0 && is_value(x.scalar_type()) && is_whole(x, x.sizes(), x),
+         "quantize_mxfp4");
   const Guard guard(x.device());
   const int64_t rows = x.size(0), cols = x.size(1);
   const auto bytes = x.options().dtype(at::kByte).requires_grad(false);
@@ -211,6 +242,7 @@ std::tuple<Tensor, Tensor> quantize_mxfp4(const Tensor& x) {
 }
 
 Tensor dequantize_mxfp4(const Tensor& q, const Tensor& scale, at::ScalarType dtype) {
+  expect(is_codes(q, scale, q) && is_value(dtype), "dequantize_mxfp4");
   const Guard guard(q.device());
   const int64_t rows = q.size(0), cols = 2 * q.size(1);
   const Tensor x = at::empty({rows, cols}, q.options().dtype(dtype));
@@ -223,6 +255,13 @@ std::tuple<Tensor, Tensor> logprobs_mxfp4(const Tensor& hidden, const std::optio
                                           const Tensor& weight, const Tensor& weight_scale,
                                           const std::optional<Tensor>& bias, const Tensor& targets, double logit_scale,
                                           double softcap, int64_t ignore_index, int64_t workspace, bool want_entropy) {
+  expect(is_codes(weight, weight_scale, hidden) && hidden.dim() == 2 &&
+             (hidden_scale ? is_codes(hidden, *hidden_scale, hidden) && hidden.size(1) == weight.size(1)
+                           : is_value(hidden.scalar_type()) &&
+                                 is_whole(hidden, {hidden.size(0), 2 * weight.size(1)}, hidden)) &&
+             is_id(targets) && is_whole(targets, {hidden.size(0)}, hidden) &&
+             (!bias || (bias->scalar_type() == at::kFloat && is_whole(*bias, {weight.size(0)}, hidden))),
+         "token_logprobs_mxfp4");
   const Guard guard(hidden.device());
   const int64_t n = hidden.size(0);
   flce_params p{};

@@ -46,3 +46,21 @@ def test_embedding_and_layer_norm(flce_lib):
     traced = _trace(fn, (ids,))
     assert torch.equal(traced(ids.flip(0)), fn(ids.flip(0)))
     assert torch.equal(traced(ids[:7]), fn(ids[:7]))               # fewer rows of the recorded types are no other call
+
+
+def test_other_sizes_than_the_recorded_ones(flce_lib):
+    """Where the recorded graph's constants do not fit, the call is refused, not made."""
+    import torch
+    gain, ids = torch.ones(64, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    norm = _trace(lambda x: flce_lib.layer_norm(x, gain), (torch.randn(4, 64, device="cuda"),))
+    for x in (torch.randn(4, 128, device="cuda"), torch.randn(4, 32, device="cuda"), torch.randn(4, 64, device="cuda").double()):
+        with pytest.raises(RuntimeError, match="type, size, layout or device"):
+            norm(x)
+    q, s = flce_lib.quantize_mxfp4(torch.randn(30, 64, device="cuda"))
+    scores = _trace(lambda x: flce_lib.token_logprobs_mxfp4(x, q, s, ids), (torch.randn(4, 64, device="cuda"),))
+    for shape in ((4, 128), (5, 64), (3, 64)):
+        with pytest.raises(RuntimeError, match="type, size, layout or device"):
+            scores(torch.randn(*shape, device="cuda"))
+    lookup = _trace(lambda w: flce_lib.embedding(ids, w), (torch.randn(10, 64, device="cuda"),))
+    w = torch.randn(7, 40, device="cuda")
+    assert torch.equal(lookup(w), w[ids])                          # a table of any size fits
