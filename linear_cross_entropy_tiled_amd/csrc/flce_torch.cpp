@@ -139,9 +139,10 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
     flce_norm_params p = norm_params(x, w, b, ctx->saved_data["eps"].toDouble());
     p.ld_grad = row_stride(dy);
     Tensor dx, dw, db, workspace;
-    if (x.requires_grad()) dx = at::empty({p.rows, p.cols}, x.options());
-    if (w.defined() && w.requires_grad()) dw = at::empty({p.cols}, w.options());
-    if (b.defined() && b.requires_grad()) db = at::empty({p.cols}, b.options());
+    // the gradients that this backward was asked for; inputs are counted without absent ones
+    if (ctx->needs_input_grad(0)) dx = at::empty({p.rows, p.cols}, x.options());
+    if (w.defined() && ctx->needs_input_grad(1)) dw = at::empty({p.cols}, w.options());
+    if (b.defined() && ctx->needs_input_grad(w.defined() ? 2 : 1)) db = at::empty({p.cols}, b.options());
     const int64_t bytes = dw.defined() || db.defined() ? ctx->saved_data["workspace"].toInt() : 0;
     if (bytes > 0) workspace = at::empty({bytes}, x.options().dtype(at::kByte));
     const float* mean = stats.data_ptr<float>();
