@@ -28,6 +28,7 @@ There is no fallback: if the library is missing, ``load()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -595,6 +596,28 @@ def status_string(code: int) -> str:
 
 # ----------------------------------------------------------------------------- torch conveniences
 
+_tracing = None   # torch.compiler.is_dynamo_compiling, kept: looking it up takes longer than calling it
+
+
+def _find_tracing():
+    global _tracing
+    import torch
+    _tracing = torch.compiler.is_dynamo_compiling
+    return _tracing
+
+
+def between_graphs(f):
+    """f for callers under torch.compile, whose tracer cannot follow pointers and structs into the C entry points (it
+    raised, or made the call with values of its own): f runs as it is, between the compiled pieces."""
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        if (_tracing or _find_tracing())():
+            import torch
+            return torch.compiler.disable(f)(*args, **kwargs)
+        return f(*args, **kwargs)
+    return call
+
+
 def make_params(n_tokens: int, hidden: int, vocab: int, *, dtype: str = "bf16",
                 grad_weight_dtype: Optional[str] = None, logit_scale: float = 1.0,
                 softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
@@ -718,6 +741,7 @@ def _validate(hidden, weight, targets, bias=None, *, reduction="mean", lse=None,
     return dt
 
 
+@between_graphs
 def forward(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0,
             softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
             reduction: str = "mean", return_metrics: bool = False, workspace=None):
@@ -747,6 +771,7 @@ def forward(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0,
     return loss, lse, metrics
 
 
+@between_graphs
 def backward(hidden, weight, targets, lse, grad_loss, bias=None, *, logit_scale: float = 1.0,
              softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
              reduction: str = "mean", grad_weight_dtype: Optional[str] = None, workspace=None,
@@ -784,6 +809,7 @@ def backward(hidden, weight, targets, lse, grad_loss, bias=None, *, logit_scale:
     return gh, gw, gb
 
 
+@between_graphs
 def forward_backward(hidden, weight, targets, grad_loss, bias=None, *, logit_scale: float = 1.0,
                      softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
                      reduction: str = "mean", grad_weight_dtype: Optional[str] = None, return_metrics: bool = False,
@@ -828,6 +854,7 @@ def forward_backward(hidden, weight, targets, grad_loss, bias=None, *, logit_sca
     return loss, lse, metrics, gh, gw, gb
 
 
+@between_graphs
 def linear_cross_entropy(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0,
                          softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
                          reduction: str = "mean", one_pass: bool = False):
@@ -888,6 +915,7 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, *, logit_scale: flo
     return _Fn.apply(hidden, weight, bias)
 
 
+@between_graphs
 def get_status(workspace) -> int:
     return flce_get_status(_ptr(workspace), _stream_handle(workspace.device))
 
@@ -948,6 +976,7 @@ def _run_chunked(inputs, weight, fn, user, *, chunk_rows, grad_weight_dtype, gra
     return loss.reshape(()), gi, gw
 
 
+@between_graphs
 def chunked_linear_loss(inputs, weight, loss_and_grad_fn, *args, chunk_rows: int = 0,
                         grad_weight_dtype: Optional[str] = None, grad_weight_accum_dtype: str = "fp32",
                         grad_weight=None, workspace=None, **kwargs):
@@ -1002,6 +1031,7 @@ def chunked_linear_loss(inputs, weight, loss_and_grad_fn, *args, chunk_rows: int
     return ws_holder["loss"].reshape(()), gi, gw
 
 
+@between_graphs
 def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_rows: int = 0,
                  grad_weight_dtype: Optional[str] = None, grad_weight_accum_dtype: str = "fp32",
                  grad_weight=None, workspace=None):

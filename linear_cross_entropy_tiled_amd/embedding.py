@@ -6,8 +6,8 @@ import functools
 import math
 from typing import Optional
 
-from . import (DTYPES, FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32, _dtype_name, _ptr, flce_embedding_backward,
-               flce_embedding_params, flce_embedding_workspace_size, torch_ops)
+from . import (DTYPES, FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32, _dtype_name, _ptr, between_graphs,
+               flce_embedding_backward, flce_embedding_params, flce_embedding_workspace_size, torch_ops)
 from .logprobs import has_tangent, on_device, raise_for, stream_handle
 
 
@@ -61,6 +61,7 @@ def _op():
     return torch_ops()._embedding.default
 
 
+@between_graphs
 def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100):
     """Rows ``scale * weight[ids]`` (N, H) in weight's dtype (fp32, bf16, fp16), differentiable in weight (V, H).
 
@@ -79,6 +80,7 @@ def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100):
     return _op()(ids, weight, float(scale), int(ignore_index), workspace)
 
 
+@between_graphs
 def embedding_backward(grad, ids, vocab: int, *, scale: float = 1.0, ignore_index: int = -100,
                        grad_weight_dtype: Optional[str] = None, grad_weight=None):
     """The gradient (vocab, H) of ``embedding``'s weight from that of its output, grad (N, H), summed in fp32.

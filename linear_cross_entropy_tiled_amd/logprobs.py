@@ -7,7 +7,7 @@ import functools
 from typing import Optional
 
 from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError, _dtype_name, _ptr, _stream_handle,
-               _targets_int32, _validate, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_int8,
+               _targets_int32, _validate, between_graphs, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_int8,
                flce_logprobs_int8_workspace_size, flce_logprobs_mxfp4_workspace_size, flce_logprobs_workspace_size,
                flce_quantize_int8, make_params, torch_ops)
 
@@ -123,6 +123,7 @@ def _function():
     return TokenLogprobs
 
 
+@between_graphs
 def token_logprobs(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0, softcap: Optional[float] = None,
                    ignore_index: int = -100, return_entropy: bool = False, vocab_chunk: int = 0):
     """Log-probabilities (N,) of ``targets`` under softmax(softcap(logit_scale (hidden @ weight.T + bias))),
@@ -155,6 +156,7 @@ def _quantize(x):
     return q, scale
 
 
+@between_graphs
 def quantize_int8(x):
     """Rows of x (R, H) as 8-bit integers: (q int8 (R, H), scale fp32 (R,)), x ~ scale[:, None] * q, with
     scale = max|row| / 127.  For a weight (V, H) once, when a scorer is loaded.  H must be a multiple of 16.
@@ -218,6 +220,7 @@ def _aligned16(t):
     return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
 
 
+@between_graphs
 def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
                         logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
                         return_entropy: bool = False):
@@ -251,6 +254,7 @@ def _mx_ops():
     return ops._quantize_mxfp4.default, ops._dequantize_mxfp4.default, ops._logprobs_mxfp4.default
 
 
+@between_graphs
 def quantize_mxfp4(x):
     """Rows of x (R, H) in MXFP4: (codes uint8 (R, H / 2), two to a byte, the earlier one in the low half; scales uint8
     (R, H / 32), byte s for 2^(s - 127)).  For a weight (V, H) once, when a scorer is loaded.  H must be a multiple of
@@ -281,6 +285,7 @@ def _check_mx(name, q, scale):
         raise ValueError(f"{name}_scale must have shape {(rows, cols // 16)}, got {tuple(scale.shape)}")
 
 
+@between_graphs
 def dequantize_mxfp4(q, scale, dtype=None):
     """The values (R, H) that ``quantize_mxfp4``'s codes and scales stand for, in ``dtype`` (float32, the default,
     bfloat16 or float16; rounded where it does not hold them)."""
@@ -306,6 +311,7 @@ def _mx_workspace(n, h, v, dtype, logit_scale, softcap, ignore_index, targets_in
                     reduction="none", targets_int32=targets_int32))
 
 
+@between_graphs
 def token_logprobs_mxfp4(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
                          logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
                          return_entropy: bool = False):

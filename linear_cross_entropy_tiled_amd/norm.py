@@ -5,7 +5,7 @@ from __future__ import annotations
 import functools
 import math
 
-from . import DTYPES, _dtype_name, flce_layer_norm_workspace_size, flce_norm_params, torch_ops
+from . import DTYPES, _dtype_name, between_graphs, flce_layer_norm_workspace_size, flce_norm_params, torch_ops
 from .logprobs import has_tangent
 
 
@@ -69,6 +69,7 @@ def _op():
     return torch_ops()._layer_norm.default
 
 
+@between_graphs
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     """Layer norm of the rows of x (N, H): weight (x - mean) / sqrt(var + eps) + bias, in x's dtype (fp32, bf16,
     fp16), formed in fp32.  Differentiable in x, weight and bias.
