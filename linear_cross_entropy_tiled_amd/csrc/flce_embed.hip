@@ -8,8 +8,9 @@
 // that reaches over a chunk's edge is left in fp32 and a second kernel adds the parts.
 //
 // What bounds it is memory, and of the whole gradient mostly its zeros.  N = 8192, H = 4096,
-// V = 128256, bf16, Zipf's ids: forward 24 us; zeros and sort 163 us (1.05 GB at 6.4 TB/s,
-// where a plain fill reaches 6.9), runs 36, joins 10.
+// V = 128256, bf16, Zipf's ids: forward 29 us in a training step (22 to 31; its 112 MB at 3.9
+// TB/s), zeros and sort 165 us (1.05 GB at 6.4 TB/s, where a plain fill reaches 6.9), runs 36,
+// joins 10.
 #include "flce_device.h"
 #include "flce_embed.h"
 

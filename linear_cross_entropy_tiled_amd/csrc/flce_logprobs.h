@@ -50,7 +50,7 @@ struct LpTileArgs {
   const uint8_t* hidden_mx;   // MXFP4: scale bytes, rows of ld_hmx (a multiple of 4)
   const uint8_t* weight_mx;
   uint32_t ld_hmx, ld_wmx;
-  const uint8_t* hidden_tmx;  // the same in the large tiles' order (launch_tile_scales)
+  const uint8_t* hidden_tmx;  // the same in the large tiles' order (launch_mx_prep)
   const uint8_t* weight_tmx;
   const void* targets;
   int tgt_i32;

@@ -25,7 +25,7 @@ hipError_t launch_dequantize_mx(int dtype, const uint8_t* q, const uint8_t* scal
 // Scale rows of `cols` bytes to rows of `ld` bytes, a multiple of 4.
 hipError_t launch_pad_scales(const uint8_t* scale, int64_t rows, int cols, int ld, uint8_t* out, hipStream_t st);
 // Scales (rows of ld bytes, a multiple of 4; 0 past the last row and block) in the order of the large tiles, which
-// take three words a lane and stage from LDS for all their matrix instructions' scales (one byte a fragment out of
+// take six words a lane and stage from LDS for all their matrix instructions' scales (one byte a fragment out of
 // rows as they are stored would be 24 reads).  A stage is 256 values, 8 blocks, four sub-steps s of 2; lane l holds
 // row l % 32 and block 2 s + l / 32.  Of a tile of 256 rows and a stage, kMxStage bytes:
 //  a (the weight):        for each 128 rows and lane four words, by s; byte m is row 32 m + l % 32;

@@ -6,7 +6,7 @@
 //  - v_mfma_scale_f32_32x32x64_f8f6f4.  An instruction that carries scales takes twice the
 //    issue slots of one without; the 32 x 32 form does the work of two 16 x 16 ones, and its
 //    fragments are 24 registers a sub-step instead of 36.
-//  - The scales come through LDS in the order of launch_tile_scales, 24 bytes a lane and
+//  - The scales come through LDS in the order of launch_mx_prep, 24 bytes a lane and
 //    stage.
 //  - A workgroup's vocabulary tiles are one run of stages: 16 stages at H = 4096 are so
 //    short that the loads of a tile's first two, if nothing else ran, would be a tenth of it.

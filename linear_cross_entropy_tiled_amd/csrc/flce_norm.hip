@@ -8,10 +8,11 @@
 // Everything is formed in fp32 and rounded once to the output's type.  The variance is the
 // mean of the squared distances from the mean, not a difference of two large numbers.
 //
-// What bounds it is memory.  Rows of up to 16384 values stay in registers between the
-// passes over them: 8 or 16 columns a thread, 64 to 1024 threads a row, and a workgroup
-// takes row after row with the weight (backward: and the column sums) in registers too,
-// loading the next row while it works on one.  Every value is read once and written once.
+// What bounds it is memory.  Rows of up to 16384 values are held between the passes over
+// them: 8 or 16 columns a thread, 64 to 1024 threads a row, and a workgroup takes row after
+// row with the weight (backward: and the column sums) held too, loading the next row while
+// it works on one.  Every value is read once and written once.  All of it is in registers,
+// but for the backward of 8193 to 16384 columns (norm_bwd_kernel has its figures).
 // N = 8192, H = 4096, bf16, fp32 parameters, where a large copy reaches 4.7 TB/s: forward
 // 33 us (4.1 TB/s), backward 43 us and 5 for the parts (4.7); with 16 columns to each of 256
 // threads 52, 49 and 9, as one workgroup a row with its passes from cache 196 in all.
@@ -308,6 +309,14 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_fwd_kernel(NormArgs a) {
 // Workgroup g takes the row groups g, g + gridDim.x, ...; its column sums are part g.  512
 // workgroups at most (256 of 1024 threads): each part is 8 bytes a column to write and to
 // read, an eighth of the traffic at N = 8192.
+// Of 8193 to 16384 columns a thread's 16 need more than the 128 registers that 1024 threads
+// leave it: the weight and two column sums are 48, a row ahead of two inputs and the row in
+// work 32 in 16 bits, 64 in fp32.  It spills 12 of them (16 bits, rows of whole 16 bytes; 88
+// of other rows) and 72 (fp32; 81), some of which go to scratch memory and back for each row.
+// 4096 rows, fp32 parameters, us here | by the kernels for any length: bf16 8200 columns 80 |
+// 85, 12288 98 | 112, 16384 116 | 152, 12287 160 | 168; fp32 8200 236 | 144, 12288 262 | 224,
+// 16384 297 | 306, 12287 256 | 246.  (So fp32 rows of up to some 14000 columns would be better
+// off there.)
 template <typename T, int VEC, int CPT, int TPR, int ROWS>
 __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormArgs a) {
   typedef RowPart<T, VEC, CPT, TPR> Part;
@@ -401,7 +410,7 @@ static constexpr int rows_at_once(int tpr) { return tpr >= 512 ? 1 : 512 / tpr; 
 
 int norm_parts(int64_t rows, int64_t cols) {
   if (cols > kRegisterCols) {
-    const int64_t n = (rows + 31) / 32;   // 8 rows to a thread at least
+    const int64_t n = (rows + 31) / 32;   // up to 8192 rows at most 8 rows to a thread, beyond more
     return (int)(n < 1 ? 1 : (n > 256 ? 256 : n));
   }
   const int tpr = threads_per_row(cols), most = tpr == 1024 ? 256 : 512;
