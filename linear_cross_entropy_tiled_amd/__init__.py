@@ -596,17 +596,18 @@ def status_string(code: int) -> str:
 
 # ----------------------------------------------------------------------------- torch conveniences
 
-_tracing = None   # torch.compiler.is_dynamo_compiling, kept: looking it up takes longer than calling it
+_tracing = _recording = None   # torch.compiler.is_dynamo_compiling and torch.jit.is_tracing, kept: looked up once
 
 
 def _find_tracing():
-    global _tracing
+    global _tracing, _recording
     import torch
+    _recording = torch.jit.is_tracing
     _tracing = torch.compiler.is_dynamo_compiling
     return _tracing
 
 
-def between_graphs(f):
+def between_graphs(f, recorded: bool = True):
     """f for callers under torch.compile, whose tracer cannot follow pointers and structs into the C entry points (it
     raised, or made the call with values of its own): f runs as it is, between the compiled pieces."""
     @functools.wraps(f)
@@ -614,8 +615,17 @@ def between_graphs(f):
         if (_tracing or _find_tracing())():
             import torch
             return torch.compiler.disable(f)(*args, **kwargs)
+        if not recorded and _recording():
+            raise RuntimeError(f"{f.__name__} cannot be recorded by torch.jit.trace: a replay would return memory that "
+                               "nothing has written")
         return f(*args, **kwargs)
     return call
+
+
+def by_pointers(f):
+    """between_graphs of a function that is no operator of PyTorch's: torch.jit.trace would record the outputs' allocation
+    and not the call that fills them, or the call with the recorded sizes."""
+    return between_graphs(f, recorded=False)
 
 
 def make_params(n_tokens: int, hidden: int, vocab: int, *, dtype: str = "bf16",
@@ -741,7 +751,7 @@ def _validate(hidden, weight, targets, bias=None, *, reduction="mean", lse=None,
     return dt
 
 
-@between_graphs
+@by_pointers
 def forward(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0,
             softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
             reduction: str = "mean", return_metrics: bool = False, workspace=None):
@@ -771,7 +781,7 @@ def forward(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0,
     return loss, lse, metrics
 
 
-@between_graphs
+@by_pointers
 def backward(hidden, weight, targets, lse, grad_loss, bias=None, *, logit_scale: float = 1.0,
              softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
              reduction: str = "mean", grad_weight_dtype: Optional[str] = None, workspace=None,
@@ -809,7 +819,7 @@ def backward(hidden, weight, targets, lse, grad_loss, bias=None, *, logit_scale:
     return gh, gw, gb
 
 
-@between_graphs
+@by_pointers
 def forward_backward(hidden, weight, targets, grad_loss, bias=None, *, logit_scale: float = 1.0,
                      softcap: Optional[float] = None, z_loss: float = 0.0, ignore_index: int = -100,
                      reduction: str = "mean", grad_weight_dtype: Optional[str] = None, return_metrics: bool = False,
@@ -875,11 +885,12 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, *, logit_scale: flo
             raise ValueError('one_pass needs reduction "sum" or "mean": the per-row upstream gradient of '
                              '"none" must be known before the pass (use forward_backward)')
 
+        # (torch.jit.trace records autograd's functions as themselves: the calls in them are made again in a replay)
         class _OnePass(torch.autograd.Function):
             @staticmethod
             def forward(ctx, x, w, b):
                 one = torch.ones(1, dtype=torch.float32, device=x.device)
-                loss, _, _, gh, gw, gb = forward_backward(x, w, targets, one, b, **opts)
+                loss, _, _, gh, gw, gb = forward_backward.__wrapped__(x, w, targets, one, b, **opts)
                 p = make_params(x.shape[0], x.shape[1], w.shape[0], dtype=_dtype_name(x), **opts)
                 ctx.state = [p, gh, gw, gb]
                 return loss
@@ -901,7 +912,7 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, *, logit_scale: flo
     class _Fn(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, w, b):
-            loss, lse, _ = forward(x, w, targets, b, **opts)
+            loss, lse, _ = forward.__wrapped__(x, w, targets, b, **opts)
             ctx.save_for_backward(x, w, b, lse)
             return loss
 
@@ -909,13 +920,13 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, *, logit_scale: flo
         def backward(ctx, g):
             x, w, b, lse = ctx.saved_tensors
             g = g.detach().to(torch.float32).contiguous().reshape(-1)
-            gh, gw, gb = backward(x, w, targets, lse, g, b, **opts)   # gradients in the inputs' dtypes
+            gh, gw, gb = backward.__wrapped__(x, w, targets, lse, g, b, **opts)   # gradients in the inputs' dtypes
             return gh, gw, gb
 
     return _Fn.apply(hidden, weight, bias)
 
 
-@between_graphs
+@by_pointers
 def get_status(workspace) -> int:
     return flce_get_status(_ptr(workspace), _stream_handle(workspace.device))
 
@@ -976,7 +987,7 @@ def _run_chunked(inputs, weight, fn, user, *, chunk_rows, grad_weight_dtype, gra
     return loss.reshape(()), gi, gw
 
 
-@between_graphs
+@by_pointers
 def chunked_linear_loss(inputs, weight, loss_and_grad_fn, *args, chunk_rows: int = 0,
                         grad_weight_dtype: Optional[str] = None, grad_weight_accum_dtype: str = "fp32",
                         grad_weight=None, workspace=None, **kwargs):
@@ -1031,7 +1042,7 @@ def chunked_linear_loss(inputs, weight, loss_and_grad_fn, *args, chunk_rows: int
     return ws_holder["loss"].reshape(()), gi, gw
 
 
-@between_graphs
+@by_pointers
 def weighted_mse(inputs, weight, target, row_weight, feature_weight, *, chunk_rows: int = 0,
                  grad_weight_dtype: Optional[str] = None, grad_weight_accum_dtype: str = "fp32",
                  grad_weight=None, workspace=None):

@@ -15,7 +15,7 @@ import functools
 import math
 from typing import Optional
 
-from . import (DTYPES, REDUCTIONS, _dtype_name, _ptr, between_graphs, flce_policy_backward,
+from . import (DTYPES, REDUCTIONS, _dtype_name, _ptr, by_pointers, flce_policy_backward,
                flce_policy_forward, flce_policy_params, flce_policy_workspace_size, flce_preference_backward,
                flce_preference_forward, flce_preference_params, flce_preference_workspace_size, flce_token_view)
 from .logprobs import differentiable, first_order, on_device, raise_for, stream_handle, upstream
@@ -146,7 +146,7 @@ def _preference_function():
     return PreferenceLoss
 
 
-@between_graphs
+@by_pointers
 def preference_loss(logps, ref_logps=None, *, offsets=None, mask=None, beta: float = 0.1, loss_type: str = "sigmoid",
                     label_smoothing: float = 0.0, margin: float = 0.0, length_normalize: bool = False,
                     reduction: str = "mean", return_metrics: bool = False):
@@ -240,7 +240,7 @@ def _policy_function():
     return PolicyLoss
 
 
-@between_graphs
+@by_pointers
 def policy_loss(logps, old_logps, advantages, *, ref_logps=None, entropy=None, offsets=None, mask=None,
                 clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: Optional[float] = None,
                 kl_coef: float = 0.0, entropy_coef: float = 0.0, reduction: str = "mean",

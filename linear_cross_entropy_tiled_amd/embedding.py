@@ -6,7 +6,7 @@ import functools
 import math
 from typing import Optional
 
-from . import (DTYPES, FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32, _dtype_name, _ptr, between_graphs,
+from . import (DTYPES, FLCE_ACCUMULATE_GRAD_WEIGHT, FLCE_TARGETS_INT32, _dtype_name, _ptr, between_graphs, by_pointers,
                flce_embedding_backward, flce_embedding_params, flce_embedding_workspace_size, torch_ops)
 from .logprobs import has_tangent, on_device, raise_for, stream_handle
 
@@ -80,7 +80,7 @@ def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100):
     return _op()(ids, weight, float(scale), int(ignore_index), workspace)
 
 
-@between_graphs
+@by_pointers
 def embedding_backward(grad, ids, vocab: int, *, scale: float = 1.0, ignore_index: int = -100,
                        grad_weight_dtype: Optional[str] = None, grad_weight=None):
     """The gradient (vocab, H) of ``embedding``'s weight from that of its output, grad (N, H), summed in fp32.

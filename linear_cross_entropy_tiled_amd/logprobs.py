@@ -7,9 +7,10 @@ import functools
 from typing import Optional
 
 from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError, _dtype_name, _ptr, _stream_handle,
-               _targets_int32, _validate, between_graphs, flce_logprobs_backward, flce_logprobs_forward, flce_logprobs_int8,
-               flce_logprobs_int8_workspace_size, flce_logprobs_mxfp4_workspace_size, flce_logprobs_workspace_size,
-               flce_quantize_int8, make_params, torch_ops)
+               _targets_int32, _validate, between_graphs, by_pointers, flce_logprobs_backward, flce_logprobs_forward,
+               flce_logprobs_int8, flce_logprobs_int8_workspace_size, flce_logprobs_mxfp4_workspace_size,
+               flce_logprobs_workspace_size, flce_quantize_int8, make_params, torch_ops)
+
 
 
 _SAME_DEVICE = contextlib.nullcontext()
@@ -123,7 +124,7 @@ def _function():
     return TokenLogprobs
 
 
-@between_graphs
+@by_pointers
 def token_logprobs(hidden, weight, targets, bias=None, *, logit_scale: float = 1.0, softcap: Optional[float] = None,
                    ignore_index: int = -100, return_entropy: bool = False, vocab_chunk: int = 0):
     """Log-probabilities (N,) of ``targets`` under softmax(softcap(logit_scale (hidden @ weight.T + bias))),
@@ -156,7 +157,7 @@ def _quantize(x):
     return q, scale
 
 
-@between_graphs
+@by_pointers
 def quantize_int8(x):
     """Rows of x (R, H) as 8-bit integers: (q int8 (R, H), scale fp32 (R,)), x ~ scale[:, None] * q, with
     scale = max|row| / 127.  For a weight (V, H) once, when a scorer is loaded.  H must be a multiple of 16.
@@ -220,7 +221,7 @@ def _aligned16(t):
     return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
 
 
-@between_graphs
+@by_pointers
 def token_logprobs_int8(hidden, weight, weight_scale, targets, bias=None, *, hidden_scale=None,
                         logit_scale: float = 1.0, softcap: Optional[float] = None, ignore_index: int = -100,
                         return_entropy: bool = False):
