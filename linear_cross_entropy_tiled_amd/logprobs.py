@@ -12,7 +12,6 @@ from . import (DTYPES, FLCE_OK, FLCE_PASS_BACKWARD, FLCE_PASS_FORWARD, FlceError
                flce_logprobs_workspace_size, flce_quantize_int8, make_params, torch_ops)
 
 
-
 _SAME_DEVICE = contextlib.nullcontext()
 
 
